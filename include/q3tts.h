@@ -298,6 +298,38 @@ int q3tts_sample_logits_noalloc(int n, int vocab, const float* logits, int talke
                                 const uint8_t* seen, const int32_t* sel_index, int step, const int32_t* noise_row,
                                 int eos_id, int suppress_lo, int suppress_hi, int32_t* ids_out, void* stream);
 
+/* Draws from logits with given uniform numbers, for vocabularies past the
+ * codec's (a text vocabulary) and for callers that keep everything on the
+ * device: nothing is synchronised, so the call can be captured into a graph.
+ * Row i, with l = logits / temperature (one fp32 division):
+ *   top-k   keeps every l >= the k-th largest (ties kept);
+ *   weights W = floor(2^40 e), e = exp(l - max l) in the fp32 arithmetic of the
+ *           other draws;
+ *   top-p   in the order (l descending, id ascending) keeps an id when the
+ *           weight before it is < top_p times the weight of all that top-k kept;
+ *   min-p   keeps e >= min_p;
+ *   the draw is the first kept id, by id, at which the running kept weight
+ *           exceeds floor(u * kept weight) (at most kept weight - 1).
+ * The id of the largest l (the lowest one on ties) is always kept.  Sums are
+ * whole numbers, so the result does not depend on their order.
+ *   n, vocab        rows (0..65535), entries of a row (1..262144)
+ *   logits          [n][vocab] f32 or bf16 (dtype), row stride logits_stride
+ *                   elements (0: packed); -inf: never drawn
+ *   u               [n] f32 in [0, 1)
+ *   temperature     [n] f32: > 0, or 0: the largest l (the lowest id on ties)
+ *   top_k           [n] <= 0: off
+ *   top_p           [n] >= 1: off; min_p [n] <= 0: off
+ *   ids_out         [n]; -1 where the logits hold NaN, +inf or nothing finite,
+ *                   or the temperature is negative or NaN
+ *   logprob_out     [n] f32 or NULL: log of the drawn id's share of the kept
+ *                   weight (0 for temperature 0, NaN where the id is -1)
+ *   err             or NULL: bit 1 (value 1) is set where an id is -1
+ * All arrays are device memory.  Errors: Q3_ERR_ARG, Q3_ERR_CUDA
+ * (q3paged_last_error() of q3paged.h has the reason). */
+int q3tts_sample_given(int n, int vocab, const void* logits, int dtype, int64_t logits_stride, const float* u,
+                       const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                       int32_t* ids_out, float* logprob_out, int32_t* err, void* stream);
+
 /* Number of kernel launches one talker step of the current batch makes (the
  * kernel nodes of the step's CUDA graph, which this call records if needed).
  * Errors: Q3_ERR_STATE (no prefill), Q3_ERR_CUDA. */

@@ -23,7 +23,7 @@ PATH_NAMES = {Q3_PATH_GRAPH: "graph", Q3_PATH_FRAME: "frame", Q3_PATH_CLUSTER: "
 
 EXPORTS = ("q3tts_workspace_bytes", "q3tts_create", "q3tts_prefill", "q3tts_step_frames", "q3tts_set_capture",
            "q3tts_sample_logits", "q3tts_sample_logits_noalloc", "q3tts_step_kernel_count", "q3tts_step_path",
-           "q3tts_text_embed", "q3tts_last_error", "q3tts_destroy")
+           "q3tts_text_embed", "q3tts_sample_given", "q3tts_last_error", "q3tts_destroy")
 
 
 class Q3Error(RuntimeError):
@@ -91,6 +91,14 @@ def lib():
         L.q3tts_step_path.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_int)]
         L.q3tts_text_embed.argtypes = [vp, i32, vp, vp]
         L.q3tts_sample_logits_noalloc.argtypes = [i32, i32, vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp]
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        L.q3tts_sample_given.argtypes = [i32, i32, vp, i32, i64] + [vp] * 9
+        L.q3paged_append.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, f32, vp, i32, vp, i64, vp, vp]
+        L.q3paged_workspace_bytes.restype = ctypes.c_size_t
+        L.q3paged_workspace_bytes.argtypes = [vp]
+        L.q3paged_attention.argtypes = [vp, i32, i32, vp, i64, vp, vp, f32, vp, i64, vp, ctypes.c_size_t, vp, vp]
+        L.q3paged_last_error.restype = ctypes.c_char_p
+        L.q3paged_last_error.argtypes = []
         L.q3tts_last_error.restype = ctypes.c_char_p
         L.q3tts_last_error.argtypes = [vp]
         L.q3tts_destroy.argtypes = [vp]
@@ -498,3 +506,206 @@ class Q3Codec:
 
     def kernel_count(self) -> int:
         return _codec_lib().q3codec_window_kernel_count(self.h)
+
+
+# ---------------------------------------------------------------- paged cache (q3paged.h)
+PAGED_EXPORTS = ("q3paged_append", "q3paged_workspace_bytes", "q3paged_attention", "q3paged_last_error")
+Q3PAGED_ERR_BOUNDS, Q3PAGED_ERR_TIMEOUT = 2, 4
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_q_heads", "n_kv_heads", "head_dim", "act_dtype", "kv_dtype",
+                                            "page_size", "n_pages", "n_seqs", "max_pages")] + \
+              [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")] + \
+              [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "page_table")]
+
+
+def _paged_raise(rc):
+    raise Q3Error(rc, lib().q3paged_last_error().decode())
+
+
+def _dtype_code(t):
+    import torch
+    code = {torch.float32: Q3_F32, torch.bfloat16: Q3_BF16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"float32 or bfloat16 expected, not {t.dtype}")
+    return code
+
+
+class _on_device:
+    """The tensors' device made current for a call (nothing to do where it is already)."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        import torch
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        import torch
+        if self.prev != self.index:
+            torch.cuda.set_device(self.prev)
+
+
+def _need(t, name, dtype, shape, device):
+    """A contiguous CUDA tensor of this type, shape and device (the kernels read it by its address)."""
+    if not (t.is_cuda and t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous() and t.device == device):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on {device} is expected")
+    return t.data_ptr()
+
+
+class PagedKV:
+    """A paged key / value cache over tensors that the caller owns (q3paged.h).
+
+    k_pages, v_pages: CUDA tensors [n_pages, n_kv_heads, page_size, 128], float32 or bfloat16, of the same
+    strides (a permuted view of [n_pages, page_size, n_kv_heads, 128] serves as well); page_table: int32
+    [n_seqs, max_pages].  The tensors may be written between calls (the table as sequences grow); their
+    addresses are taken once, here.  Work is queued on the current stream; calls on different streams have
+    a workspace each, and a call that is being captured gets one of its graph's own."""
+
+    def __init__(self, k_pages, v_pages, page_table, n_q_heads: int):
+        import torch
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.shape[3] == 128 and
+                    t.stride(3) == 1):
+                raise ValueError(f"{name}: a CUDA tensor [n_pages, n_kv_heads, page_size, 128] with contiguous rows "
+                                 "is expected")
+        if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
+                or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must agree in type, shape, strides and device")
+        if not (isinstance(page_table, torch.Tensor) and page_table.dim() == 2):
+            raise ValueError("page_table: an int32 tensor [n_seqs, max_pages] is expected")
+        self.device = k_pages.device
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        c = PagedCache()
+        c.n_pages, c.n_kv_heads, c.page_size, c.head_dim = k_pages.shape
+        c.page_stride, c.head_stride, c.token_stride = k_pages.stride()[:3]
+        c.n_q_heads = n_q_heads
+        c.kv_dtype = _dtype_code(k_pages)
+        c.n_seqs, c.max_pages = page_table.shape
+        c.k_pages, c.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
+        c.page_table = _need(page_table, "page_table", torch.int32, tuple(page_table.shape), self.device)
+        self.nq, self.nkv = n_q_heads, c.n_kv_heads
+        # one description for each type of activations
+        self._c = {}
+        for act in (Q3_F32, Q3_BF16):
+            d = PagedCache.from_buffer_copy(c)
+            d.act_dtype = act
+            self._c[act] = d
+        self.ws_bytes = lib().q3paged_workspace_bytes(ctypes.addressof(self._c[Q3_F32]))
+        if self.ws_bytes == 0:
+            _paged_raise(Q3_ERR_ARG)
+        self._ws = {}
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _workspace(self, stream):
+        import torch
+        if torch.cuda.is_current_stream_capturing():
+            # the graph's own, zeroed by a node of it
+            return torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        ws = self._ws.get(stream)
+        if ws is None:
+            ws = self._ws[stream] = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        return ws
+
+    def _rows(self, t, name, width, dtype=None):
+        """A 2-D or 3-D CUDA tensor whose rows are `width` contiguous values: (rows, row stride)."""
+        if not (t.is_cuda and t.device == self.device and t.dim() in (2, 3) and (dtype is None or t.dtype == dtype)):
+            raise ValueError(f"{name}: a CUDA tensor of rows on {self.device} is expected")
+        n = t.shape[0]
+        inner = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
+        dense = t.stride(-1) == 1 and (t.dim() == 2 or t.shape[1] == 1 or t.stride(1) == t.shape[2])
+        if inner != width or not dense:
+            raise ValueError(f"{name}: rows of {width} contiguous values are expected")
+        return n, (t.stride(0) if n > 1 else width)
+
+    def append(self, qkv, seq, pos, rope, q_norm=None, k_norm=None, eps=1e-6, out=None):
+        """Norms and turns the q and k heads of qkv [n, (nq + 2 nkv) * 128], stores keys and values at positions
+        `pos` of sequences `seq` (int32 [n]; a position < 0 skips its row) and returns the queries [n, nq, 128].
+        rope: float32 [rows, 64, 2], cosine and sine of each pair at each position."""
+        import torch
+        n, ld = self._rows(qkv, "qkv", (self.nq + 2 * self.nkv) * 128)
+        c = self._c[_dtype_code(qkv)]
+        dev = self.device
+        if out is None:
+            out = torch.empty((n, self.nq, 128), dtype=qkv.dtype, device=dev)
+        no, ldo = self._rows(out, "out", self.nq * 128, qkv.dtype)
+        if no != n:
+            raise ValueError("out: one row for each token is expected")
+        rows = rope.shape[0]
+        args = (_need(seq, "seq", torch.int32, (n,), dev), _need(pos, "pos", torch.int32, (n,), dev),
+                None if q_norm is None else _need(q_norm, "q_norm", torch.float32, (128,), dev),
+                None if k_norm is None else _need(k_norm, "k_norm", torch.float32, (128,), dev), eps,
+                _need(rope, "rope", torch.float32, (rows, 64, 2), dev))
+        with _on_device(dev.index):
+            rc = lib().q3paged_append(ctypes.addressof(c), n, qkv.data_ptr(), ld, *args, rows, out.data_ptr(), ldo,
+                                      self.err.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        if rc:
+            _paged_raise(rc)
+        return out
+
+    def attend(self, q, q_off, ctx_len, max_q: int, scale=128 ** -0.5, out=None):
+        """Causal attention of the newest tokens of every sequence: rows q_off[s]..q_off[s+1]-1 of q [n, nq, 128]
+        are the last ones of sequence s, which has ctx_len[s] positions (int32 tensors); max_q bounds the new
+        tokens of a sequence.  Returns [n, nq, 128]."""
+        import torch
+        n, ld = self._rows(q, "q", self.nq * 128)
+        c = self._c[_dtype_code(q)]
+        dev = self.device
+        if out is None:
+            out = torch.empty((n, self.nq, 128), dtype=q.dtype, device=dev)
+        no, ldo = self._rows(out, "out", self.nq * 128, q.dtype)
+        if no != n:
+            raise ValueError("out: one row for each row of q is expected")
+        off = _need(q_off, "q_off", torch.int32, (c.n_seqs + 1,), dev)
+        ctx = _need(ctx_len, "ctx_len", torch.int32, (c.n_seqs,), dev)
+        with _on_device(dev.index):
+            stream = torch.cuda.current_stream().cuda_stream
+            ws = self._workspace(stream)
+            rc = lib().q3paged_attention(ctypes.addressof(c), n, max_q, q.data_ptr(), ld, off, ctx, scale,
+                                         out.data_ptr(), ldo, ws.data_ptr(), self.ws_bytes, self.err.data_ptr(),
+                                         stream)
+        if rc:
+            _paged_raise(rc)
+        return out
+
+    def check(self):
+        """Waits for the work so far and raises where the device met a page, position or length out of range."""
+        e = int(self.err.item())
+        if e:
+            self.err.zero_()
+            raise Q3Error(Q3_ERR_TIMEOUT if e & Q3PAGED_ERR_TIMEOUT else Q3_ERR_BOUNDS,
+                          "a device wait timed out" if e & Q3PAGED_ERR_TIMEOUT else
+                          "a page, position or length is out of range")
+
+
+def sample_given(logits, u, temperature, top_k, top_p, min_p, ids=None, logprob=None, err=None):
+    """Draws one id for each row of logits ([n, vocab], float32 or bfloat16) from the given uniform numbers u,
+    everything on the GPU and queued on the current stream: u, temperature, top_p, min_p float32 [n], top_k
+    int32 [n].  Returns (ids int32 [n], log probabilities float32 [n]); an id is -1 where a row's logits hold
+    NaN, +inf or nothing finite (q3tts_sample_given in q3tts.h has the definition)."""
+    import torch
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2 and
+            (logits.shape[1] <= 1 or logits.stride(1) == 1)):
+        raise ValueError("logits: a CUDA tensor [n, vocab] with contiguous rows is expected")
+    n, vocab = logits.shape
+    dev, code = logits.device, _dtype_code(logits)
+    if ids is None:
+        ids = torch.empty(n, dtype=torch.int32, device=dev)
+    if logprob is None:
+        logprob = torch.empty(n, dtype=torch.float32, device=dev)
+    f = torch.float32
+    args = (_need(u, "u", f, (n,), dev), _need(temperature, "temperature", f, (n,), dev),
+            _need(top_k, "top_k", torch.int32, (n,), dev), _need(top_p, "top_p", f, (n,), dev),
+            _need(min_p, "min_p", f, (n,), dev), _need(ids, "ids", torch.int32, (n,), dev),
+            _need(logprob, "logprob", f, (n,), dev),
+            None if err is None else _need(err, "err", torch.int32, (1,), dev))
+    with _on_device(dev.index):
+        rc = lib().q3tts_sample_given(n, vocab, logits.data_ptr(), code, logits.stride(0) if n > 1 else vocab, *args,
+                                      torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _paged_raise(rc)
+    return ids, logprob
