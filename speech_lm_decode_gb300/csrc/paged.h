@@ -38,6 +38,10 @@ cudaError_t launch_paged_append(const PagedView& c, int act, int kv, int n_token
                                 int64_t q_stride, int* err, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttn& a, cudaStream_t st);
 size_t paged_workspace_bytes();
+// few query rows over bf16 pages (paged_decode.cu)
+bool paged_decode_takes(const PagedAttn& a);
+cudaError_t launch_paged_decode(const PagedAttn& a, cudaStream_t st);
+size_t paged_decode_ws();
 
 // text of the calling thread's last error (q3paged_last_error)
 int paged_fail(int code, const char* fmt, ...);

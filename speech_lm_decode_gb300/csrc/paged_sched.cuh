@@ -1,0 +1,103 @@
+// Work split of the paged attention kernels, computed on the device from the
+// sequence lengths (the host never sees them).
+//
+// The keys that the items of a call have to read are numbered as one list of
+// units (an item: a kv head and a tile of query rows of one sequence; a unit:
+// a fixed number of its keys), and CTA c of P takes units
+// [c W / P, (c + 1) W / P).  So every CTA has the same amount to read however
+// the lengths differ, and an item is cut only at a CTA's ends: a CTA has at
+// most two cut items, one that it continues (partial slot 0) and one that it
+// begins (slot 1).  The CTAs of a cut item are consecutive; each stores its
+// unnormalised output, maximum and sum, and the last one to arrive (a counter
+// that belongs to the first of them, reset by the last) joins them in CTA
+// order, so results do not depend on timing.  No CTA waits for another.
+#pragma once
+#include "common.cuh"
+#include "paged.h"
+
+namespace q3 {
+
+// A sequence as the kernels may use it: rows inside [0, n_tokens), lengths
+// inside the table; anything else sets the bounds bit and has no rows (or a
+// clamped context).
+struct PagedSeq { int row0, n_new, ctx; };
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedAttn& a, int s, bool report) {
+    PagedSeq q;
+    q.row0 = a.q_off[s];
+    const int end = a.q_off[s + 1], cap = a.c.max_pages << a.c.page_shift;
+    q.n_new = end - q.row0;
+    q.ctx = a.ctx[s];
+    bool bad = false;
+    if (q.row0 < 0 || q.n_new < 0 || end > a.n_tokens || q.n_new > a.max_q) { bad = true; q.n_new = 0; }
+    if (q.n_new > 0 && (q.ctx < 0 || q.ctx > cap)) { bad = true; q.ctx = min(max(q.ctx, 0), cap); }
+    if (bad && report && a.err) atomicOr(a.err, ERRB_BOUNDS);
+    return q;
+}
+
+struct PagedRange {
+    long long W;        // units of the call
+    long long u0, u1;   // this CTA's
+    int s;              // sequence of u0
+    long long start;    // first unit of that sequence
+    int P;              // CTAs that share the units
+};
+
+// first unit of CTA c, and the CTA that owns unit u
+__device__ __forceinline__ long long paged_first(long long W, int P, int c) { return W * c / P; }
+__device__ __forceinline__ int paged_owner(long long W, int P, long long u) { return (int)(((u + 1) * P - 1) / W); }
+
+// This CTA's range.  units(s): units of sequence s, all kv heads.  NT threads
+// call it; min_units: units that a CTA gets at least (fewer CTAs then work).
+template <int NT, class F>
+__device__ __forceinline__ PagedRange paged_range(int n_seqs, int P, int min_units, F units) {
+    __shared__ long long warp_sum_s[NT / 32];
+    __shared__ long long found_start;
+    __shared__ int found_s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (n_seqs + NT - 1) / NT;
+    const int s0 = min(tid * per, n_seqs), s1 = min(s0 + per, n_seqs);
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) mine += units(s);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum_s[warp] = incl;
+    __syncthreads();
+    long long before = 0, W = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += warp_sum_s[w];
+        W += warp_sum_s[w];
+    }
+    PagedRange r;
+    r.W = W;
+    r.P = (int)min((long long)P, max(1LL, W / min_units));
+    const int c = blockIdx.x;
+    r.u0 = c < r.P ? paged_first(W, r.P, c) : W;
+    r.u1 = c < r.P ? paged_first(W, r.P, c + 1) : W;
+    long long start = before + incl - mine;
+    if (r.u0 < r.u1 && start <= r.u0 && r.u0 < start + mine) {
+        int s = s0;
+        for (; s < s1 - 1; ++s) {
+            const long long n = units(s);
+            if (r.u0 < start + n) break;
+            start += n;
+        }
+        found_s = s;
+        found_start = start;
+    }
+    __syncthreads();
+    r.s = found_s;
+    r.start = found_start;
+    return r;
+}
+
+// Workspace of the paged attention: counters, then two partial slots a CTA.
+constexpr int PAGED_MAX_CTAS = 1024;
+constexpr size_t PAGED_COUNTER_BYTES = PAGED_MAX_CTAS * sizeof(int);
+
+}  // namespace q3
