@@ -40,6 +40,9 @@ extern "C" {
 #define Q3PAGED_ERR_BOUNDS   2
 #define Q3PAGED_ERR_TIMEOUT  4
 
+/* leading bytes of the workspace that are zero before its first use */
+#define Q3PAGED_COUNTER_BYTES  4096
+
 /* A paged cache.  Position p of sequence s is slot p % page_size of page
  * page_table[s][p / page_size]; pages may be shared between sequences that
  * only read them.  Strides are in elements; 0 selects the packed layout
@@ -84,8 +87,8 @@ int q3paged_append(const q3paged_cache* c, int n_tokens, const void* qkv, int64_
                    int rope_rows, void* q_out, int64_t q_stride, int32_t* err, void* stream);
 
 /* Bytes of workspace that q3paged_attention wants for this cache's heads
- * (0: invalid cache).  The caller fills it with zeros once; every call leaves
- * it ready for the next.  Calls that may run at the same time (other streams,
+ * (0: invalid cache).  The caller clears its first Q3PAGED_COUNTER_BYTES bytes
+ * once; every call leaves it ready for the next.  Calls that may run at the same time (other streams,
  * graphs replayed side by side) need one workspace each. */
 size_t q3paged_workspace_bytes(const q3paged_cache* c);
 

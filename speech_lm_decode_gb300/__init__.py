@@ -510,7 +510,7 @@ class Q3Codec:
 
 # ---------------------------------------------------------------- paged cache (q3paged.h)
 PAGED_EXPORTS = ("q3paged_append", "q3paged_workspace_bytes", "q3paged_attention", "q3paged_last_error")
-Q3PAGED_ERR_BOUNDS, Q3PAGED_ERR_TIMEOUT = 2, 4
+Q3PAGED_ERR_BOUNDS, Q3PAGED_ERR_TIMEOUT, Q3PAGED_COUNTER_BYTES = 2, 4, 4096
 
 
 class PagedCache(ctypes.Structure):
@@ -604,8 +604,10 @@ class PagedKV:
     def _workspace(self, stream):
         import torch
         if torch.cuda.is_current_stream_capturing():
-            # the graph's own, zeroed by a node of it
-            return torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            # the graph's own; a node of it clears the counters
+            ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            ws[:Q3PAGED_COUNTER_BYTES].zero_()
+            return ws
         ws = self._ws.get(stream)
         if ws is None:
             ws = self._ws[stream] = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)

@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libq3tts.so")
 SOURCES = ["linear.cu", "gemm_tc.cu", "attention.cu", "sampler.cu", "loop.cu", "persist.cu", "cluster_step.cu", "q3tts.cu",
-           "noalloc.cu", "codec.cu", "paged.cu", "paged_attn.cu", "paged_decode.cu", "sample_given.cu"]
+           "noalloc.cu", "codec.cu", "paged.cu", "paged_attn.cu", "paged_decode.cu", "paged_chunk.cu", "sample_given.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]

@@ -42,6 +42,9 @@ size_t paged_workspace_bytes();
 bool paged_decode_takes(const PagedAttn& a);
 cudaError_t launch_paged_decode(const PagedAttn& a, cudaStream_t st);
 size_t paged_decode_ws();
+// many query rows over bf16 pages (paged_chunk.cu)
+cudaError_t launch_paged_chunk(const PagedAttn& a, cudaStream_t st);
+size_t paged_chunk_ws();
 
 // text of the calling thread's last error (q3paged_last_error)
 int paged_fail(int code, const char* fmt, ...);

@@ -67,10 +67,11 @@ __global__ void __launch_bounds__(128) paged_plain_kernel(PagedAttn a) {
 
 }  // namespace
 
-size_t paged_workspace_bytes() { return PAGED_COUNTER_BYTES + paged_decode_ws(); }
+size_t paged_workspace_bytes() { return PAGED_COUNTER_BYTES + max(paged_decode_ws(), paged_chunk_ws()); }
 
 cudaError_t launch_paged_attention(const PagedAttn& a, cudaStream_t st) {
     if (paged_decode_takes(a)) return launch_paged_decode(a, st);
+    if (a.kv == Q3_BF16) return launch_paged_chunk(a, st);
     const int64_t blocks = ((int64_t)a.n_tokens * a.c.nq + 3) / 4;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     if (a.act == Q3_BF16) return launch_pdl(paged_plain_kernel<bf16, bf16>, (unsigned)blocks, 128, 0, st, a);

@@ -1,0 +1,750 @@
+// Paged attention for many query rows (chunks of prompts, mixed batches) over
+// bf16 pages, on the fifth-generation tensor cores.
+//
+// An item is up to 256 query rows (tokens x q heads of one kv head; two tiles
+// of 128) of one sequence, its units are tiles of 128 keys; one persistent CTA
+// per SM takes an equal share of all units (paged_sched.cuh).  Inside a CTA
+//   warp 0      copies K and V tiles into a ring of 32 KB stages (TMA, one box
+//               per page and 64 values of the head, 128-byte swizzle);
+//   warp 1      issues S = Q K^T and O += P V (tcgen05.mma, M = N = 128); P is
+//               the A operand in tensor memory, V the transposed B operand;
+//   warps 4-7   softmax of slot 0, warps 8-11 of slot 1: a thread owns a row,
+//               reads its 128 scores from tensor memory, keeps the running
+//               maximum and sum, and writes P back over the scores.
+// The two slots alternate on the tensor cores, so that one's softmax runs while
+// the other's products do.  With two tiles of rows, a slot is a tile and both
+// read the same keys; with one tile (few rows, or fp32 activations), the slots
+// take the tile's even and odd key tiles, each with its own maximum, sum and
+// output, joined at the end from tensor memory.
+//
+// fp32 activations enter as three bf16 parts of q (24 bits: exact) and two of p
+// (16 bits): 5 products for 2.
+//
+// Every wait is bounded: one that runs out sets the timeout bit, after which
+// the CTA goes through its remaining steps without waiting or issuing, drains
+// its copies, frees its tensor memory and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "paged.h"
+#include "paged_sched.cuh"
+
+namespace q3 {
+
+namespace {
+
+constexpr int CT = 128;                    // rows of a tile, keys of a unit
+constexpr int STAGE = CT * HD * 2;         // bytes of a K or V tile
+constexpr int C_THREADS = 384;
+constexpr int C_MAX_CTAS = 192;
+constexpr int C_MIN_UNITS = 2;
+constexpr long long C_WAIT_LIMIT = 2000000000LL;
+constexpr int c_stages(bool f32) { return f32 ? 4 : 5; }
+constexpr int c_qbytes(bool f32) { return f32 ? 3 * STAGE : 2 * STAGE; }
+constexpr size_t C_SLOT = (size_t)2 * CT * (HD + 2);   // floats of a partial
+
+struct ChunkSmem {
+    uint64_t full[5], empty[5], s_full[2], p_full[2], q_full, o_full, drain;
+    uint32_t tmem;
+    int dead, last;
+    float m[CT], l[CT];      // slot 1's statistics for slot 0
+};
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t* b, unsigned n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, unsigned bytes) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
+                 ::"r"(su32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, unsigned parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// bounded wait; false once the CTA has given up (heed: not even looked at then)
+__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, ChunkSmem& s, int* err, bool heed = true) {
+    if (bar_try(b, parity)) return true;
+    const long long t0 = clock64();
+    while (!bar_try(b, parity)) {
+        if (heed && *(volatile int*)&s.dead) return false;
+        if (clock64() - t0 > C_WAIT_LIMIT) {
+            *(volatile int*)&s.dead = 1;
+            if (err) atomicOr(err, ERRB_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar)) : "memory");
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+          "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+          "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+          "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+          "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr) : "memory");
+}
+// waits for the loads; the registers pass through it, so that no use of them can move in front
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of a tile in shared memory, rows of 128 bytes, 128-byte swizzle.
+// K-major (Q, K): eight-row groups 1024 bytes apart.  MN-major (V: the 128
+// bytes run along the head): eight-key groups 1024 bytes apart, the second half
+// of the head `lead` bytes on.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t lead) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// fp32 D, bf16 A and B, M = N = 128; bit 16: B is MN-major
+constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(CT >> 3) << 17) | ((uint32_t)(CT >> 4) << 24);
+constexpr uint32_t IDESC_V = IDESC | (1u << 16);
+
+__device__ __forceinline__ float ex2f(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t*)&v;
+}
+
+// ------------------------------------------------------------------ items
+// One cut of an item that a CTA works on.
+struct Seg {
+    int s, h;             // sequence, kv head
+    int tok0, ntok;       // first token (of the sequence's new ones) and tokens of the item
+    int n;                // key tiles of this cut (0: the item sees no key)
+    int kt0;              // first of them
+    bool two;             // two tiles of rows
+    bool whole;           // the cut is the item
+    int ca, cb;           // CTAs of the item
+};
+
+struct Walk {
+    PagedSeq q;
+    long long u, u1, item0;   // next unit, end of the range, first unit of the current item
+    int s, h, item;
+};
+
+// tokens of an item (tpi) and the key tiles that item i of a sequence reads
+__device__ __forceinline__ int item_units(const PagedSeq& q, int tpi, int i) {
+    const int last = min(q.n_new, (i + 1) * tpi);
+    const int vis = min(q.ctx - q.n_new + last, q.ctx);
+    return max(1, (vis + CT - 1) / CT);
+}
+__device__ __forceinline__ long long seq_units(const PagedSeq& q, int tpi) {
+    long long n = 0;
+    for (int i = 0; i * tpi < q.n_new; ++i) n += item_units(q, tpi, i);
+    return n;
+}
+
+__device__ __forceinline__ void walk_begin(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
+    w.u = R.u0;
+    w.u1 = R.u1;
+    w.s = R.s;
+    w.q = paged_seq(a, w.s, false);
+    const long long per = seq_units(w.q, tpi);
+    long long rel = w.u - R.start;
+    w.h = (int)(rel / per);
+    rel -= w.h * per;
+    w.item0 = R.start + w.h * per;
+    w.item = 0;
+    for (;;) {
+        const int n = item_units(w.q, tpi, w.item);
+        if (rel < n) break;
+        rel -= n;
+        w.item0 += n;
+        ++w.item;
+    }
+}
+__device__ __forceinline__ bool walk_next(Walk& w, const PagedAttn& a, const PagedRange& R, int tpt, int tpi, Seg& g) {
+    if (w.u >= w.u1) return false;
+    const int nu = item_units(w.q, tpi, w.item);
+    const long long end = min(w.u1, w.item0 + nu);
+    g.s = w.s;
+    g.h = w.h;
+    g.tok0 = w.item * tpi;
+    g.ntok = min(tpi, w.q.n_new - g.tok0);
+    g.two = g.ntok > tpt;
+    g.kt0 = (int)(w.u - w.item0);
+    g.n = (int)(end - w.u);
+    const int vis = min(w.q.ctx - w.q.n_new + g.tok0 + g.ntok, w.q.ctx);
+    if (vis <= 0) g.n = 0;
+    g.whole = w.u == w.item0 && end == w.item0 + nu;
+    g.ca = paged_owner(R.W, R.P, w.item0);
+    g.cb = paged_owner(R.W, R.P, w.item0 + nu - 1);
+    w.u = end;
+    return true;
+}
+// on to the next item once the current one is done (only while units remain)
+__device__ __forceinline__ void walk_step(Walk& w, const PagedAttn& a, int tpi) {
+    const int nu = item_units(w.q, tpi, w.item);
+    if (w.u < w.item0 + nu) return;
+    w.item0 += nu;
+    ++w.item;
+    if (w.item * tpi < w.q.n_new) return;
+    w.item = 0;
+    if (++w.h < a.c.nkv) return;
+    w.h = 0;
+    if (w.u >= w.u1) return;
+    do { w.q = paged_seq(a, ++w.s, false); } while (w.q.n_new <= 0);
+}
+
+template <typename TA>
+__global__ void __launch_bounds__(C_THREADS, 1)
+paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                   const __grid_constant__ PagedAttn a) {
+    constexpr bool F32 = sizeof(TA) == 4;
+    constexpr int ST = c_stages(F32), QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    __shared__ ChunkSmem sm;
+    unsigned char* base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    unsigned char* qs = base;                       // Q tiles (bf16: per slot; fp32: per part)
+    unsigned char* ring = base + c_qbytes(F32);
+    const PagedView& c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tpt = CT / c.G, tpi = F32 ? tpt : 2 * tpt;   // tokens of a tile, of an item
+
+    const PagedRange R = paged_range<C_THREADS>(c.n_seqs, gridDim.x, C_MIN_UNITS, [&](int s) {
+        return c.nkv * seq_units(paged_seq(a, s, blockIdx.x == 0), tpi);
+    });
+    if (R.u0 >= R.u1) return;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) { bar_init(&sm.full[i], 1); bar_init(&sm.empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { bar_init(&sm.s_full[i], 1); bar_init(&sm.p_full[i], CT); }
+        bar_init(&sm.q_full, 2 * CT);
+        bar_init(&sm.o_full, 1);
+        bar_init(&sm.drain, 1);
+        sm.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sm.tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = sm.tmem;
+
+    Walk w;
+    walk_begin(w, a, R, tpi);
+    Seg g;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- K and V tiles
+        int cnt = 0, issued = 0;
+        bool ok = true;
+        const int box = min(1 << c.page_shift, CT), pmask = (1 << c.page_shift) - 1;
+        auto load = [&](const CUtensorMap* map, int kt) {
+            const int st = cnt % ST;
+            if (cnt >= ST) ok = ok && bar_wait(&sm.empty[st], (cnt / ST - 1) & 1, sm, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            ++cnt;
+            if (!ok) return;
+            issued = cnt;
+            const int rows = min(CT, w.q.ctx - kt * CT), nbox = (rows + box - 1) / box;
+            if (lane == 0) bar_expect(&sm.full[st], (unsigned)(nbox * box * HD * 2));
+            __syncwarp();
+            for (int i = lane; i < nbox; i += 32) {
+                const int key = kt * CT + i * box;
+                int page = c.table[(int64_t)g.s * c.max_pages + (key >> c.page_shift)];
+                if ((unsigned)page >= (unsigned)c.n_pages) {
+                    if (a.err) atomicOr(a.err, ERRB_BOUNDS);
+                    page = 0;
+                }
+                const uint32_t dst = su32(ring + (size_t)st * STAGE) + i * box * 128;
+                tma_4d(dst, map, 0, key & pmask, g.h, page, &sm.full[st]);
+                tma_4d(dst + STAGE / 2, map, 64, key & pmask, g.h, page, &sm.full[st]);
+            }
+        };
+        while (walk_next(w, a, R, tpt, tpi, g)) {
+            const int lead = g.two ? 1 : 2;
+            for (int i = 0; i < min(lead, g.n); ++i) load(&mapK, g.kt0 + i);
+            for (int i = 0; i < g.n; ++i) {
+                load(&mapV, g.kt0 + i);
+                if (i + lead < g.n) load(&mapK, g.kt0 + i + lead);
+            }
+            walk_step(w, a, tpi);
+        }
+        // given up: nothing may still be writing this CTA's shared memory when it leaves
+        if (*(volatile int*)&sm.dead)
+            for (int i = max(0, issued - ST); i < issued; ++i) bar_wait(&sm.full[i % ST], (i / ST) & 1, sm, a.err, false);
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- products
+        int cnt = 0, pc[2] = {0, 0}, qc = 0;
+        bool ok = true;
+        const uint32_t ring0 = su32(ring), q0 = su32(qs);
+        auto full = [&](int i) {
+            ok = ok && bar_wait(&sm.full[i % ST], (i / ST) & 1, sm, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            fence_after();
+        };
+        auto p_ready = [&](int t) {
+            ok = ok && bar_wait(&sm.p_full[t], pc[t] & 1, sm, a.err);
+            ++pc[t];
+            ok = __all_sync(0xffffffffu, ok);
+            fence_after();
+        };
+        auto release = [&](int i) { if (ok && lane == 0) commit(&sm.empty[i % ST]); };
+        // S of slot t from the K tile of ring entry i
+        auto scores = [&](int t, int i) {
+            if (ok && lane == 0) {
+                const uint32_t kb = ring0 + (i % ST) * STAGE;
+#pragma unroll
+                for (int p = 0; p < QP; ++p) {
+                    const uint32_t qb = q0 + (F32 ? p : (g.two ? t : 0)) * STAGE;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t off = (ks >> 2) * (STAGE / 2) + (ks & 3) * 32;
+                        umma_ss(tmem + t * CT, tile_desc(qb + off, 16), tile_desc(kb + off, 16), IDESC, (p | ks) != 0);
+                    }
+                }
+                commit(&sm.s_full[t]);
+            }
+            __syncwarp();
+        };
+        // O of slot t += P V
+        auto outputs = [&](int t, int i, bool acc) {
+            if (ok && lane == 0) {
+                const uint32_t vb = ring0 + (i % ST) * STAGE;
+#pragma unroll
+                for (int p = 0; p < PP; ++p)
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t pa = F32 ? 32 * (ks >> 1) + 8 * (ks & 1) + 16 * p : 8 * ks;
+                        umma_ts(tmem + 2 * CT + t * CT, tmem + t * CT + pa, tile_desc(vb + ks * 2048, STAGE / 2), IDESC_V,
+                                (acc || (p | ks) != 0) ? 1 : 0);
+                    }
+            }
+            __syncwarp();
+        };
+        // V rows of keys that do not exist become zeros (their weights are zero, what the pages hold may be NaN)
+        auto clear_tail = [&](int kt, int i) {
+            const int rows = w.q.ctx - kt * CT;
+            if (rows >= CT || !ok) return;
+            uint4* v = (uint4*)(ring + (size_t)(i % ST) * STAGE);
+            for (int r = rows * 8 + lane; r < CT * 8; r += 32) {
+                v[r] = make_uint4(0, 0, 0, 0);
+                v[r + STAGE / 32] = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            __syncwarp();
+        };
+        while (walk_next(w, a, R, tpt, tpi, g)) {
+            if (g.n > 0) {
+                ok = ok && bar_wait(&sm.q_full, qc & 1, sm, a.err);
+                ++qc;
+                ok = __all_sync(0xffffffffu, ok);
+                fence_after();
+                const int lead = g.two ? 1 : 2;
+                const int first = min(lead, g.n);
+                for (int i = 0; i < first; ++i) {
+                    full(cnt);
+                    scores(g.two ? 0 : i, cnt);
+                    if (g.two) scores(1, cnt);
+                    release(cnt);
+                    ++cnt;
+                }
+                for (int i = 0; i < g.n; ++i) {
+                    const int v = cnt, k = cnt + 1;
+                    const bool more = i + lead < g.n;
+                    if (g.two) {
+                        p_ready(0);
+                        full(v);
+                        clear_tail(g.kt0 + i, v);
+                        outputs(0, v, i > 0);
+                        if (more) { full(k); scores(0, k); }
+                        p_ready(1);
+                        outputs(1, v, i > 0);
+                        release(v);
+                        if (more) { scores(1, k); release(k); }
+                    } else {
+                        const int t = i & 1;
+                        p_ready(t);
+                        full(v);
+                        clear_tail(g.kt0 + i, v);
+                        outputs(t, v, i > 1);
+                        release(v);
+                        if (more) { full(k); scores(t, k); release(k); }
+                    }
+                    cnt += more ? 2 : 1;
+                }
+                if (ok && lane == 0) commit(&sm.o_full);
+                __syncwarp();
+            }
+            walk_step(w, a, tpi);
+        }
+        if (!ok && lane == 0) {   // products in flight end before the tensor memory goes
+            commit(&sm.drain);
+            bar_wait(&sm.drain, 0, sm, a.err, false);
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------- softmax
+        const int t = warp >= 8 ? 1 : 0;
+        const int r = (threadIdx.x & 127);                 // this thread's row of a tile
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + t * CT, tO = tmem + lanes + 2 * CT + t * CT, tO1 = tmem + lanes + 3 * CT;
+        const float sl2 = a.scale * 1.4426950408889634f, slack = 8.f / sl2;
+        int* counters = (int*)a.ws;
+        float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
+        int sc = 0, oc = 0;
+        bool ok = true;
+        while (walk_next(w, a, R, tpt, tpi, g)) {
+            // both slots are done with Q and with the tensor memory of the item before
+            wg_sync(1);
+            const int tile = g.two ? t : 0;
+            const int tok = g.tok0 + tile * tpt + r / c.G, head = g.h * c.G + r % c.G;
+            const bool live = r < tpt * c.G && tok < g.tok0 + g.ntok;
+            const int lim = live ? min(w.q.ctx - w.q.n_new + tok + 1, w.q.ctx) : 0;
+            float mx = -INFINITY, l = 0.f;
+            if (g.n > 0) {
+                // ---- query rows: 16 threads a row, 16 bytes of bf16 each
+                const int first = g.two ? 0 : t * 64, count = g.two ? CT : 64;
+                for (int i = r; i < count * 16; i += CT) {
+                    const int row = first + (i >> 4), ch = i & 15;
+                    const int rt = g.tok0 + tile * tpt + row / c.G;
+                    const bool there = row < tpt * c.G && rt < g.tok0 + g.ntok;
+                    const TA* src = (const TA*)a.q + (int64_t)(w.q.row0 + (there ? rt : 0)) * a.q_stride +
+                                    (int64_t)(g.h * c.G + (there ? row % c.G : 0)) * HD + ch * 8;
+                    const uint32_t off = (uint32_t)((ch >> 3) * (STAGE / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                    if constexpr (F32) {
+                        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                        const float4 f0 = there ? *(const float4*)src : z, f1 = there ? *(const float4*)(src + 4) : z;
+                        float x[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) {
+                            uint32_t d[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float h0 = __bfloat162float(__float2bfloat16_rn(x[2 * j]));
+                                const float h1 = __bfloat162float(__float2bfloat16_rn(x[2 * j + 1]));
+                                d[j] = pack_bf16(h0, h1);
+                                x[2 * j] -= h0;
+                                x[2 * j + 1] -= h1;
+                            }
+                            *(uint4*)(qs + (size_t)p * STAGE + off) = make_uint4(d[0], d[1], d[2], d[3]);
+                        }
+                    } else {
+                        *(uint4*)(qs + (size_t)tile * STAGE + off) = there ? *(const uint4*)src : make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_async_smem();
+                bar_arrive(&sm.q_full);
+            }
+            const int n = g.two ? g.n : (g.n + 1 - t) / 2;
+            for (int j = 0; j < n; ++j) {
+                const int k0 = (g.kt0 + (g.two ? j : 2 * j + t)) * CT;
+                ok = ok && bar_wait(&sm.s_full[t], sc & 1, sm, a.err);
+                ++sc;
+                ok = __all_sync(0xffffffffu, ok);
+                fence_after();
+                const int seen = lim - k0;                         // columns that the row sees
+                const bool masked = __any_sync(0xffffffffu, seen < CT);
+                float top = -INFINITY;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t x[32];
+                    tmem_ld32(tS + 32 * cc, x);
+                    tmem_wait_ld(x);
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * cc + i >= seen) x[i] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[i]));
+                }
+                // The maximum that the weights refer to moves only when a score passes it by 2^8.
+                const bool grew = top > mx + slack;
+                if (__any_sync(0xffffffffu, grew)) {
+                    const float nm = fmaxf(mx, top);
+                    const float f = nm == -INFINITY ? 1.f : ex2f((mx - nm) * sl2);
+                    mx = nm;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            uint32_t x[32];
+                            tmem_ld32(tO + 32 * cc, x);
+                            tmem_wait_ld(x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                            tmem_st32(tO + 32 * cc, x);
+                        }
+                    }
+                }
+                const float ref = mx == -INFINITY ? 0.f : -mx * sl2;
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t x[32], hi[16];
+                    tmem_ld32(tS + 32 * cc, x);
+                    tmem_wait_ld(x);
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * cc + i >= seen) x[i] = 0xff800000u;
+                    }
+                    float p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) p[i] = ex2f(fmaf(__uint_as_float(x[i]), sl2, ref));
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) { s0 += p[i]; s1 += p[i + 1]; }
+                    l += s0 + s1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) hi[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+                    if constexpr (F32) {
+                        uint32_t lo[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            lo[i] = pack_bf16(p[2 * i] - __uint_as_float(hi[i] << 16),
+                                              p[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
+                        tmem_st16(tS + 32 * cc, hi);
+                        tmem_st16(tS + 32 * cc + 16, lo);
+                    } else {
+                        tmem_st16(tS + 16 * cc, hi);
+                    }
+                }
+                tmem_wait_st();
+                fence_before();
+                bar_arrive(&sm.p_full[t]);
+            }
+            // ---- the item's (or the cut's) output
+            float l1 = 0.f, f0 = 1.f, f1 = 0.f;
+            if (g.n > 0) {
+                ok = ok && bar_wait(&sm.o_full, oc & 1, sm, a.err);
+                ++oc;
+                ok = __all_sync(0xffffffffu, ok);
+                fence_after();
+            }
+            if (!g.two) {
+                // slot 1's share of the keys joins slot 0's
+                if (t == 1) { sm.m[r] = mx; sm.l[r] = l; }
+                wg_sync(2);
+                if (t == 0) {
+                    const float m1 = sm.m[r];
+                    l1 = sm.l[r];
+                    const float m = fmaxf(mx, m1), ms = m == -INFINITY ? 0.f : m;
+                    f0 = ex2f((mx - ms) * sl2);
+                    f1 = ex2f((m1 - ms) * sl2);
+                    mx = m;
+                    l = l * f0 + l1 * f1;
+                }
+            }
+            const bool mine = g.two || t == 0;
+            const bool second = !g.two && g.n > 1;     // slot 1 has an output
+            TA* dst = (TA*)a.out + (int64_t)(w.q.row0 + tok) * a.out_stride + (int64_t)head * HD;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            auto put = [&](int col, const float (&v)[32]) {      // 32 values of the row
+                if (!live) return;
+                if constexpr (F32) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *(float4*)(dst + col + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        *(uint4*)(dst + col + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                                                              pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+                }
+            };
+            // partials: [32 groups of 4 values][256 rows], then maxima and sums
+            const int prow = tile * CT + r;
+            float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == g.ca ? 1 : 0)) * C_SLOT;
+            if (mine) {
+#pragma unroll 1
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t x[32], y[32];
+                    float v[32];
+                    if (g.n > 0) {
+                        tmem_ld32(tO + 32 * cc, x);
+                        if (second) tmem_ld32(tO1 + 32 * cc, y);
+                        tmem_wait_ld(x);
+                        if (second) tmem_wait_ld(y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        v[i] = l > 0.f ? __uint_as_float(x[i]) * f0 : 0.f;
+                        if (second && l > 0.f) v[i] = fmaf(__uint_as_float(y[i]), f1, v[i]);
+                    }
+                    if (g.whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] *= inv;
+                        put(32 * cc, v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *(float4*)(slot + ((size_t)(8 * cc + i / 4) * 2 * CT + prow) * 4) =
+                                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    }
+                }
+                if (!g.whole) {
+                    slot[2 * CT * HD + prow] = mx;
+                    slot[2 * CT * HD + 2 * CT + prow] = l;
+                }
+            }
+            fence_before();
+            if (!g.whole) {
+                __threadfence();
+                wg_sync(3);
+                if (threadIdx.x == 128) {
+                    sm.last = atomicAdd(&counters[g.ca], 1) == g.cb - g.ca;
+                    if (sm.last) counters[g.ca] = 0;
+                    __threadfence();
+                }
+                wg_sync(3);
+                if (sm.last && mine) {
+                    float m = -INFINITY;
+                    for (int cc = g.ca; cc <= g.cb; ++cc)
+                        m = fmaxf(m, __ldcg(parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT + 2 * CT * HD + prow));
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    float sum = 0.f;
+#pragma unroll 1
+                    for (int b = 0; b < 4; ++b) {
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                        sum = 0.f;
+#pragma unroll 1
+                        for (int cc = g.ca; cc <= g.cb; ++cc) {
+                            const float* p = parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT;
+                            const float f = ex2f((__ldcg(p + 2 * CT * HD + prow) - ms) * sl2);
+                            sum += f * __ldcg(p + 2 * CT * HD + 2 * CT + prow);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 z = __ldcg((const float4*)(p + ((size_t)(8 * b + i) * 2 * CT + prow) * 4));
+                                v[4 * i] = fmaf(z.x, f, v[4 * i]);
+                                v[4 * i + 1] = fmaf(z.y, f, v[4 * i + 1]);
+                                v[4 * i + 2] = fmaf(z.z, f, v[4 * i + 2]);
+                                v[4 * i + 3] = fmaf(z.w, f, v[4 * i + 3]);
+                            }
+                        }
+                        const float rs = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] *= rs;
+                        put(32 * b, v);
+                    }
+                }
+            }
+            walk_step(w, a, tpi);
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void* p = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)p;
+    }();
+    return fn;
+}
+
+// pages as [page][head][position][128], boxes of min(page, 128) positions x 64 values
+bool page_map(CUtensorMap* m, const PagedView& c, void* base) {
+    auto fn = encoder();
+    if (!fn) return false;
+    const int P = 1 << c.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)HD, (cuuint64_t)P, (cuuint64_t)c.nkv, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2,
+                                   (cuuint64_t)c.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)min(P, CT), 1, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+template <typename TA>
+cudaError_t launch_t(const PagedAttn& a, cudaStream_t st) {
+    constexpr bool F32 = sizeof(TA) == 4;
+    CUtensorMap mk, mv;
+    if (!page_map(&mk, a.c, a.c.k) || !page_map(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
+    constexpr int smem = c_qbytes(F32) + c_stages(F32) * STAGE + 1024;
+    // a per-device attribute: set on every call (a host-side table lookup)
+    cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<TA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = min(device_sm_count(), C_MAX_CTAS);
+    paged_chunk_kernel<TA><<<grid, C_THREADS, smem, st>>>(mk, mv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t paged_chunk_ws() { return (size_t)C_MAX_CTAS * 2 * C_SLOT * sizeof(float); }
+
+cudaError_t launch_paged_chunk(const PagedAttn& a, cudaStream_t st) {
+    return a.act == Q3_BF16 ? launch_t<bf16>(a, st) : launch_t<float>(a, st);
+}
+
+}  // namespace q3

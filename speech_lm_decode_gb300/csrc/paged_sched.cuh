@@ -98,6 +98,7 @@ __device__ __forceinline__ PagedRange paged_range(int n_seqs, int P, int min_uni
 
 // Workspace of the paged attention: counters, then two partial slots a CTA.
 constexpr int PAGED_MAX_CTAS = 1024;
-constexpr size_t PAGED_COUNTER_BYTES = PAGED_MAX_CTAS * sizeof(int);
+constexpr size_t PAGED_COUNTER_BYTES = Q3PAGED_COUNTER_BYTES;
+static_assert(PAGED_MAX_CTAS * sizeof(int) <= PAGED_COUNTER_BYTES, "a counter for each CTA");
 
 }  // namespace q3
