@@ -183,8 +183,9 @@ struct Seg {
 
 struct Walk {
     PagedSeq q;
-    long long u, u1, item0;   // next unit, end of the range, first unit of the current item
-    int s, h, item;
+    long long u, item0;   // unit to begin at, first unit of the item
+    int s, h, item, nu;   // nu: units of the item
+    bool more;
 };
 
 // tokens of an item (tpi) and the key tiles that item i of a sequence reads
@@ -199,29 +200,44 @@ __device__ __forceinline__ long long seq_units(const PagedSeq& q, int tpi) {
     return n;
 }
 
+// on to the next item
+__device__ __forceinline__ void walk_step(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
+    w.item0 += w.nu;
+    w.u = w.item0;
+    if (w.item0 >= R.u1) { w.more = false; return; }
+    if (++w.item * tpi >= w.q.n_new) {
+        w.item = 0;
+        if (++w.h == a.c.nkv) {
+            w.h = 0;
+            do { w.q = paged_seq(a, ++w.s, false); } while (w.q.n_new <= 0);
+        }
+    }
+    w.nu = item_units(w.q, tpi, w.item);
+}
 __device__ __forceinline__ void walk_begin(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
-    w.u = R.u0;
-    w.u1 = R.u1;
     w.s = R.s;
-    w.q = paged_seq(a, w.s, false);
+    w.q = R.q;
+    w.more = true;
     const long long per = seq_units(w.q, tpi);
-    long long rel = w.u - R.start;
+    long long rel = R.u0 - R.start;
     w.h = (int)(rel / per);
     rel -= w.h * per;
     w.item0 = R.start + w.h * per;
     w.item = 0;
     for (;;) {
-        const int n = item_units(w.q, tpi, w.item);
-        if (rel < n) break;
-        rel -= n;
-        w.item0 += n;
+        w.nu = item_units(w.q, tpi, w.item);
+        if (rel < w.nu) break;
+        rel -= w.nu;
+        w.item0 += w.nu;
         ++w.item;
     }
+    w.u = paged_begin(R, w.item0, w.item0 + w.nu);
+    if (w.u == w.item0 + w.nu) walk_step(w, a, R, tpi);
 }
-__device__ __forceinline__ bool walk_next(Walk& w, const PagedAttn& a, const PagedRange& R, int tpt, int tpi, Seg& g) {
-    if (w.u >= w.u1) return false;
-    const int nu = item_units(w.q, tpi, w.item);
-    const long long end = min(w.u1, w.item0 + nu);
+// the part of the walk's item that this CTA takes
+__device__ __forceinline__ bool walk_seg(Walk& w, const PagedRange& R, int tpt, int tpi, Seg& g) {
+    long long end;
+    if (!w.more || !paged_cut(R, w.item0, w.item0 + w.nu, &end)) return false;
     g.s = w.s;
     g.h = w.h;
     g.tok0 = w.item * tpi;
@@ -229,26 +245,12 @@ __device__ __forceinline__ bool walk_next(Walk& w, const PagedAttn& a, const Pag
     g.two = g.ntok > tpt;
     g.kt0 = (int)(w.u - w.item0);
     g.n = (int)(end - w.u);
-    const int vis = min(w.q.ctx - w.q.n_new + g.tok0 + g.ntok, w.q.ctx);
-    if (vis <= 0) g.n = 0;
-    g.whole = w.u == w.item0 && end == w.item0 + nu;
-    g.ca = paged_owner(R.W, R.P, w.item0);
-    g.cb = paged_owner(R.W, R.P, w.item0 + nu - 1);
-    w.u = end;
+    if (w.q.ctx - w.q.n_new + g.tok0 + g.ntok <= 0 || w.q.ctx <= 0) g.n = 0;
+    g.whole = w.u == w.item0 && end == w.item0 + w.nu;
+    g.ca = paged_cut_first(R, w.item0);
+    g.cb = paged_cut_last(R, w.item0 + w.nu);
+    w.more = end == w.item0 + w.nu;   // a cut end is this CTA's last
     return true;
-}
-// on to the next item once the current one is done (only while units remain)
-__device__ __forceinline__ void walk_step(Walk& w, const PagedAttn& a, int tpi) {
-    const int nu = item_units(w.q, tpi, w.item);
-    if (w.u < w.item0 + nu) return;
-    w.item0 += nu;
-    ++w.item;
-    if (w.item * tpi < w.q.n_new) return;
-    w.item = 0;
-    if (++w.h < a.c.nkv) return;
-    w.h = 0;
-    if (w.u >= w.u1) return;
-    do { w.q = paged_seq(a, ++w.s, false); } while (w.q.n_new <= 0);
 }
 
 template <typename TA>
@@ -266,9 +268,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tpt = CT / c.G, tpi = F32 ? tpt : 2 * tpt;   // tokens of a tile, of an item
 
-    const PagedRange R = paged_range<C_THREADS>(c.n_seqs, gridDim.x, C_MIN_UNITS, [&](int s) {
-        return c.nkv * seq_units(paged_seq(a, s, blockIdx.x == 0), tpi);
-    });
+    const PagedRange R = paged_range<C_THREADS>(a, gridDim.x, C_MIN_UNITS,
+                                                [&](const PagedSeq& q) { return c.nkv * seq_units(q, tpi); });
     if (R.u0 >= R.u1) return;
 
     if (threadIdx.x == 0) {
@@ -321,14 +322,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 tma_4d(dst + STAGE / 2, map, 64, key & pmask, g.h, page, &sm.full[st]);
             }
         };
-        while (walk_next(w, a, R, tpt, tpi, g)) {
+        while (walk_seg(w, R, tpt, tpi, g)) {
             const int lead = g.two ? 1 : 2;
             for (int i = 0; i < min(lead, g.n); ++i) load(&mapK, g.kt0 + i);
             for (int i = 0; i < g.n; ++i) {
                 load(&mapV, g.kt0 + i);
                 if (i + lead < g.n) load(&mapK, g.kt0 + i + lead);
             }
-            walk_step(w, a, tpi);
+            if (w.more) walk_step(w, a, R, tpi);
         }
         // given up: nothing may still be writing this CTA's shared memory when it leaves
         if (*(volatile int*)&sm.dead)
@@ -394,7 +395,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             fence_async_smem();
             __syncwarp();
         };
-        while (walk_next(w, a, R, tpt, tpi, g)) {
+        while (walk_seg(w, R, tpt, tpi, g)) {
             if (g.n > 0) {
                 ok = ok && bar_wait(&sm.q_full, qc & 1, sm, a.err);
                 ++qc;
@@ -436,7 +437,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 if (ok && lane == 0) commit(&sm.o_full);
                 __syncwarp();
             }
-            walk_step(w, a, tpi);
+            if (w.more) walk_step(w, a, R, tpi);
         }
         if (!ok && lane == 0) {   // products in flight end before the tensor memory goes
             commit(&sm.drain);
@@ -453,7 +454,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
         int sc = 0, oc = 0;
         bool ok = true;
-        while (walk_next(w, a, R, tpt, tpi, g)) {
+        while (walk_seg(w, R, tpt, tpi, g)) {
             // both slots are done with Q and with the tensor memory of the item before
             wg_sync(1);
             const int tile = g.two ? t : 0;
@@ -649,9 +650,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             }
             fence_before();
             if (!g.whole) {
-                __threadfence();
                 wg_sync(3);
                 if (threadIdx.x == 128) {
+                    __threadfence();
                     sm.last = atomicAdd(&counters[g.ca], 1) == g.cb - g.ca;
                     if (sm.last) counters[g.ca] = 0;
                     __threadfence();
@@ -690,7 +691,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                 }
             }
-            walk_step(w, a, tpi);
+            if (w.more) walk_step(w, a, R, tpi);
         }
     }
     __syncwarp();

@@ -90,32 +90,34 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
         const int groups = (q.n_new * c.G + RG - 1) / RG;
         return (long long)c.nkv * groups * max(1, (q.ctx + DU - 1) / DU);
     };
-    const PagedRange R = paged_range<DW * 32>(c.n_seqs, grid_max, D_MIN_UNITS, [&](int s) {
-        return units_of(paged_seq(a, s, blockIdx.x == 0));
-    });
+    const PagedRange R = paged_range<DW * 32>(a, grid_max, D_MIN_UNITS, units_of);
     if (R.u0 >= R.u1) return;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in powers of two
     const float slack = 8.f / sl2;
     int* counters = (int*)a.ws;
-    constexpr size_t SLOT = (size_t)RG * (HD + 2);
+    constexpr size_t SLOT = (size_t)RG * (HD + 4);   // outputs, maxima, sums (16-byte rows)
     float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
+    static_assert(sizeof(so) / sizeof(float) >= (size_t)160 * d_ctas(NT) * RG, "weights of the parts fit");
 
-    long long u = R.u0, start = R.start;
     int s = R.s;
-    PagedSeq q = paged_seq(a, s, false);
-    long long sunits = units_of(q);
-    while (u < R.u1) {
-        while (u >= start + sunits) {
-            start += sunits;
-            q = paged_seq(a, ++s, false);
-            sunits = units_of(q);
-        }
-        const int nu = max(1, (q.ctx + DU - 1) / DU);
-        const long long item = (u - start) / nu;
-        const long long item0 = start + item * nu;            // the item's units [item0, item0 + nu)
-        const long long seg_end = min(R.u1, item0 + nu);
-        const int groups = (q.n_new * c.G + RG - 1) / RG;
-        const int h = (int)(item / groups), rg = (int)(item - (long long)h * groups);
+    PagedSeq q = R.q;
+    int nu = max(1, (q.ctx + DU - 1) / DU), groups = (q.n_new * c.G + RG - 1) / RG;   // units and row groups of a head
+    int item = (int)((R.u0 - R.start) / nu);                                          // head * groups + row group
+    long long item0 = R.start + (long long)item * nu;                                 // the item's units [item0, item0 + nu)
+    auto next_item = [&]() -> bool {
+        item0 += nu;
+        if (++item < c.nkv * groups) return true;
+        if (item0 >= R.u1) return false;
+        do { q = paged_seq(a, ++s, false); } while (q.n_new <= 0);
+        nu = max(1, (q.ctx + DU - 1) / DU);
+        groups = (q.n_new * c.G + RG - 1) / RG;
+        item = 0;
+        return true;
+    };
+    long long u = paged_begin(R, item0, item0 + nu), seg_end;
+    if (u == item0 + nu && !next_item()) return;
+    while (paged_cut(R, item0, item0 + nu, &seg_end)) {
+        const int h = item / groups, rg = item - h * groups;
         const int key0 = (int)(u - item0) * DU, key1 = min(q.ctx, (int)(seg_end - item0) * DU);
         const int rows = min(RG, q.n_new * c.G - rg * RG);
 
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
         }
         __syncthreads();
         const bool whole = u == item0 && seg_end == item0 + nu;
-        const int ca = paged_owner(R.W, R.P, item0), cb = paged_owner(R.W, R.P, item0 + nu - 1);
+        const int ca = paged_cut_first(R, item0), cb = paged_cut_last(R, item0 + nu);   // where it is cut
         float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == ca ? 1 : 0)) * SLOT;
         TA* out = (TA*)a.out;
         auto store = [&](int r, float v) {
@@ -352,45 +354,79 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
             }
         }
         if (!whole) {
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
+                __threadfence();
                 s_last = atomicAdd(&counters[ca], 1) == cb - ca;
                 if (s_last) counters[ca] = 0;
                 __threadfence();
             }
             __syncthreads();
             if (s_last) {
-                for (int r = 0; r < rows; ++r) {
-                    float m = -INFINITY, acc = 0.f, sum = 0.f;
-#pragma unroll 4
-                    for (int cc = ca; cc <= cb; ++cc) {
-                        const float* p = parts + (size_t)(cc * 2 + (cc == ca ? 1 : 0)) * SLOT;
-                        const float pm = __ldcg(p + RG * HD + r), pl = __ldcg(p + RG * HD + RG + r);
-                        const float v = __ldcg(p + r * HD + tid);
-                        const float nm = fmaxf(m, pm), ms = nm == -INFINITY ? 0.f : nm;
-                        const float f0 = ex2((m - ms) * sl2), f1 = ex2((pm - ms) * sl2);
-                        acc = acc * f0 + v * f1;
-                        sum = sum * f0 + pl * f1;
-                        m = nm;
+                // weights of the parts (so is free: every thread is past the barriers above), then each warp
+                // adds up every fourth part
+                const int n = cb - ca + 1;
+                float* wt = &so[0][0][0];
+                auto part = [&](int i) { return parts + (size_t)((ca + i) * 2 + (i == 0 ? 1 : 0)) * SLOT; };
+                for (int r = warp; r < rows; r += DW) {
+                    float m = -INFINITY, sum = 0.f;
+                    for (int i = lane; i < n; i += 32) {
+                        const float v = __ldcg(part(i) + RG * HD + r);
+                        wt[i * RG + r] = v;
+                        m = fmaxf(m, v);
                     }
-                    store(r, sum > 0.f ? acc / sum : 0.f);
+                    m = warp_max(m);
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    for (int i = lane; i < n; i += 32) {
+                        const float f = ex2((wt[i * RG + r] - ms) * sl2);
+                        wt[i * RG + r] = f;
+                        sum += f * __ldcg(part(i) + RG * HD + RG + r);
+                    }
+                    sum = warp_sum(sum);
+                    if (lane == 0) sm_l[0][r] = sum;
+                }
+                __syncthreads();
+                float4 acc[RG];
+#pragma unroll
+                for (int r = 0; r < RG; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int i = warp; i < n; i += DW) {
+                    const float* p = part(i) + lane * 4;
+#pragma unroll
+                    for (int r = 0; r < RG; ++r)
+                        if (r < rows) {
+                            const float4 v = __ldcg((const float4*)(p + r * HD));
+                            const float f = wt[i * RG + r];
+                            acc[r].x = fmaf(v.x, f, acc[r].x); acc[r].y = fmaf(v.y, f, acc[r].y);
+                            acc[r].z = fmaf(v.z, f, acc[r].z); acc[r].w = fmaf(v.w, f, acc[r].w);
+                        }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < RG; ++r)
+                    if (r < rows) *(float4*)&so[warp][r][lane * 4] = acc[r];
+                __syncthreads();
+                for (int r = 0; r < rows; ++r) {
+                    const float sum = sm_l[0][r];
+                    const float v = so[0][r][tid] + so[1][r][tid] + so[2][r][tid] + so[3][r][tid];
+                    store(r, sum > 0.f ? v / sum : 0.f);
                 }
             }
         }
-        u = seg_end;
+        if (seg_end < item0 + nu || !next_item()) return;
+        u = item0;
     }
 }
 
 template <typename TA, int NT>
 cudaError_t launch_t(const PagedAttn& a, cudaStream_t st) {
-    const int grid = min(device_sm_count() * d_ctas(NT), PAGED_MAX_CTAS);
+    const int grid = min(device_sm_count(), 160) * d_ctas(NT);
     return launch_pdl(paged_decode_kernel<TA, NT>, grid, DW * 32, 0, st, a, grid);
 }
 
 }  // namespace
 
-size_t paged_decode_ws() { return (size_t)PAGED_MAX_CTAS * 2 * 16 * (HD + 2) * sizeof(float); }
+size_t paged_decode_ws() { return (size_t)PAGED_MAX_CTAS * 2 * 16 * (HD + 4) * sizeof(float); }
 
 bool paged_decode_takes(const PagedAttn& a) {
     return a.kv == Q3_BF16 && (int64_t)a.max_q * a.c.G <= (a.act == Q3_BF16 ? 16 : 8);

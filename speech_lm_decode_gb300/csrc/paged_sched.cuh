@@ -38,8 +38,10 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttn& a, int s, bool re
 struct PagedRange {
     long long W;        // units of the call
     long long u0, u1;   // this CTA's
-    int s;              // sequence of u0
-    long long start;    // first unit of that sequence
+    long long snap;     // cuts so near to an item's end move to it
+    long long start;    // first unit of the sequence of u0
+    int s;              // that sequence
+    PagedSeq q;
     int P;              // CTAs that share the units
 };
 
@@ -47,18 +49,42 @@ struct PagedRange {
 __device__ __forceinline__ long long paged_first(long long W, int P, int c) { return W * c / P; }
 __device__ __forceinline__ int paged_owner(long long W, int P, long long u) { return (int)(((u + 1) * P - 1) / W); }
 
-// This CTA's range.  units(s): units of sequence s, all kv heads.  NT threads
+// The part of item [a, b) that a CTA takes, having come to unit `from` of it;
+// false: none, its share ends in front of the item.
+__device__ __forceinline__ bool paged_cut(const PagedRange& r, long long a, long long b, long long* end) {
+    if (r.u1 <= a) return false;
+    *end = b;
+    if (r.u1 >= b) return true;
+    if (r.u1 - a <= r.snap) return false;
+    if (b - r.u1 > r.snap) *end = r.u1;
+    return true;
+}
+// Where a CTA whose share begins inside item [a, b) starts: a, u0, or b (the next item).
+__device__ __forceinline__ long long paged_begin(const PagedRange& r, long long a, long long b) {
+    return r.u0 - a <= r.snap ? a : b - r.u0 <= r.snap ? b : r.u0;
+}
+// first and last CTA of a cut item
+__device__ __forceinline__ int paged_cut_first(const PagedRange& r, long long a) { return paged_owner(r.W, r.P, a + r.snap); }
+__device__ __forceinline__ int paged_cut_last(const PagedRange& r, long long b) { return paged_owner(r.W, r.P, b - r.snap - 1); }
+
+// This CTA's range.  units(q): units of a sequence, all kv heads.  NT threads
 // call it; min_units: units that a CTA gets at least (fewer CTAs then work).
 template <int NT, class F>
-__device__ __forceinline__ PagedRange paged_range(int n_seqs, int P, int min_units, F units) {
+__device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int min_units, F units) {
     __shared__ long long warp_sum_s[NT / 32];
     __shared__ long long found_start;
     __shared__ int found_s;
+    __shared__ PagedSeq found_q;
+    const int n_seqs = a.c.n_seqs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (n_seqs + NT - 1) / NT;
     const int s0 = min(tid * per, n_seqs), s1 = min(s0 + per, n_seqs);
     long long mine = 0;
-    for (int s = s0; s < s1; ++s) mine += units(s);
+    PagedSeq q;
+    for (int s = s0; s < s1; ++s) {
+        q = paged_seq(a, s, blockIdx.x == 0);
+        mine += units(q);
+    }
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -82,17 +108,23 @@ __device__ __forceinline__ PagedRange paged_range(int n_seqs, int P, int min_uni
     long long start = before + incl - mine;
     if (r.u0 < r.u1 && start <= r.u0 && r.u0 < start + mine) {
         int s = s0;
-        for (; s < s1 - 1; ++s) {
-            const long long n = units(s);
-            if (r.u0 < start + n) break;
-            start += n;
+        if (s1 - s0 > 1) {
+            for (;; ++s) {
+                q = paged_seq(a, s, false);
+                const long long n = units(q);
+                if (r.u0 < start + n) break;
+                start += n;
+            }
         }
         found_s = s;
         found_start = start;
+        found_q = q;
     }
     __syncthreads();
     r.s = found_s;
     r.start = found_start;
+    r.q = found_q;
+    r.snap = min(W / r.P / 4, 2LL);
     return r;
 }
 
