@@ -541,20 +541,30 @@ class _on_device:
     def __enter__(self):
         import torch
         self.prev = torch.cuda.current_device()
-        if self.prev != self.index:
-            torch.cuda.set_device(self.index)
+        torch.cuda.set_device(self.index)
 
     def __exit__(self, *exc):
         import torch
-        if self.prev != self.index:
-            torch.cuda.set_device(self.prev)
+        torch.cuda.set_device(self.prev)
 
 
 def _need(t, name, dtype, shape, device):
-    """A contiguous CUDA tensor of this type, shape and device (the kernels read it by its address)."""
-    if not (t.is_cuda and t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous() and t.device == device):
-        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {shape} on {device} is expected")
+    """A contiguous CUDA tensor of this type, shape and device index (the kernels read it by its address)."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device} is expected")
     return t.data_ptr()
+
+
+def _on_stream(device, call):
+    """call(stream) with the tensors' device current, on its current stream."""
+    from torch import _C
+    if _C._cuda_getDevice() == device:
+        rc = call(_C._cuda_getCurrentRawStream(device))
+    else:
+        with _on_device(device):
+            rc = call(_C._cuda_getCurrentRawStream(device))
+    if rc:
+        _paged_raise(rc)
 
 
 class PagedKV:
@@ -578,7 +588,7 @@ class PagedKV:
             raise ValueError("k_pages and v_pages must agree in type, shape, strides and device")
         if not (isinstance(page_table, torch.Tensor) and page_table.dim() == 2):
             raise ValueError("page_table: an int32 tensor [n_seqs, max_pages] is expected")
-        self.device = k_pages.device
+        self.device, self._dev = k_pages.device, k_pages.get_device()
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         c = PagedCache()
         c.n_pages, c.n_kv_heads, c.page_size, c.head_dim = k_pages.shape
@@ -587,23 +597,26 @@ class PagedKV:
         c.kv_dtype = _dtype_code(k_pages)
         c.n_seqs, c.max_pages = page_table.shape
         c.k_pages, c.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
-        c.page_table = _need(page_table, "page_table", torch.int32, tuple(page_table.shape), self.device)
+        c.page_table = _need(page_table, "page_table", torch.int32, page_table.shape, self._dev)
         self.nq, self.nkv = n_q_heads, c.n_kv_heads
+        self._q_off_shape, self._ctx_shape = (c.n_seqs + 1,), (c.n_seqs,)
         # one description for each type of activations
         self._c = {}
         for act in (Q3_F32, Q3_BF16):
             d = PagedCache.from_buffer_copy(c)
             d.act_dtype = act
-            self._c[act] = d
-        self.ws_bytes = lib().q3paged_workspace_bytes(ctypes.addressof(self._c[Q3_F32]))
+            self._c[torch.float32 if act == Q3_F32 else torch.bfloat16] = (d, ctypes.addressof(d))
+        self._lib = lib()
+        self.ws_bytes = self._lib.q3paged_workspace_bytes(self._c[torch.float32][1])
         if self.ws_bytes == 0:
             _paged_raise(Q3_ERR_ARG)
         self._ws = {}
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._err = self.err.data_ptr()
 
     def _workspace(self, stream):
         import torch
-        if torch.cuda.is_current_stream_capturing():
+        if torch._C._cuda_isCurrentStreamCapturing():
             # the graph's own; a node of it clears the counters
             ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
             ws[:Q3PAGED_COUNTER_BYTES].zero_()
@@ -613,65 +626,61 @@ class PagedKV:
             ws = self._ws[stream] = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
         return ws
 
-    def _rows(self, t, name, width, dtype=None):
-        """A 2-D or 3-D CUDA tensor whose rows are `width` contiguous values: (rows, row stride)."""
-        if not (t.is_cuda and t.device == self.device and t.dim() in (2, 3) and (dtype is None or t.dtype == dtype)):
-            raise ValueError(f"{name}: a CUDA tensor of rows on {self.device} is expected")
-        n = t.shape[0]
-        inner = t.shape[1] if t.dim() == 2 else t.shape[1] * t.shape[2]
-        dense = t.stride(-1) == 1 and (t.dim() == 2 or t.shape[1] == 1 or t.stride(1) == t.shape[2])
-        if inner != width or not dense:
+    def _rows(self, t, name, heads, dtype=None):
+        """A 2-D or 3-D CUDA tensor whose rows are heads * 128 contiguous values: (type, rows, row stride)."""
+        shape, stride, width = t.shape, t.stride(), heads * 128
+        if t.get_device() != self._dev or (dtype is not None and t.dtype is not dtype):
+            raise ValueError(f"{name}: a tensor of the activations' type on {self.device} is expected")
+        n = len(shape)
+        if not ((n == 3 and shape[1] == heads and shape[2] == 128 and stride[2] == 1 and (heads == 1 or stride[1] == 128))
+                or (n == 2 and shape[1] == width and stride[1] == 1)):
             raise ValueError(f"{name}: rows of {width} contiguous values are expected")
-        return n, (t.stride(0) if n > 1 else width)
+        return shape[0], (stride[0] if shape[0] > 1 else width)
+
+    def _act(self, t):
+        c = self._c.get(t.dtype)
+        if c is None:
+            raise ValueError(f"float32 or bfloat16 expected, not {t.dtype}")
+        return c[1]
+
+    def _out(self, out, n, like):
+        import torch
+        if out is None:
+            return torch.empty((n, self.nq, 128), dtype=like.dtype, device=self.device), self.nq * 128
+        rows, ld = self._rows(out, "out", self.nq, like.dtype)
+        if rows != n:
+            raise ValueError("out: one row for each row given is expected")
+        return out, ld
 
     def append(self, qkv, seq, pos, rope, q_norm=None, k_norm=None, eps=1e-6, out=None):
         """Norms and turns the q and k heads of qkv [n, (nq + 2 nkv) * 128], stores keys and values at positions
         `pos` of sequences `seq` (int32 [n]; a position < 0 skips its row) and returns the queries [n, nq, 128].
         rope: float32 [rows, 64, 2], cosine and sine of each pair at each position."""
-        import torch
-        n, ld = self._rows(qkv, "qkv", (self.nq + 2 * self.nkv) * 128)
-        c = self._c[_dtype_code(qkv)]
-        dev = self.device
-        if out is None:
-            out = torch.empty((n, self.nq, 128), dtype=qkv.dtype, device=dev)
-        no, ldo = self._rows(out, "out", self.nq * 128, qkv.dtype)
-        if no != n:
-            raise ValueError("out: one row for each token is expected")
-        rows = rope.shape[0]
-        args = (_need(seq, "seq", torch.int32, (n,), dev), _need(pos, "pos", torch.int32, (n,), dev),
-                None if q_norm is None else _need(q_norm, "q_norm", torch.float32, (128,), dev),
-                None if k_norm is None else _need(k_norm, "k_norm", torch.float32, (128,), dev), eps,
-                _need(rope, "rope", torch.float32, (rows, 64, 2), dev))
-        with _on_device(dev.index):
-            rc = lib().q3paged_append(ctypes.addressof(c), n, qkv.data_ptr(), ld, *args, rows, out.data_ptr(), ldo,
-                                      self.err.data_ptr(), torch.cuda.current_stream().cuda_stream)
-        if rc:
-            _paged_raise(rc)
+        from torch import float32, int32
+        c = self._act(qkv)
+        n, ld = self._rows(qkv, "qkv", self.nq + 2 * self.nkv)
+        out, ldo = self._out(out, n, qkv)
+        dev, rows = self._dev, rope.shape[0]
+        _on_stream(dev, lambda stream: self._lib.q3paged_append(
+            c, n, qkv.data_ptr(), ld, _need(seq, "seq", int32, (n,), dev), _need(pos, "pos", int32, (n,), dev),
+            None if q_norm is None else _need(q_norm, "q_norm", float32, (128,), dev),
+            None if k_norm is None else _need(k_norm, "k_norm", float32, (128,), dev), eps,
+            _need(rope, "rope", float32, (rows, 64, 2), dev), rows, out.data_ptr(), ldo, self._err, stream))
         return out
 
     def attend(self, q, q_off, ctx_len, max_q: int, scale=128 ** -0.5, out=None):
         """Causal attention of the newest tokens of every sequence: rows q_off[s]..q_off[s+1]-1 of q [n, nq, 128]
         are the last ones of sequence s, which has ctx_len[s] positions (int32 tensors); max_q bounds the new
         tokens of a sequence.  Returns [n, nq, 128]."""
-        import torch
-        n, ld = self._rows(q, "q", self.nq * 128)
-        c = self._c[_dtype_code(q)]
-        dev = self.device
-        if out is None:
-            out = torch.empty((n, self.nq, 128), dtype=q.dtype, device=dev)
-        no, ldo = self._rows(out, "out", self.nq * 128, q.dtype)
-        if no != n:
-            raise ValueError("out: one row for each row of q is expected")
-        off = _need(q_off, "q_off", torch.int32, (c.n_seqs + 1,), dev)
-        ctx = _need(ctx_len, "ctx_len", torch.int32, (c.n_seqs,), dev)
-        with _on_device(dev.index):
-            stream = torch.cuda.current_stream().cuda_stream
-            ws = self._workspace(stream)
-            rc = lib().q3paged_attention(ctypes.addressof(c), n, max_q, q.data_ptr(), ld, off, ctx, scale,
-                                         out.data_ptr(), ldo, ws.data_ptr(), self.ws_bytes, self.err.data_ptr(),
-                                         stream)
-        if rc:
-            _paged_raise(rc)
+        from torch import int32
+        c = self._act(q)
+        n, ld = self._rows(q, "q", self.nq)
+        out, ldo = self._out(out, n, q)
+        off = _need(q_off, "q_off", int32, self._q_off_shape, self._dev)
+        ctx = _need(ctx_len, "ctx_len", int32, self._ctx_shape, self._dev)
+        _on_stream(self._dev, lambda stream: self._lib.q3paged_attention(
+            c, n, max_q, q.data_ptr(), ld, off, ctx, scale, out.data_ptr(), ldo, self._workspace(stream).data_ptr(),
+            self.ws_bytes, self._err, stream))
         return out
 
     def check(self):
@@ -693,21 +702,17 @@ def sample_given(logits, u, temperature, top_k, top_p, min_p, ids=None, logprob=
     if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2 and
             (logits.shape[1] <= 1 or logits.stride(1) == 1)):
         raise ValueError("logits: a CUDA tensor [n, vocab] with contiguous rows is expected")
-    n, vocab = logits.shape
-    dev, code = logits.device, _dtype_code(logits)
+    (n, vocab), dev, f = logits.shape, logits.get_device(), torch.float32
     if ids is None:
-        ids = torch.empty(n, dtype=torch.int32, device=dev)
+        ids = torch.empty(n, dtype=torch.int32, device=logits.device)
     if logprob is None:
-        logprob = torch.empty(n, dtype=torch.float32, device=dev)
-    f = torch.float32
-    args = (_need(u, "u", f, (n,), dev), _need(temperature, "temperature", f, (n,), dev),
-            _need(top_k, "top_k", torch.int32, (n,), dev), _need(top_p, "top_p", f, (n,), dev),
-            _need(min_p, "min_p", f, (n,), dev), _need(ids, "ids", torch.int32, (n,), dev),
-            _need(logprob, "logprob", f, (n,), dev),
+        logprob = torch.empty(n, dtype=f, device=logits.device)
+    shape = (n,)
+    args = (_need(u, "u", f, shape, dev), _need(temperature, "temperature", f, shape, dev),
+            _need(top_k, "top_k", torch.int32, shape, dev), _need(top_p, "top_p", f, shape, dev),
+            _need(min_p, "min_p", f, shape, dev), _need(ids, "ids", torch.int32, shape, dev),
+            _need(logprob, "logprob", f, shape, dev),
             None if err is None else _need(err, "err", torch.int32, (1,), dev))
-    with _on_device(dev.index):
-        rc = lib().q3tts_sample_given(n, vocab, logits.data_ptr(), code, logits.stride(0) if n > 1 else vocab, *args,
-                                      torch.cuda.current_stream().cuda_stream)
-    if rc:
-        _paged_raise(rc)
+    _on_stream(dev, lambda stream: lib().q3tts_sample_given(
+        n, vocab, logits.data_ptr(), _dtype_code(logits), logits.stride(0) if n > 1 else vocab, *args, stream))
     return ids, logprob

@@ -183,7 +183,7 @@ struct Seg {
 
 struct Walk {
     PagedSeq q;
-    long long u, item0;   // unit to begin at, first unit of the item
+    int u, item0;         // unit to begin at, first unit of the item
     int s, h, item, nu;   // nu: units of the item
     bool more;
 };
@@ -218,9 +218,9 @@ __device__ __forceinline__ void walk_begin(Walk& w, const PagedAttn& a, const Pa
     w.s = R.s;
     w.q = R.q;
     w.more = true;
-    const long long per = seq_units(w.q, tpi);
-    long long rel = R.u0 - R.start;
-    w.h = (int)(rel / per);
+    const int per = (int)seq_units(w.q, tpi);
+    int rel = R.u0 - R.start;
+    w.h = rel / per;
     rel -= w.h * per;
     w.item0 = R.start + w.h * per;
     w.item = 0;
@@ -236,15 +236,15 @@ __device__ __forceinline__ void walk_begin(Walk& w, const PagedAttn& a, const Pa
 }
 // the part of the walk's item that this CTA takes
 __device__ __forceinline__ bool walk_seg(Walk& w, const PagedRange& R, int tpt, int tpi, Seg& g) {
-    long long end;
+    int end;
     if (!w.more || !paged_cut(R, w.item0, w.item0 + w.nu, &end)) return false;
     g.s = w.s;
     g.h = w.h;
     g.tok0 = w.item * tpi;
     g.ntok = min(tpi, w.q.n_new - g.tok0);
     g.two = g.ntok > tpt;
-    g.kt0 = (int)(w.u - w.item0);
-    g.n = (int)(end - w.u);
+    g.kt0 = w.u - w.item0;
+    g.n = end - w.u;
     if (w.q.ctx - w.q.n_new + g.tok0 + g.ntok <= 0 || w.q.ctx <= 0) g.n = 0;
     g.whole = w.u == w.item0 && end == w.item0 + w.nu;
     g.ca = paged_cut_first(R, w.item0);

@@ -31,7 +31,7 @@ namespace {
 constexpr int DW = 4;             // warps of a CTA
 constexpr int DU = 64;            // keys of a unit
 constexpr int d_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of an SM (registers)
-constexpr int D_MIN_UNITS = 2;
+constexpr int D_MIN_UNITS = 1;
 
 __device__ __forceinline__ uint4 ldg16(const bf16* p, bool ok) {
     uint4 r;
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
     int s = R.s;
     PagedSeq q = R.q;
     int nu = max(1, (q.ctx + DU - 1) / DU), groups = (q.n_new * c.G + RG - 1) / RG;   // units and row groups of a head
-    int item = (int)((R.u0 - R.start) / nu);                                          // head * groups + row group
-    long long item0 = R.start + (long long)item * nu;                                 // the item's units [item0, item0 + nu)
+    int item = (R.u0 - R.start) / nu;       // head * groups + row group
+    int item0 = R.start + item * nu;        // the item's units [item0, item0 + nu)
     auto next_item = [&]() -> bool {
         item0 += nu;
         if (++item < c.nkv * groups) return true;
@@ -114,11 +114,11 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
         item = 0;
         return true;
     };
-    long long u = paged_begin(R, item0, item0 + nu), seg_end;
+    int u = paged_begin(R, item0, item0 + nu), seg_end;
     if (u == item0 + nu && !next_item()) return;
     while (paged_cut(R, item0, item0 + nu, &seg_end)) {
         const int h = item / groups, rg = item - h * groups;
-        const int key0 = (int)(u - item0) * DU, key1 = min(q.ctx, (int)(seg_end - item0) * DU);
+        const int key0 = (u - item0) * DU, key1 = (int)min((long long)q.ctx, (long long)(seg_end - item0) * DU);
         const int rows = min(RG, q.n_new * c.G - rg * RG);
 
         // ---- blocks of 16 keys: lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9

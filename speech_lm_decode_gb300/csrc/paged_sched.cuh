@@ -36,22 +36,26 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttn& a, int s, bool re
 }
 
 struct PagedRange {
-    long long W;        // units of the call
-    long long u0, u1;   // this CTA's
-    long long snap;     // cuts so near to an item's end move to it
-    long long start;    // first unit of the sequence of u0
+    int W;              // units of the call (0: nothing to do)
+    int P;              // CTAs that share them: the first `extra` take quota + 1, the others quota
+    int quota, extra;
+    int u0, u1;         // this CTA's
+    int snap;           // cuts so near to an item's end move to it
+    int start;          // first unit of the sequence of u0
     int s;              // that sequence
     PagedSeq q;
-    int P;              // CTAs that share the units
 };
 
 // first unit of CTA c, and the CTA that owns unit u
-__device__ __forceinline__ long long paged_first(long long W, int P, int c) { return W * c / P; }
-__device__ __forceinline__ int paged_owner(long long W, int P, long long u) { return (int)(((u + 1) * P - 1) / W); }
+__device__ __forceinline__ int paged_first(const PagedRange& r, int c) { return c * r.quota + min(c, r.extra); }
+__device__ __forceinline__ int paged_owner(const PagedRange& r, int u) {
+    const int big = r.extra * (r.quota + 1);
+    return u < big ? u / (r.quota + 1) : r.extra + (u - big) / r.quota;
+}
 
 // The part of item [a, b) that a CTA takes, having come to unit `from` of it;
 // false: none, its share ends in front of the item.
-__device__ __forceinline__ bool paged_cut(const PagedRange& r, long long a, long long b, long long* end) {
+__device__ __forceinline__ bool paged_cut(const PagedRange& r, int a, int b, int* end) {
     if (r.u1 <= a) return false;
     *end = b;
     if (r.u1 >= b) return true;
@@ -60,20 +64,19 @@ __device__ __forceinline__ bool paged_cut(const PagedRange& r, long long a, long
     return true;
 }
 // Where a CTA whose share begins inside item [a, b) starts: a, u0, or b (the next item).
-__device__ __forceinline__ long long paged_begin(const PagedRange& r, long long a, long long b) {
+__device__ __forceinline__ int paged_begin(const PagedRange& r, int a, int b) {
     return r.u0 - a <= r.snap ? a : b - r.u0 <= r.snap ? b : r.u0;
 }
 // first and last CTA of a cut item
-__device__ __forceinline__ int paged_cut_first(const PagedRange& r, long long a) { return paged_owner(r.W, r.P, a + r.snap); }
-__device__ __forceinline__ int paged_cut_last(const PagedRange& r, long long b) { return paged_owner(r.W, r.P, b - r.snap - 1); }
+__device__ __forceinline__ int paged_cut_first(const PagedRange& r, int a) { return paged_owner(r, a + r.snap); }
+__device__ __forceinline__ int paged_cut_last(const PagedRange& r, int b) { return paged_owner(r, b - r.snap - 1); }
 
 // This CTA's range.  units(q): units of a sequence, all kv heads.  NT threads
 // call it; min_units: units that a CTA gets at least (fewer CTAs then work).
 template <int NT, class F>
 __device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int min_units, F units) {
     __shared__ long long warp_sum_s[NT / 32];
-    __shared__ long long found_start;
-    __shared__ int found_s;
+    __shared__ int found_start, found_s;
     __shared__ PagedSeq found_q;
     const int n_seqs = a.c.n_seqs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -100,18 +103,25 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int
         W += warp_sum_s[w];
     }
     PagedRange r;
-    r.W = W;
-    r.P = (int)min((long long)P, max(1LL, W / min_units));
+    if (W > 0x7fff0000LL) {   // more than 2^31 units (tens of terabytes of keys): not served
+        if (tid == 0 && blockIdx.x == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
+        W = 0;
+    }
+    r.W = (int)W;
+    r.P = min(P, max(1, r.W / min_units));
+    r.quota = r.W / r.P;
+    r.extra = r.W - r.quota * r.P;
+    r.snap = min(r.quota / 4, 2);
     const int c = blockIdx.x;
-    r.u0 = c < r.P ? paged_first(W, r.P, c) : W;
-    r.u1 = c < r.P ? paged_first(W, r.P, c + 1) : W;
-    long long start = before + incl - mine;
+    r.u0 = c < r.P ? paged_first(r, c) : r.W;
+    r.u1 = c < r.P ? paged_first(r, c + 1) : r.W;
+    int start = (int)(before + incl - mine);
     if (r.u0 < r.u1 && start <= r.u0 && r.u0 < start + mine) {
         int s = s0;
         if (s1 - s0 > 1) {
             for (;; ++s) {
                 q = paged_seq(a, s, false);
-                const long long n = units(q);
+                const int n = (int)units(q);
                 if (r.u0 < start + n) break;
                 start += n;
             }
@@ -124,7 +134,6 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int
     r.s = found_s;
     r.start = found_start;
     r.q = found_q;
-    r.snap = min(W / r.P / 4, 2LL);
     return r;
 }
 

@@ -38,11 +38,12 @@ using u64 = unsigned long long;
 constexpr int GT = 512, GW = GT / 32;   // threads, warps of a CTA
 constexpr int GIVEN_MAX_VOCAB = 262144; // whole weights of a row stay below 2^58
 constexpr int MAX_CLUSTER = 8;
-constexpr int LIST = 1024;              // entries of the candidate lists
+constexpr int LIST = 512;               // entries of the candidate lists
 constexpr int SMALL_K = 128;            // top-k that the list path takes
 constexpr int GROUPS = 512;             // group maxima of a row
-constexpr int BINS = 656;               // 41 octaves of 16 bins: e from 2^-41 to 1
-constexpr uint32_t BIN0 = (127u - 40u) << 4;   // bits >> 19 of 2^-40
+constexpr int BINS = 41 * 64;           // 64 bins an octave: e from 2^-40 to 2
+constexpr int COARSE = BINS / 16;
+constexpr uint32_t BIN0 = (127u - 40u) << 6;   // bits >> 17 of 2^-40
 
 __device__ __forceinline__ float lval(const float* p, int i) { return p[i]; }
 __device__ __forceinline__ float lval(const bf16* p, int i) { return __bfloat162float(p[i]); }
@@ -103,18 +104,21 @@ struct Quotient {
 };
 
 struct GivenSmem {
-    u64 hist64[2][256];          // radix passes, in turn
     u64 wsum[GW];                // kept weight of each warp's ids
     u64 red[GW + 1];
     u64 best;                    // largest (order key, ~id) of the slice
-    u64 total, above;            // weight of the slice; of it above the bracket
-    uint32_t hist[BINS];         // sums of mantissas, by e
+    u64 total, above, kept;      // weight of the slice; of it above the bracket; kept
+    uint32_t hist[BINS];         // sums of mantissas by e, or counts by max - l, from the top
+    uint32_t coarse[COARSE];     // of 16 bins each
     uint32_t maxima[GROUPS];     // first CTA: group maxima of the row
-    alignas(16) uint32_t mine[GROUPS];   // a copy of them
+    uint32_t radix[2][3 * 256];  // radix passes, in turn
     uint32_t lkey[LIST], skey[LIST];
     int lid[LIST], sid[LIST];
-    int n_list, bad, pick;
+    float le[LIST], se[LIST];
+    unsigned char keep[LIST];
+    int n_list, pick;
     u64 pick64;
+    double logz;
     int edge_bin;
 };
 
@@ -156,6 +160,18 @@ __device__ u64 cta_scan64(GivenSmem& s, u64 v) {
     return v;
 }
 
+// *p of every CTA of the cluster, all loads in flight at once: f(rank, value)
+template <class P, class F>
+__device__ __forceinline__ void from_all(cg::cluster_group& cl, int C, P* p, F f) {
+    P v[MAX_CLUSTER];
+#pragma unroll
+    for (int r = 0; r < MAX_CLUSTER; ++r)
+        if (r < C) v[r] = *cl.map_shared_rank(p, r);
+#pragma unroll
+    for (int r = 0; r < MAX_CLUSTER; ++r)
+        if (r < C) f(r, v[r]);
+}
+
 // One row's state that all its functions use.
 template <typename T>
 struct Row {
@@ -172,22 +188,34 @@ struct Row {
 
     // Radix selection over (key, amount) pairs that each(f) walks on every CTA: the key at which the amounts from
     // the top, starting with `above`, reach the goal; reach(sum) says whether a sum does.  Returns whether there
-    // is one; then *above is the amount above that key.  All threads of the cluster call it.
+    // is one; then *above is the amount above that key.  All threads of the cluster call it.  Amounts (up to
+    // 2^41) are added in three parts of 14 bits, as 32-bit atomics are the native ones: 2^15 entries a slice fit.
     template <class Each, class Reach>
     __device__ bool select(Each each, Reach reach, int bits, uint32_t* key, u64* above) {
         uint32_t prefix = 0, mask = 0;
         for (int shift = bits - 8, pass = 0; shift >= 0; shift -= 8, ++pass) {
-            u64* h = s.hist64[pass & 1];
-            if (threadIdx.x < 256) h[threadIdx.x] = 0;
+            uint32_t* h = s.radix[pass & 1];
+            for (int i = threadIdx.x; i < 3 * 256; i += GT) h[i] = 0;
             if (threadIdx.x == 0) s.pick = -1;
             __syncthreads();
             each([&](uint32_t k, u64 amount) {
-                if ((k & mask) == prefix) atomicAdd(&h[(k >> shift) & 255u], amount);
+                if ((k & mask) == prefix) {
+                    uint32_t* d = h + ((k >> shift) & 255u);
+                    atomicAdd(d, (uint32_t)amount & 0x3FFFu);
+                    if (amount >> 14) {
+                        atomicAdd(d + 256, (uint32_t)(amount >> 14) & 0x3FFFu);
+                        atomicAdd(d + 512, (uint32_t)(amount >> 28));
+                    }
+                }
             });
             cl.sync();
             u64 c = 0;
-            if (threadIdx.x < 256)
-                for (int r = 0; r < C; ++r) c += cl.map_shared_rank(h, r)[255 - threadIdx.x];
+            if (threadIdx.x < 256) {
+                uint32_t* d = &h[255 - threadIdx.x];
+                from_all(cl, C, d, [&](int, uint32_t v) { c += v; });
+                from_all(cl, C, d + 256, [&](int, uint32_t v) { c += (u64)v << 14; });
+                from_all(cl, C, d + 512, [&](int, uint32_t v) { c += (u64)v << 28; });
+            }
             const u64 incl = cta_scan64(s, c);
             if (threadIdx.x < 256 && !reach(*above + incl - c) && reach(*above + incl)) {
                 s.pick = 255 - threadIdx.x;
@@ -203,6 +231,71 @@ struct Row {
         }
         *key = prefix;
         return true;
+    }
+
+    // The bin of the cluster's histograms in which the running sum of weigh(entry, bin) passes the goal (into
+    // s.edge_bin, -1: none) and the sum in front of it (s.pick64).  All threads of the cluster call it.
+    template <class Weigh, class Reach>
+    __device__ void locate(Weigh weigh, Reach reach) {
+        const int t = threadIdx.x;
+        __syncthreads();
+        if (t < COARSE) {
+            uint32_t c = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) c += s.hist[t * 16 + ((i + t) & 15)];
+            s.coarse[t] = c;
+        }
+        if (t == 0) { s.pick = -1; s.edge_bin = -1; }
+        cl.sync();
+        u64 c = 0;
+        if (t < COARSE) from_all(cl, C, &s.coarse[t], [&](int, uint32_t v) { c += weigh(v, t * 16); });
+        u64 incl = cta_scan64(s, c);
+        if (t < COARSE && !reach(incl - c) && reach(incl)) { s.pick = t; s.pick64 = incl - c; }
+        __syncthreads();
+        if (s.pick >= 0 && t < 32) {
+            const int b = s.pick * 16 + (t & 15);
+            c = 0;
+            from_all(cl, C, &s.hist[b], [&](int, uint32_t v) { c += weigh(v, b); });
+            if (t >= 16) c = 0;
+            const u64 front = s.pick64;
+            incl = warp_scan64(c) + front;
+            __syncwarp();
+            if (t < 16 && !reach(incl - c) && reach(incl)) { s.edge_bin = b; s.pick64 = incl - c; }
+        }
+        __syncthreads();
+    }
+
+    // Adds an entry to this CTA's list; one that finds no place is only counted.
+    __device__ void push(uint32_t key, int id, float ev) {
+        const int n = atomicAdd(&s.n_list, 1);
+        if (n < LIST) { s.lkey[n] = key; s.lid[n] = id; s.le[n] = ev; }
+    }
+    // The lists of all CTAs, by rank, into skey / sid / se of each; *own: where this CTA's begins.  Returns their
+    // length, or -1 if it is more than LIST.  All threads of the cluster call it.
+    __device__ int merge(int* own) {
+        cl.sync();
+        int n[MAX_CLUSTER], total = 0;
+        *own = 0;
+        from_all(cl, C, &s.n_list, [&](int r, int v) {
+            n[r] = v;
+            if (r < rank) *own += v;
+            total += v;
+        });
+        if (total > LIST) return -1;
+        int off = 0;
+#pragma unroll
+        for (int r = 0; r < MAX_CLUSTER; ++r)
+            if (r < C) {
+                GivenSmem* o = cl.map_shared_rank(&s, r);
+                for (int i = threadIdx.x; i < n[r]; i += GT) {
+                    s.skey[off + i] = o->lkey[i];
+                    s.sid[off + i] = o->lid[i];
+                    s.se[off + i] = o->le[i];
+                }
+                off += n[r];
+            }
+        __syncthreads();
+        return total;
     }
 };
 
@@ -276,18 +369,16 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         if (tid == 0) {
             best = s.red[0];
             for (int w = 1; w < GW; ++w) best = s.red[w] > best ? s.red[w] : best;
-            s.best = best;
-            s.bad = bad;
+            s.best = bad ? ~0ull : best;   // (a key of +inf or NaN)
         }
     }
     cl.sync();
     u64 best = 0;
     bad = 0;
-    for (int r = 0; r < C; ++r) {
-        const u64 b = *cl.map_shared_rank(&s.best, r);
+    from_all(cl, C, &s.best, [&](int, u64 b) {
+        bad |= b == ~0ull;
         best = b > best ? b : best;
-        bad |= *cl.map_shared_rank(&s.bad, r);
-    }
+    });
     const float m = R.m = order_key_inv((uint32_t)(best >> 32));
     const int first = R.first = (int)~(uint32_t)best;
     const bool fails = bad || m == -INFINITY;
@@ -311,24 +402,16 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         if (logprob) logprob[row] = (float)((double)__fsub_rn(l, m) - log((double)Z * 0x1p-40));
     };
 
-    // ---- small k: the list path
+    // ---- small k: the list path (its list is the first CTA's alone)
     const bool with_k = k > 0 && k < V;
     if (with_k && k <= SMALL_K) {
-        s.mine[tid] = cl.map_shared_rank(s.maxima, 0)[tid];
-        if (tid == 0) s.pick = 0;
-        __syncthreads();
-        {
-            const uint32_t v = s.mine[tid];
-            int ge = 0;
-#pragma unroll 8
-            for (int j = 0; j < GROUPS; j += 4) {
-                const uint4 o = *(const uint4*)&s.mine[j];
-                ge += (o.x >= v) + (o.y >= v) + (o.z >= v) + (o.w >= v);
-            }
-            if (ge >= k) atomicMax((unsigned*)&s.pick, v);
-        }
-        __syncthreads();
-        const float tau = order_key_inv((uint32_t)s.pick);   // at least k values reach it
+        // the k-th largest group maximum, rounded down to 16 bits of its key: at least k values reach it
+        const uint32_t v = cl.map_shared_rank(s.maxima, 0)[tid];
+        uint32_t tk = 0;
+#pragma unroll 1
+        for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
+            if (__syncthreads_count(v >= (tk | bit)) >= k) tk |= bit;
+        const float tau = tk < 0x00800000u ? -INFINITY : order_key_inv(tk);
         GivenSmem* lead = cl.map_shared_rank(&s, 0);
         for (int i = w0 + lane * 4; i < w0 + seg; i += 128) {
             const float4 v = *(const float4*)(e + i);
@@ -346,12 +429,19 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         const int n = *cl.map_shared_rank(&s.n_list, 0);
         if (n <= LIST) {
             if (rank == 0) {
-                // sorted by (l descending, id ascending)
-                for (int i = tid; i < n; i += GT) {
+                // sorted by (l descending, id ascending): eight threads count an entry's rank
+                for (int i0 = 0; i0 < n; i0 += GT / 8) {
+                    const int i = min(i0 + tid / 8, n - 1);
                     const uint32_t a = s.lkey[i];
                     const int id = s.lid[i];
                     int r = 0;
-                    for (int j = 0; j < n; ++j) r += s.lkey[j] > a || (s.lkey[j] == a && s.lid[j] < id);
+                    for (int j = tid & 7; j < n; j += 8) {
+                        const uint32_t o = s.lkey[j];
+                        r += o > a || (o == a && s.lid[j] < id);
+                    }
+                    r += __shfl_xor_sync(0xffffffffu, r, 1);
+                    r += __shfl_xor_sync(0xffffffffu, r, 2);
+                    r += __shfl_xor_sync(0xffffffffu, r, 4);
                     s.skey[r] = a;
                     s.sid[r] = id;
                 }
@@ -372,48 +462,89 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
                 const u64 Z = cta_sum64(s, own);
                 const double limit = __dmul_rn((double)top_p, (double)Z);
                 u64 kept = 0;
-                u64* wk = reinterpret_cast<u64*>(e);   // the slice (2048 floats at least) is not needed any more
+                u64* wk = reinterpret_cast<u64*>(e);   // the slice (2 LIST floats at least) is not needed any more
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
                     const int i = tid * PER + j;
                     const bool in = ex[j] >= 0.f && (i == 0 || ((top_p >= 1.f || (double)before < limit) && ex[j] >= min_p));
                     before += w[j];
-                    if (!in) w[j] = 0;
-                    kept += w[j];
-                    if (i < n) wk[i] = w[j];
+                    if (in) kept += w[j];
+                    if (i < n) wk[i] = in ? w[j] : 0ull;
                 }
                 const u64 Zk = cta_sum64(s, kept);
                 const u64 target = target_of(Zk);
-                if (tid == 0) s.pick = 0x7fffffff;
+                if (tid == 0) { s.pick = 0x7fffffff; s.pick64 = 0; }
+                if (tid == GT - 1) s.logz = log((double)Zk * 0x1p-40);
                 __syncthreads();
-                // ids are few: the weight up to an id is summed for each of them
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const int i = tid * PER + j;
-                    if (i >= n || w[j] == 0) continue;
+                // the weight up to an id is summed for each of the few ids, by eight threads
+                for (int i0 = 0; i0 < n && s.skey[i0] >= kth; i0 += GT / 8) {
+                    const int i = min(i0 + tid / 8, n - 1), id = s.sid[i];
                     u64 upto = 0;
-                    for (int o = 0; o < n && s.skey[o] >= kth; ++o)
-                        if (s.sid[o] <= s.sid[i]) upto += wk[o];
-                    if (upto > target) atomicMin(&s.pick, s.sid[i]);
+                    for (int o = tid & 7; o < n && s.skey[o] >= kth; o += 8)
+                        if (s.sid[o] <= id) upto += wk[o];
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) upto += __shfl_xor_sync(0xffffffffu, upto, o);
+                    // (id, place in the order): LIST places
+                    if (s.skey[i] >= kth && wk[i] && upto > target) atomicMin(&s.pick, id * LIST + i);
                 }
                 __syncthreads();
-                if (tid == 0) finish(s.pick, R.l_of(s.pick), Zk);
+                if (tid == 0) {
+                    ids[row] = s.pick / LIST;
+                    if (logprob)
+                        logprob[row] = (float)((double)__fsub_rn(order_key_inv(s.skey[s.pick % LIST]), m) - s.logz);
+                }
             }
             cl.sync();
             return;
         }
+        cl.sync();   // everyone knows that the list overflowed
     }
 
-    // ---- the k-th largest value
+    // ---- the k-th largest value: a histogram of max - l says in which bin it lies, a list of that bin which it is
     float kth = -INFINITY;
     if (with_k) {
-        uint32_t key = 0;
-        u64 above = 0;
-        R.select([&](auto f) {
-            for (int i = w0 + lane; i < w0 + seg; i += 32)
-                if (base + i < V) f(order_key(e[i]), 1ull);
-        }, [&](u64 n) { return n >= (u64)k; }, 32, &key, &above);
-        kth = order_key_inv(key);
+        auto bin_of = [&](float l) { return min((int)__fmul_rn(__fsub_rn(m, l), 93.f), BINS - 1); };
+        for (int i = tid; i < BINS; i += GT) s.hist[i] = 0;
+        if (tid == 0) s.n_list = 0;
+        __syncthreads();
+        for (int i = w0 + lane; i < w0 + seg; i += 32)
+            if (base + i < V) atomicAdd(&s.hist[bin_of(e[i])], 1u);
+        R.locate([](uint32_t v, int) { return (u64)v; }, [&](u64 c) { return c >= (u64)k; });
+        const int b = s.edge_bin;
+        u64 above = s.pick64;
+        for (int i = w0 + lane; i < w0 + seg; i += 32)
+            if (base + i < V && bin_of(e[i]) == b) R.push(order_key(e[i]), base + i, 0.f);
+        int own;
+        const int n = R.merge(&own);
+        if (n >= 0) {
+            // the value with fewer than k above it and at least k down to it
+            for (int i0 = 0; i0 < n; i0 += GT / 8) {
+                const int i = min(i0 + tid / 8, n - 1);
+                const uint32_t a = s.skey[i];
+                int gt = 0, ge = 0;
+                for (int j = tid & 7; j < n; j += 8) {
+                    const uint32_t o = s.skey[j];
+                    gt += o > a;
+                    ge += o >= a;
+                }
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    gt += __shfl_xor_sync(0xffffffffu, gt, o);
+                    ge += __shfl_xor_sync(0xffffffffu, ge, o);
+                }
+                if ((int)above + gt < k && (int)above + ge >= k) s.pick = (int)a;
+            }
+            __syncthreads();
+            kth = order_key_inv((uint32_t)s.pick);
+        } else {
+            uint32_t key = 0;
+            R.select([&](auto f) {
+                for (int i = w0 + lane; i < w0 + seg; i += 32)
+                    if (base + i < V && bin_of(e[i]) == b) f(order_key(e[i]), 1ull);
+            }, [&](u64 c) { return c >= (u64)k; }, 32, &key, &above);
+            kth = order_key_inv(key);
+        }
+        cl.sync();   // lists and histograms have been read
     }
 
     // ---- e in place of l; weights, and their histogram where top-p needs it
@@ -434,7 +565,8 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             if (with_p) {
                 const uint32_t b = __float_as_uint(a[j]);
                 // 16 bits of the mantissa: at most 2^15 logits a slice, so 32 bits hold their sum
-                if (b >= BIN0 << 19) atomicAdd(&s.hist[(b >> 19) - BIN0], ((b & 0x7FFFFFu) | 0x800000u) >> 8);
+                if (b >= BIN0 << 17)
+                    atomicAdd(&s.hist[BINS - 1 + BIN0 - (b >> 17)], ((b & 0x7FFFFFu) | 0x800000u) >> 8);
             }
         }
         *(float4*)(e + i) = make_float4(a[0], a[1], a[2], a[3]);
@@ -447,99 +579,126 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         if (tid == 0) s.total = sum;
         cl.sync();
         u64 Z = 0;
-        for (int r = 0; r < C; ++r) Z += *cl.map_shared_rank(&s.total, r);
+        from_all(cl, C, &s.total, [&](int, u64 v) { Z += v; });
         const double limit = __dmul_rn((double)top_p, (double)Z);
-        // the bin in which the histogram, from the top, passes the limit
-        {
-            if (tid == 0) s.edge_bin = 0;
-            u64 h2[2] = {0, 0};
-            for (int j = 0; j < 2; ++j) {
-                const int b = BINS - 1 - (tid * 2 + j);
-                if (b >= 0) {
-                    for (int r = 0; r < C; ++r) h2[j] += cl.map_shared_rank(s.hist, r)[b];
-                    const int o = (b >> 4) - 15;   // of e's exponent: weights in units of 2^-40
-                    h2[j] = o >= 0 ? h2[j] << o : h2[j] >> -o;
-                }
-            }
-            const u64 incl = cta_scan64(s, h2[0] + h2[1]);
-            const u64 all = cta_sum64(s, h2[0] + h2[1]);
-            const double lim = (double)top_p * (double)all;
-            u64 c = incl - h2[0] - h2[1];
-            for (int j = 0; j < 2; ++j) {
-                if ((double)c < lim && (double)(c + h2[j]) >= lim) s.edge_bin = BINS - 1 - (tid * 2 + j);
-                c += h2[j];
-            }
-            __syncthreads();
-        }
+        // the bin in which the histogram, from the top, passes the limit (in units of 2^-40)
+        R.locate([](uint32_t v, int i) {
+            const int o = ((BINS - 1 - i) >> 6) - 15;   // of e's exponent
+            return o >= 0 ? (u64)v << o : (u64)v >> -o;
+        }, [&](u64 c) { return !((double)c < limit); });
+        // What lies above that bin is added up, what lies in it listed, and each listed entry finds the weight in
+        // front of it (attempt 0); a bin with too many entries is searched by radix (1).  e is monotone in l up to
+        // rounding only, so the border has to lie clearly inside the bin; else its neighbours (2) or all entries (3)
+        // are searched.
         float hi;
-        uint32_t edge = 0;
-        u64 above = 0;
         bool found = false;
-        auto inside = [&](float v) { return v >= lo && v < hi; };
-        auto each_inside = [&](auto f) {   // f(entry of the slice) for what lies in the bracket
-            if (s.n_list <= LIST) {
-                for (int i = tid; i < s.n_list; i += GT) f(s.lid[i]);
-            } else {
-                for (int i = w0 + lane; i < w0 + seg; i += 32)
-                    if (base + i < V && inside(e[i])) f(i);
-            }
-        };
-        for (int attempt = 0; attempt < 2 && !found; ++attempt) {
-            const int b = s.edge_bin;
-            lo = attempt || b <= 1 ? 0.f : __uint_as_float((uint32_t)(b - 1 + BIN0) << 19);
-            hi = attempt ? 2.f : __uint_as_float((uint32_t)(b + 2 + BIN0) << 19);
-            __syncthreads();
-            if (tid == 0) s.n_list = 0;
-            __syncthreads();
-            sum = kept = 0;
-            for (int i = w0 + lane * 4; i < w0 + seg; i += 128) {
-                const float4 v = *(const float4*)(e + i);
-                const float a[4] = {v.x, v.y, v.z, v.w};
+        const int edge_bin = s.edge_bin < 0 ? 0 : BINS - 1 - s.edge_bin;
+        for (int attempt = 0; attempt < 4 && !found;) {
+            const int wide = attempt == 2, b0 = edge_bin - wide, b1 = edge_bin + 1 + wide;
+            lo = attempt == 3 || b0 <= 0 ? 0.f : __uint_as_float((uint32_t)(b0 + BIN0) << 17);
+            hi = attempt == 3 ? 2.f : __uint_as_float((uint32_t)(b1 + BIN0) << 17);
+            auto inside = [&](float v) { return v >= lo && v < hi; };
+            auto clear = [&](float v) {    // of a border at e = v (exp_of is within 2^-20)
+                return (lo == 0.f || v > lo * 1.000002f) && (hi > 1.f || v < hi * 0.999998f);
+            };
+            u64 above = 0;
+            if (attempt != 1) {
+                __syncthreads();
+                if (tid == 0) s.n_list = 0;
+                __syncthreads();
+                sum = kept = 0;
+                for (int i = w0 + lane * 4; i < w0 + seg; i += 128) {
+                    const float4 v = *(const float4*)(e + i);
+                    const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (a[j] >= hi) {
-                        const u64 w = weight_of(a[j]);
-                        sum += w;
-                        if (a[j] >= min_p) kept += w;
-                    } else if (a[j] >= lo && base + i + j < V) {
-                        const int n = atomicAdd(&s.n_list, 1);
-                        if (n < LIST) s.lid[n] = i + j;
+                    for (int j = 0; j < 4; ++j) {
+                        if (a[j] >= hi) {
+                            const u64 w = weight_of(a[j]);
+                            sum += w;
+                            if (a[j] >= min_p) kept += w;
+                        } else if (a[j] >= lo && a[j] > 0.f && attempt == 0) {
+                            R.push(order_key(R.l_of(base + i + j)), base + i + j, a[j]);
+                        }
                     }
                 }
+                kept = warp_sum64(kept);
+                if (lane == 0) s.wsum[warp] = kept;
+                sum = cta_sum64(s, sum);
+                if (tid == 0) s.above = sum;
             }
-            kept = warp_sum64(kept);
-            if (lane == 0) s.wsum[warp] = kept;
-            sum = cta_sum64(s, sum);
-            if (tid == 0) s.above = sum;
-            cl.sync();
-            above = 0;
-            for (int r = 0; r < C; ++r) above += *cl.map_shared_rank(&s.above, r);
-            // (a border above the bracket: nothing to select)
+            int own = 0, n = -1;
+            if (attempt == 0) n = R.merge(&own);
+            else cl.sync();
+            from_all(cl, C, &s.above, [&](int, u64 v) { above += v; });
+            if (attempt == 0 && n < 0) { attempt = 1; cl.sync(); continue; }
+            if (attempt == 0) {
+                // eight threads add up what is in front of an entry of this CTA; the border is the last entry kept
+                // of all, so every CTA looks at every entry for it
+                if (tid == 0) s.pick = 0;     // 1: a border, 2: not clear of the bin's ends
+                __syncthreads();
+                for (int i0 = 0; i0 < n; i0 += GT / 8) {
+                    const int i = min(i0 + tid / 8, n - 1), id = s.sid[i];
+                    const uint32_t a = s.skey[i];
+                    u64 before = 0;
+                    for (int j = tid & 7; j < n; j += 8) {
+                        const uint32_t o = s.skey[j];
+                        if (o > a || (o == a && s.sid[j] < id)) before += weight_of(s.se[j]);
+                    }
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+                    before += above;
+                    const u64 w = weight_of(s.se[i]);
+                    const bool in = (double)before < limit;
+                    if ((tid & 7) == 0 && i0 + tid / 8 < n) {
+                        if (i >= own && i < own + s.n_list) s.keep[i - own] = in;
+                        if (in && !((double)(before + w) < limit)) atomicOr(&s.pick, clear(s.se[i]) ? 1 : 2);
+                    }
+                }
+                __syncthreads();
+                found = s.pick == 1;
+                cl.sync();      // lists, sums and histograms have been read
+                if (!found) { attempt = 2; continue; }
+                // the warp's share of the kept ones
+                kept = 0;
+                for (int i = lane; i < s.n_list; i += 32) {
+                    const int at = s.sid[own + i] - base;
+                    if (at / seg != warp) continue;
+                    if (s.keep[i]) kept += s.se[own + i] >= min_p ? weight_of(s.se[own + i]) : 0ull;
+                    else e[at] = 0.f;
+                }
+                kept = warp_sum64(kept);
+                if (lane == 0) s.wsum[warp] += kept;
+                break;
+            }
+            // by radix: the border's key, then, of the ids there, the lowest ones until the limit
+            auto each_inside = [&](auto f) {
+                for (int i = w0 + lane; i < w0 + seg; i += 32)
+                    if (base + i < V && e[i] > 0.f && inside(e[i])) f(i);
+            };
+            uint32_t edge = 0;
             found = (double)above < limit && R.select([&](auto f) {
-                each_inside([&](int i) { if (e[i] > 0.f) f(order_key(R.l_of(base + i)), weight_of(e[i])); });
-            }, [&](u64 n) { return !((double)n < limit); }, 32, &edge, &above);
-            if (found && !attempt) {
-                // e is monotone in l up to rounding: the border has to lie clearly inside the bracket
-                const float eb = exp_of(__fsub_rn(order_key_inv(edge), m));
-                if (!((lo == 0.f || eb > lo * 1.0001f) && (hi == 2.f || eb < hi * 0.9999f))) found = false;
+                each_inside([&](int i) { f(order_key(R.l_of(base + i)), weight_of(e[i])); });
+            }, [&](u64 c) { return !((double)c < limit); }, 32, &edge, &above);
+            const float eb = exp_of(__fsub_rn(order_key_inv(edge), m));
+            if (found && !clear(eb)) found = false;
+            if (!found) {
+                cl.sync();
+                ++attempt;
+                continue;
             }
-            cl.sync();   // s.above and the histograms have been read
-        }
-        if (found) {
-            // of the ids at the border, the lowest ones until the limit
-            const u64 w = weight_of(exp_of(__fsub_rn(order_key_inv(edge), m)));
-            long long n = (long long)((limit - (double)above) / (double)w);
-            while (n > 0 && !((double)(above + (n - 1) * w) < limit)) --n;
-            while ((double)(above + n * w) < limit) ++n;
+            const u64 w = weight_of(eb);
+            long long n_tie = (long long)((limit - (double)above) / (double)w);
+            while (n_tie > 0 && !((double)(above + (n_tie - 1) * w) < limit)) --n_tie;
+            while ((double)(above + n_tie * w) < limit) ++n_tie;
             u64 ties = 0;
             each_inside([&](int i) { ties += order_key(R.l_of(base + i)) == edge; });
             ties = cta_sum64(s, ties);
             if (tid == 0) s.total = ties;
             cl.sync();
             u64 all = 0;
-            for (int r = 0; r < C; ++r) all += *cl.map_shared_rank(&s.total, r);
+            from_all(cl, C, &s.total, [&](int, u64 v) { all += v; });
             int cut = V;
-            if (n < (long long)all) {
+            if (n_tie < (long long)all) {
                 uint32_t key = 0;
                 u64 zero = 0;
                 // the n-th smallest id is the n-th largest of 2^24 - 1 - id
@@ -547,18 +706,22 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
                     each_inside([&](int i) {
                         if (order_key(R.l_of(base + i)) == edge) f(0xFFFFFFu - (uint32_t)(base + i), 1ull);
                     });
-                }, [&](u64 c) { return c >= (u64)n; }, 24, &key, &zero);
+                }, [&](u64 c) { return c >= (u64)n_tie; }, 24, &key, &zero);
                 cut = (int)(0xFFFFFFu - key);
             }
-            each_inside([&](int i) {
+            kept = 0;
+            each_inside([&](int i) {     // a warp walks its own run
                 const uint32_t key = order_key(R.l_of(base + i));
                 if (key > edge || (key == edge && base + i <= cut)) {
-                    if (e[i] >= min_p) atomicAdd(&s.wsum[i / seg], weight_of(e[i]));
+                    if (e[i] >= min_p) kept += weight_of(e[i]);
                 } else {
                     e[i] = 0.f;
                 }
             });
-        } else {
+            kept = warp_sum64(kept);
+            if (lane == 0) s.wsum[warp] += kept;
+        }
+        if (!found) {
             // rounding of the limit: everything is kept
             lo = 0.f;
             kept = 0;
@@ -568,21 +731,27 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             if (lane == 0) s.wsum[warp] = kept;
         }
     }
-    cl.sync();
+    __syncthreads();
 
     // ---- the draw: the warp whose run of ids holds the target
-    u64 Z = 0, before = 0, mine = 0;
-    for (int r = 0; r < C; ++r)
-        for (int w = 0; w < GW; ++w) {
-            const u64 v = cl.map_shared_rank(s.wsum, r)[w];
-            if (r < rank || (r == rank && w < warp)) before += v;
-            if (r == rank && w == warp) mine = v;
-            Z += v;
-        }
+    if (tid == 0) {
+        u64 t = 0;
+#pragma unroll
+        for (int w = 0; w < GW; ++w) t += s.wsum[w];
+        s.kept = t;
+    }
+    cl.sync();
+    u64 Z = 0, before = 0;
+    from_all(cl, C, &s.kept, [&](int r, u64 v) {
+        if (r < rank) before += v;
+        Z += v;
+    });
+    for (int w = 0; w < warp; ++w) before += s.wsum[w];
+    const u64 mine = s.wsum[warp];
     const u64 target = target_of(Z);
     if (before <= target && target < before + mine) {
         for (int i = w0 + lane * 4; ; i += 128) {
-            const float4 v = *(const float4*)(e + i);
+            const float4 v = i < w0 + seg ? *(const float4*)(e + i) : make_float4(0.f, 0.f, 0.f, 0.f);
             const float a[4] = {v.x, v.y, v.z, v.w};
             u64 w[4], own = 0;
 #pragma unroll
@@ -618,7 +787,7 @@ cudaError_t launch_t(int n, int V, const void* logits, int64_t ld, const float* 
     int C = 1;
     while (C < MAX_CLUSTER && ((V + C - 1) / C > 19456 || ((int64_t)n * C * 2 <= 2 * device_sm_count() && V / (2 * C) >= 4096)))
         C *= 2;
-    const int slice = ((V + C - 1) / C + GW * 128 - 1) / (GW * 128) * (GW * 128);
+    const int slice = max(((V + C - 1) / C + GW * 32 - 1) / (GW * 32) * (GW * 32), 2 * LIST);
     const int smem = slice * (int)sizeof(float);
     // a per-device attribute: set on every call (a host-side table lookup)
     cudaError_t e = cudaFuncSetAttribute(sample_given_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
