@@ -81,6 +81,61 @@ __device__ __forceinline__ float exp_of(float d) {
     return d < -86.0f ? 0.f : e;
 }
 
+// two fp32 values side by side: one instruction rounds both
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pk(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpk(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// exp_of of l0 - m and l1 - m
+__device__ __forceinline__ void exp_of2(float l0, float l1, float m, float& e0, float& e1) {
+    const float d0 = __fsub_rn(l0, m), d1 = __fsub_rn(l1, m);
+    const f2 c = pk(fmaxf(d0, -87.f), fmaxf(d1, -87.f));
+    const f2 s = add2(mul2(c, pk(kInvLn2, kInvLn2)), pk(12582912.0f, 12582912.0f));
+    const f2 n = add2(s, pk(-12582912.0f, -12582912.0f));
+    const f2 r = add2(add2(c, mul2(n, pk(-kLn2Hi, -kLn2Hi))), mul2(n, pk(-kLn2Lo, -kLn2Lo)));
+    auto both = [](float v) { return pk(v, v); };
+    f2 p = both(1.0f / 40320.0f);
+    p = add2(both(1.0f / 5040.0f), mul2(r, p));
+    p = add2(both(1.0f / 720.0f), mul2(r, p));
+    p = add2(both(1.0f / 120.0f), mul2(r, p));
+    p = add2(both(1.0f / 24.0f), mul2(r, p));
+    p = add2(both(1.0f / 6.0f), mul2(r, p));
+    p = add2(both(0.5f), mul2(r, p));
+    p = add2(both(1.0f), mul2(r, p));
+    p = add2(both(1.0f), mul2(r, p));
+    float p0, p1, s0, s1;
+    unpk(p, p0, p1);
+    unpk(s, s0, s1);
+    e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(s0) << 23) - (0x4B400000u << 23));
+    e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(s1) << 23) - (0x4B400000u << 23));
+    if (d0 < -86.0f) e0 = 0.f;
+    if (d1 < -86.0f) e1 = 0.f;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // x / T rounded to nearest.  With y the rounded reciprocal of T, two residual
 // corrections of x y give the rounded quotient (P. Markstein, IBM J. Res. Dev.
 // 34, 1990) while nothing under- or overflows; other operands are divided.
@@ -98,6 +153,14 @@ struct Quotient {
         const float q = __fadd_rn(__fmaf_rn(__fmaf_rn(-q1, T, x), y, q1), 0.f);   // -0 becomes +0
         return x == -INFINITY ? x : q;
     }
+    __device__ __forceinline__ void quick2(float x0, float x1, float& l0, float& l1) const {
+        const f2 x = pk(x0, x1), yy = pk(y, y), t = pk(-T, -T);
+        const f2 q0 = mul2(x, yy);
+        const f2 q1 = fma2(fma2(q0, t, x), yy, q0);
+        unpk(add2(fma2(fma2(q1, t, x), yy, q1), 0ull), l0, l1);
+        if (x0 == -INFINITY) l0 = x0;
+        if (x1 == -INFINITY) l1 = x1;
+    }
     __device__ __forceinline__ float operator()(float x) const {
         return in_range(x) ? quick(x) : __fadd_rn(__fdiv_rn(x, T), 0.f);
     }
@@ -106,7 +169,6 @@ struct Quotient {
 struct GivenSmem {
     u64 wsum[GW];                // kept weight of each warp's ids
     u64 red[GW + 1];
-    u64 best;                    // largest (order key, ~id) of the slice
     u64 total, above, kept;      // weight of the slice; of it above the bracket; kept
     uint32_t hist[BINS];         // sums of mantissas by e, or counts by max - l, from the top
     uint32_t coarse[COARSE];     // of 16 bins each
@@ -114,8 +176,10 @@ struct GivenSmem {
     uint32_t radix[2][3 * 256];  // radix passes, in turn
     uint32_t lkey[LIST], skey[LIST];
     int lid[LIST], sid[LIST];
-    float le[LIST], se[LIST];
+    float le[LIST];
+    u64 sw[LIST];                // weights of the merged list
     unsigned char keep[LIST];
+    uint32_t best;               // largest order key of the slice
     int n_list, pick;
     u64 pick64;
     double logz;
@@ -182,7 +246,6 @@ struct Row {
     Quotient q;
     int V, C, rank, slice, seg, base;   // base: id of the slice's first entry
     float m;             // largest l
-    int first;           // its lowest id
 
     __device__ float l_of(int id) const { return q(lval(x, id)); }
 
@@ -235,8 +298,9 @@ struct Row {
 
     // The bin of the cluster's histograms in which the running sum of weigh(entry, bin) passes the goal (into
     // s.edge_bin, -1: none) and the sum in front of it (s.pick64).  All threads of the cluster call it.
-    template <class Weigh, class Reach>
-    __device__ void locate(Weigh weigh, Reach reach) {
+    // goal(): sets the goal, once the cluster has met.
+    template <class Weigh, class Reach, class Goal>
+    __device__ void locate(Weigh weigh, Reach reach, Goal goal) {
         const int t = threadIdx.x;
         __syncthreads();
         if (t < COARSE) {
@@ -247,6 +311,7 @@ struct Row {
         }
         if (t == 0) { s.pick = -1; s.edge_bin = -1; }
         cl.sync();
+        goal();
         u64 c = 0;
         if (t < COARSE) from_all(cl, C, &s.coarse[t], [&](int, uint32_t v) { c += weigh(v, t * 16); });
         u64 incl = cta_scan64(s, c);
@@ -270,30 +335,28 @@ struct Row {
         const int n = atomicAdd(&s.n_list, 1);
         if (n < LIST) { s.lkey[n] = key; s.lid[n] = id; s.le[n] = ev; }
     }
-    // The lists of all CTAs, by rank, into skey / sid / se of each; *own: where this CTA's begins.  Returns their
+    // The lists of all CTAs, by rank, into skey / sid / sw of each; *own: where this CTA's begins.  Returns their
     // length, or -1 if it is more than LIST.  All threads of the cluster call it.
     __device__ int merge(int* own) {
         cl.sync();
-        int n[MAX_CLUSTER], total = 0;
+        static_assert(LIST <= GT, "a thread copies an entry");
+        int total = 0, from = 0, at = threadIdx.x;
         *own = 0;
         from_all(cl, C, &s.n_list, [&](int r, int v) {
-            n[r] = v;
             if (r < rank) *own += v;
             total += v;
+            if (r < C - 1 && from == r && at >= v) { at -= v; ++from; }
         });
         if (total > LIST) return -1;
-        int off = 0;
-#pragma unroll
-        for (int r = 0; r < MAX_CLUSTER; ++r)
-            if (r < C) {
-                GivenSmem* o = cl.map_shared_rank(&s, r);
-                for (int i = threadIdx.x; i < n[r]; i += GT) {
-                    s.skey[off + i] = o->lkey[i];
-                    s.sid[off + i] = o->lid[i];
-                    s.se[off + i] = o->le[i];
-                }
-                off += n[r];
-            }
+        if ((int)threadIdx.x < total) {
+            const GivenSmem* o = cl.map_shared_rank(&s, from);
+            const uint32_t key = o->lkey[at];
+            const int id = o->lid[at];
+            const float ev = o->le[at];
+            s.skey[threadIdx.x] = key;
+            s.sid[threadIdx.x] = id;
+            s.sw[threadIdx.x] = weight_of(ev);
+        }
         __syncthreads();
         return total;
     }
@@ -316,12 +379,11 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
     const float temp = temp_[row], top_p = topp_[row], min_p = minp_[row];
     const int k = topk_[row];
     Row<T> R{s, cl, e, logits + row * ld, Quotient(temp > 0.f ? temp : 1.f), V, C, rank, slice, slice / GW,
-             rank * slice, 0.f, 0};
+             rank * slice, 0.f};
     const int seg = R.seg, base = R.base, w0 = warp * seg;   // the warp's run of the slice
 
     // ---- quotients into shared memory; the largest, and maxima of groups of C lanes
-    float mx = -INFINITY;
-    int at = 0, bad = !(temp >= 0.f);
+    float mx = -INFINITY;   // NaN once it has met one
     {
         const T* x = R.x + base;
         const bool vec = ((uintptr_t)x & (4 * sizeof(T) - 1)) == 0;
@@ -336,54 +398,44 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             }
             const bool quick = R.q.in_range(v[0]) && R.q.in_range(v[1]) && R.q.in_range(v[2]) && R.q.in_range(v[3]);
             if (quick) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = R.q.quick(v[j]);
+                R.q.quick2(v[0], v[1], v[0], v[1]);
+                R.q.quick2(v[2], v[3], v[2], v[3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = R.q(v[j]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                bad |= !(v[j] < INFINITY);
-                if (v[j] > mx) { mx = v[j]; at = base + i + j; }
-            }
+            mx = max_nan(mx, max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])));
             *(float4*)(e + i) = make_float4(v[0], v[1], v[2], v[3]);
         }
     }
     {
-        const uint32_t key = order_key(mx);
-        u64 best = (u64)key << 32 | (uint32_t)~at;
+        const uint32_t key = mx < INFINITY && temp >= 0.f ? order_key(mx) : 0xFFFFFFFFu;   // all ones: the row fails
         uint32_t gm = key;
         __syncwarp();
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         for (int o = 1; o < C; o <<= 1) gm = max(gm, __shfl_xor_sync(0xffffffffu, gm, o));
         if ((lane & (C - 1)) == 0) cl.map_shared_rank(s.maxima, 0)[((rank * GW + warp) * 32 + lane) / C] = gm;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const u64 b = __shfl_xor_sync(0xffffffffu, best, o);
-            best = b > best ? b : best;
-        }
-        if (lane == 0) s.red[warp] = best;
-        if (tid == 0) s.n_list = 0;
-        bad = __syncthreads_or(bad);
-        if (tid == 0) {
-            best = s.red[0];
-            for (int w = 1; w < GW; ++w) best = s.red[w] > best ? s.red[w] : best;
-            s.best = bad ? ~0ull : best;   // (a key of +inf or NaN)
-        }
+        gm = __reduce_max_sync(0xffffffffu, key);
+        if (tid == 0) { s.n_list = 0; s.best = 0; }
+        __syncthreads();
+        if (lane == 0) atomicMax(&s.best, gm);
     }
     cl.sync();
-    u64 best = 0;
-    bad = 0;
-    from_all(cl, C, &s.best, [&](int, u64 b) {
-        bad |= b == ~0ull;
-        best = b > best ? b : best;
-    });
-    const float m = R.m = order_key_inv((uint32_t)(best >> 32));
-    const int first = R.first = (int)~(uint32_t)best;
+    uint32_t best = 0;
+    from_all(cl, C, &s.best, [&](int, uint32_t b) { best = max(best, b); });
+    const bool bad = best == 0xFFFFFFFFu;
+    const float m = R.m = order_key_inv(best);
     const bool fails = bad || m == -INFINITY;
-    // the largest alone: greedy, or nothing else passes top-p or min-p
+    // the largest alone (the lowest id on ties): greedy, or nothing else passes top-p or min-p
     if (fails || temp == 0.f || !(top_p > 0.f) || !(min_p <= 1.f)) {
+        if (tid == 0) s.pick = 0x7fffffff;
+        __syncthreads();
+        if (!fails)
+            for (int i = w0 + lane; i < w0 + seg; i += 32)
+                if (e[i] == m && base + i < V) atomicMin(&s.pick, base + i);
+        cl.sync();
+        int first = 0x7fffffff;
+        if (rank == 0) from_all(cl, C, &s.pick, [&](int, int v) { first = min(first, v); });
         if (rank == 0 && tid == 0) {
             ids[row] = fails ? -1 : first;
             if (logprob) logprob[row] = fails ? __uint_as_float(0x7fc00000u) : 0.f;
@@ -428,6 +480,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         cl.sync();
         const int n = *cl.map_shared_rank(&s.n_list, 0);
         if (n <= LIST) {
+            cl.sync();       // from here on the first CTA works on its own memory alone
             if (rank == 0) {
                 // sorted by (l descending, id ascending): eight threads count an entry's rank
                 for (int i0 = 0; i0 < n; i0 += GT / 8) {
@@ -494,7 +547,6 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
                         logprob[row] = (float)((double)__fsub_rn(order_key_inv(s.skey[s.pick % LIST]), m) - s.logz);
                 }
             }
-            cl.sync();
             return;
         }
         cl.sync();   // everyone knows that the list overflowed
@@ -509,7 +561,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         __syncthreads();
         for (int i = w0 + lane; i < w0 + seg; i += 32)
             if (base + i < V) atomicAdd(&s.hist[bin_of(e[i])], 1u);
-        R.locate([](uint32_t v, int) { return (u64)v; }, [&](u64 c) { return c >= (u64)k; });
+        R.locate([](uint32_t v, int) { return (u64)v; }, [&](u64 c) { return c >= (u64)k; }, [] {});
         const int b = s.edge_bin;
         u64 above = s.pick64;
         for (int i = w0 + lane; i < w0 + seg; i += 32)
@@ -553,23 +605,33 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
     if (tid == 0) s.n_list = 0;
     __syncthreads();
     u64 sum = 0, kept = 0;
-    for (int i = w0 + lane * 4; i < w0 + seg; i += 128) {
+    auto to_e = [&](int i, auto use) {
         const float4 v = *(const float4*)(e + i);
-        float a[4] = {v.x, v.y, v.z, v.w};
+        float a[4];
+        exp_of2(v.x, v.y, m, a[0], a[1]);
+        exp_of2(v.z, v.w, m, a[2], a[3]);
+        if (with_k) {
+            a[0] = v.x >= kth ? a[0] : 0.f;
+            a[1] = v.y >= kth ? a[1] : 0.f;
+            a[2] = v.z >= kth ? a[2] : 0.f;
+            a[3] = v.w >= kth ? a[3] : 0.f;
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[j] = a[j] >= kth ? exp_of(__fsub_rn(a[j], m)) : 0.f;
-            const u64 w = weight_of(a[j]);
-            sum += w;
-            if (a[j] >= min_p) kept += w;
-            if (with_p) {
-                const uint32_t b = __float_as_uint(a[j]);
+        for (int j = 0; j < 4; ++j) use(a[j]);
+        *(float4*)(e + i) = make_float4(a[0], a[1], a[2], a[3]);
+    };
+    if (with_p) {
+        for (int i = w0 + lane * 4; i < w0 + seg; i += 128)
+            to_e(i, [&](float a) {
+                const uint32_t b = __float_as_uint(a);
+                sum += weight_of(a);
                 // 16 bits of the mantissa: at most 2^15 logits a slice, so 32 bits hold their sum
                 if (b >= BIN0 << 17)
-                    atomicAdd(&s.hist[BINS - 1 + BIN0 - (b >> 17)], ((b & 0x7FFFFFu) | 0x800000u) >> 8);
-            }
-        }
-        *(float4*)(e + i) = make_float4(a[0], a[1], a[2], a[3]);
+                    atomicAdd(&s.hist[BINS - 1 + BIN0 - (b >> 17)], ((b & 0x7FFFFFu) + 0x800080u) >> 8);
+            });
+    } else {
+        for (int i = w0 + lane * 4; i < w0 + seg; i += 128)
+            to_e(i, [&](float a) { kept += a >= min_p ? weight_of(a) : 0ull; });
     }
     float lo = 0.f;            // entries with e below it are not kept
     kept = warp_sum64(kept);
@@ -577,22 +639,23 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
     if (with_p) {
         sum = cta_sum64(s, sum);
         if (tid == 0) s.total = sum;
-        cl.sync();
-        u64 Z = 0;
-        from_all(cl, C, &s.total, [&](int, u64 v) { Z += v; });
-        const double limit = __dmul_rn((double)top_p, (double)Z);
+        double limit = 0.;
         // the bin in which the histogram, from the top, passes the limit (in units of 2^-40)
         R.locate([](uint32_t v, int i) {
             const int o = ((BINS - 1 - i) >> 6) - 15;   // of e's exponent
             return o >= 0 ? (u64)v << o : (u64)v >> -o;
-        }, [&](u64 c) { return !((double)c < limit); });
+        }, [&](u64 c) { return !((double)c < limit); }, [&] {
+            u64 Z = 0;
+            from_all(cl, C, &s.total, [&](int, u64 v) { Z += v; });
+            limit = __dmul_rn((double)top_p, (double)Z);
+        });
         // What lies above that bin is added up, what lies in it listed, and each listed entry finds the weight in
-        // front of it (attempt 0); a bin with too many entries is searched by radix (1).  e is monotone in l up to
-        // rounding only, so the border has to lie clearly inside the bin; else its neighbours (2) or all entries (3)
-        // are searched.
+        // front of it (attempt 0, on the next bin if the border turns out to lie there); a bin with too many entries is
+        // searched by radix (1).  e is monotone in l up to rounding only, so the border has to lie clearly inside the
+        // bin; else its neighbours (2) or all entries (3) are searched.
         float hi;
         bool found = false;
-        const int edge_bin = s.edge_bin < 0 ? 0 : BINS - 1 - s.edge_bin;
+        int edge_bin = s.edge_bin < 0 ? 0 : BINS - 1 - s.edge_bin, shifts = 0;
         for (int attempt = 0; attempt < 4 && !found;) {
             const int wide = attempt == 2, b0 = edge_bin - wide, b1 = edge_bin + 1 + wide;
             lo = attempt == 3 || b0 <= 0 ? 0.f : __uint_as_float((uint32_t)(b0 + BIN0) << 17);
@@ -632,39 +695,47 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             from_all(cl, C, &s.above, [&](int, u64 v) { above += v; });
             if (attempt == 0 && n < 0) { attempt = 1; cl.sync(); continue; }
             if (attempt == 0) {
-                // eight threads add up what is in front of an entry of this CTA; the border is the last entry kept
-                // of all, so every CTA looks at every entry for it
-                if (tid == 0) s.pick = 0;     // 1: a border, 2: not clear of the bin's ends
+                // eight threads add up what is in front of an entry of this CTA; the last entry kept is the border
+                const int mine = s.n_list;
+                if (tid == 0) s.pick = 0;     // 1: the border is here, 2: but not clear of the bin's ends
                 __syncthreads();
-                for (int i0 = 0; i0 < n; i0 += GT / 8) {
-                    const int i = min(i0 + tid / 8, n - 1), id = s.sid[i];
-                    const uint32_t a = s.skey[i];
+                for (int i0 = 0; i0 < mine; i0 += GT / 8) {
+                    const int i = min(i0 + tid / 8, mine - 1), id = s.sid[own + i];
+                    const uint32_t a = s.skey[own + i];
                     u64 before = 0;
+#pragma unroll 4
                     for (int j = tid & 7; j < n; j += 8) {
                         const uint32_t o = s.skey[j];
-                        if (o > a || (o == a && s.sid[j] < id)) before += weight_of(s.se[j]);
+                        if (o > a || (o == a && s.sid[j] < id)) before += s.sw[j];
                     }
 #pragma unroll
                     for (int o = 1; o < 8; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
                     before += above;
-                    const u64 w = weight_of(s.se[i]);
                     const bool in = (double)before < limit;
-                    if ((tid & 7) == 0 && i0 + tid / 8 < n) {
-                        if (i >= own && i < own + s.n_list) s.keep[i - own] = in;
-                        if (in && !((double)(before + w) < limit)) atomicOr(&s.pick, clear(s.se[i]) ? 1 : 2);
+                    if ((tid & 7) == 0) {
+                        s.keep[i] = in;
+                        if (in && !((double)(before + s.sw[own + i]) < limit)) atomicOr(&s.pick, clear(s.le[i]) ? 1 : 2);
                     }
                 }
-                __syncthreads();
-                found = s.pick == 1;
-                cl.sync();      // lists, sums and histograms have been read
-                if (!found) { attempt = 2; continue; }
+                cl.sync();
+                int border = 0;
+                from_all(cl, C, &s.pick, [&](int, int v) { border |= v; });
+                found = border == 1;
+                if (!found) {
+                    cl.sync();      // lists and sums have been read
+                    // next door, where the sums say so; else, or after that, all of the neighbours
+                    const int step = !((double)above < limit) ? 1 : border == 0 ? -1 : 0;
+                    if (step == 0 || ++shifts > 2) attempt = 2;
+                    else edge_bin = min(max(edge_bin + step, 0), BINS - 1);
+                    continue;
+                }
                 // the warp's share of the kept ones
                 kept = 0;
-                for (int i = lane; i < s.n_list; i += 32) {
+                for (int i = lane; i < mine; i += 32) {
                     const int at = s.sid[own + i] - base;
-                    if (at / seg != warp) continue;
-                    if (s.keep[i]) kept += s.se[own + i] >= min_p ? weight_of(s.se[own + i]) : 0ull;
-                    else e[at] = 0.f;
+                    if (at < w0 || at >= w0 + seg) continue;
+                    if (!s.keep[i]) e[at] = 0.f;
+                    else if (s.le[i] >= min_p) kept += s.sw[own + i];
                 }
                 kept = warp_sum64(kept);
                 if (lane == 0) s.wsum[warp] += kept;
