@@ -116,6 +116,13 @@ typedef struct {
                            the same dot product in both, so results differ
                            only where the tensor-core tile / K-split choice,
                            which depends on the product's width, differs      */
+    int kv_page_size;   /* > 0: the talker's keys and values lie in pages of this
+                           many positions (a power of two, 16..1024) that the
+                           rows share, instead of max_ctx positions a row: a
+                           prefill gives each row the pages for its prompt and
+                           max_frames.  Per-layer kernels only (the operators
+                           of q3paged.h); 0: one slab a row                     */
+    int kv_pages;       /* pages in all (0: max_batch rows of max_ctx positions) */
 } q3tts_config;
 
 /* step_path values */
@@ -201,7 +208,8 @@ int q3tts_create(const q3tts_config* cfg, const q3tts_weights* w, void* workspac
  *   rows            [batch] host: per-row settings
  *   code0_out       [batch] int32, host or device, or NULL: selection 0
  * Resets every row.  Errors: Q3_ERR_ARG, Q3_ERR_CAPACITY (len + max_frames >
- * max_ctx, n_text > max_text), Q3_ERR_NAN, Q3_ERR_CUDA. */
+ * max_ctx, n_text > max_text, the rows' pages are more than kv_pages),
+ * Q3_ERR_NAN, Q3_ERR_CUDA. */
 int q3tts_prefill(q3tts_t* h, int batch, const float* prompt, const int32_t* prompt_offsets, const float* text,
                   const int32_t* text_offsets, const float* tts_pad, const q3tts_sampling* rows,
                   int32_t* code0_out);

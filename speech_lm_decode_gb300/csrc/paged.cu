@@ -135,6 +135,19 @@ cudaError_t launch_paged_append(const PagedView& c, int act, int kv, int n_token
     return go(append_t<float, float, 4>);
 }
 
+namespace {
+__global__ void paged_lengths_kernel(const int* __restrict__ pos, int n, int* __restrict__ ctx) {
+    pdl_wait();
+    pdl_trigger();
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) ctx[i] = max(pos[i] + 1, 0);
+}
+}  // namespace
+
+cudaError_t launch_paged_lengths(const int* pos, int n, int* ctx, cudaStream_t st) {
+    return launch_pdl(paged_lengths_kernel, (n + 127) / 128, 128, 0, st, pos, n, ctx);
+}
+
 // ------------------------------------------------------------------ C entry points
 namespace {
 

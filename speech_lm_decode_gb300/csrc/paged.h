@@ -38,6 +38,8 @@ cudaError_t launch_paged_append(const PagedView& c, int act, int kv, int n_token
                                 int64_t q_stride, int* err, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttn& a, cudaStream_t st);
 size_t paged_workspace_bytes();
+// ctx[b] = pos[b] + 1 for a step's rows (pos < 0, a finished row: 0)
+cudaError_t launch_paged_lengths(const int* pos, int n, int* ctx, cudaStream_t st);
 // few query rows over bf16 pages (paged_decode.cu)
 bool paged_decode_takes(const PagedAttn& a);
 cudaError_t launch_paged_decode(const PagedAttn& a, cudaStream_t st);

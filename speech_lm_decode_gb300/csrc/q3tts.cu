@@ -16,6 +16,7 @@
 #include "cluster_step.h"
 #include "frame_params.h"
 #include "kernels.h"
+#include "paged.h"
 
 using namespace q3;
 
@@ -29,10 +30,12 @@ constexpr int MIN_SAMPLE_SETS = 256; // staging for q3tts_sample_logits
 struct Layout {
     size_t kvK, kvV, ckvK, ckvV, rope, rows, params, h, x, cx, tok, opA, opB, headop, qkv, pm, pl, pacc, logits,
         cplogits, t_row, t_pos, c_row, c_pos, last_row, codes, codes_stage, text, pad, err, s_params, s_logits, s_sel, s_row, s_ids, s_seen, cap_slot,
-        fparams, fctl, fpart, fll, tcs, tcs2, clpack, clxr, cllg, clparams, ptiles;
+        fparams, fctl, fpart, fll, tcs, tcs2, clpack, clxr, cllg, clparams, ptiles, pg_table,
+        pg_off, pg_ctx, pg_coff, pg_cctx, pg_ws;
     bool cl;                            // the cluster step kernel's regions are present
     size_t total;
     int mmax, kA, kB, rope_rows, frames_cap, n_sets, vmax, fsplits;
+    int row_pages, n_pages;             // paged talker cache: table entries of a row, pages in all (0: slabs)
     size_t fll_words;                   // exchange words of the frame kernel
     size_t fw_x, fw_cx, fw_qkv, fw_o, fw_act, fw_log, fw_cpl;   // word offsets in fll
 };
@@ -57,7 +60,10 @@ Layout make_layout(const q3tts_config& c) {
     L.frames_cap = c.max_ctx;
     L.n_sets = std::max(c.max_batch, MIN_SAMPLE_SETS);
     L.vmax = std::max(c.codec_vocab, c.cp_vocab);
-    const size_t kv = (size_t)c.n_layers * B * c.n_kv_heads * c.max_ctx * hd * e;
+    L.row_pages = c.kv_page_size > 0 ? (c.max_ctx + c.kv_page_size - 1) / c.kv_page_size : 0;
+    L.n_pages = c.kv_page_size > 0 ? (c.kv_pages > 0 ? c.kv_pages : c.max_batch * L.row_pages) : 0;
+    const size_t kv = (size_t)c.n_layers * c.n_kv_heads * hd * e *
+                      (c.kv_page_size > 0 ? (size_t)L.n_pages * c.kv_page_size : B * c.max_ctx);
     L.kvK = take(kv);
     L.kvV = take(kv);
     const size_t ckv = (size_t)c.cp_layers * B * c.n_kv_heads * 16 * hd * e;
@@ -135,6 +141,15 @@ Layout make_layout(const q3tts_config& c) {
         L.cllg = take(cl.lg_words * sizeof(Word));
         L.clparams = take(sizeof(ClParams));
     }
+    // paged talker cache: page table, the step's and a prefill chunk's row offsets and lengths, workspace
+    if (L.n_pages > 0) {
+        L.pg_table = take(B * L.row_pages * sizeof(int32_t));
+        L.pg_off = take((B + 1) * sizeof(int));
+        L.pg_ctx = take(B * sizeof(int));
+        L.pg_coff = take((B + 1) * sizeof(int));
+        L.pg_cctx = take(B * sizeof(int));
+        L.pg_ws = take(paged_workspace_bytes());
+    }
     L.total = off;
     return L;
 }
@@ -163,6 +178,11 @@ bool config_ok(const q3tts_config* c, std::string* why) {
     if (c->wait_limit_us < 0 || c->inject_timeout < 0 || c->debug_sync < 0 || c->debug_sync > 1)
         return bad("bad wait_limit_us / inject_timeout / debug_sync");
     if (c->separate_projections < 0 || c->separate_projections > 1) return bad("separate_projections must be 0 or 1");
+    if (c->kv_page_size != 0 && (c->kv_page_size < 16 || c->kv_page_size > 1024 || (c->kv_page_size & (c->kv_page_size - 1))))
+        return bad("kv_page_size must be 0 or a power of two in 16..1024");
+    if (c->kv_pages < 0 || (c->kv_pages > 0 && c->kv_page_size == 0)) return bad("kv_pages goes with kv_page_size");
+    if (c->kv_page_size > 0 && c->step_path != Q3_PATH_AUTO && c->step_path != Q3_PATH_GRAPH)
+        return bad("a paged cache runs on the per-layer kernels (step_path auto or graph)");
     if (c->step_path == Q3_PATH_CLUSTER && cl_unsupported(*c)[0] != 0) return bad("cluster kernel: unsupported shape");
     if (c->text_vocab < 0 || c->text_hidden < 0 || (c->text_vocab > 0) != (c->text_hidden > 0) ||
         (c->text_hidden > 0 && c->text_hidden % 8))
@@ -214,6 +234,26 @@ struct q3tts {
         TcScratch t = tc();
         t.base = c.dtype == Q3_BF16 ? p<void>(L.tcs2) : nullptr;
         return t;
+    }
+    // layer l of the paged talker cache, for the batch's rows
+    PagedView pages(int l) const {
+        PagedView v{};
+        const size_t e = c.dtype == Q3_BF16 ? 2 : 4;
+        v.nq = c.n_q_heads;
+        v.nkv = c.n_kv_heads;
+        v.G = v.nq / v.nkv;
+        while ((1 << v.page_shift) < c.kv_page_size) ++v.page_shift;
+        v.n_pages = L.n_pages;
+        v.n_seqs = batch;
+        v.max_pages = L.row_pages;
+        v.token_stride = c.head_dim;
+        v.head_stride = (int64_t)c.kv_page_size * c.head_dim;
+        v.page_stride = v.head_stride * v.nkv;
+        const size_t layer = (size_t)v.n_pages * v.page_stride * e;
+        v.k = p<char>(L.kvK) + l * layer;
+        v.v = p<char>(L.kvV) + l * layer;
+        v.table = p<int32_t>(L.pg_table);
+        return v;
     }
     RowState* rows() const { return p<RowState>(L.rows); }
     int* err() const { return p<int>(L.err); }
@@ -275,9 +315,12 @@ void invalidate_graph(q3tts* h) {
 // tiles / n_tiles: prompt tokens of a prefill chunk, whose attention runs tiled
 // (bf16 caches); NULL for decode steps.  single: every token belongs to a
 // different row (a decode step), so short bf16 caches take the attention with
-// QK-norm, RoPE and the cache append fused in.
+// QK-norm, RoPE and the cache append fused in.  A paged talker cache takes the
+// paged operators instead, with the rows' offsets and lengths (max_new: tokens
+// of one row at most).
 int enqueue_layers(q3tts* h, bool talker, int M, float* x, const int* trow, const int* tpos,
-                   const int4* tiles = nullptr, int n_tiles = 0, bool single = false) {
+                   const int4* tiles = nullptr, int n_tiles = 0, bool single = false, const int* row_off = nullptr,
+                   const int* row_ctx = nullptr, int max_new = 0) {
     const q3tts_config& c = h->c;
     const q3tts_block_weights& bw = talker ? h->w.talker : h->w.cp;
     const int L = talker ? c.n_layers : c.cp_layers;
@@ -299,7 +342,8 @@ int enqueue_layers(q3tts* h, bool talker, int M, float* x, const int* trow, cons
     // the attention combine writes the O projection's operand, and the gate/up
     // projection the down projection's, when those run on the tensor cores
     const TcScratch tcs = h->tc(), tcs2 = h->tc2();
-    const bool presplit_o = linear_takes_split(c.dtype, M, c.n_q_heads * c.head_dim, tcs);
+    const bool paged = talker && h->L.n_pages > 0;
+    const bool presplit_o = !paged && linear_takes_split(c.dtype, M, c.n_q_heads * c.head_dim, tcs);
     const bool presplit_d = presplit && linear_takes_split(c.dtype, M, F, tcs2);
     for (int l = 0; l < L; ++l) {
         const char* wqkv = (const char*)bw.wqkv + (size_t)l * nqkv * H * e;
@@ -324,8 +368,29 @@ int enqueue_layers(q3tts* h, bool talker, int M, float* x, const int* trow, cons
         } else {
             CK(launch_linear(c.dtype, wqkv, nqkv, H, presplit ? nullptr : opA, H, M, qkv, nqkv, nullptr, 0, h->tc(), h->err(), h->st)); debug_wait(h, "launch_linear");
         }
-        const bool fused = single && !tiles && c.dtype == Q3_BF16 && nq == 2 * nkv && cap <= 64;
-        if (fused) {
+        const bool fused = !paged && single && !tiles && c.dtype == Q3_BF16 && nq == 2 * nkv && cap <= 64;
+        if (paged) {
+            PagedAttn a{};
+            a.c = h->pages(l);
+            CK(launch_paged_append(a.c, Q3_F32, c.dtype, M, qkv, nqkv, trow, tpos,
+                                   (const float*)bw.q_norm + (size_t)l * hd, (const float*)bw.k_norm + (size_t)l * hd,
+                                   eps, h->p<float>(h->L.rope), h->L.rope_rows, qkv, nqkv, h->err(), h->st));
+            debug_wait(h, "launch_paged_append");
+            a.act = Q3_F32;
+            a.kv = c.dtype;
+            a.n_tokens = M;
+            a.max_q = max_new;
+            a.q = qkv;
+            a.q_stride = nqkv;
+            a.q_off = row_off;
+            a.ctx = row_ctx;
+            a.scale = 0.08838834764831845f;   // 1/sqrt(128)
+            a.out = opA;
+            a.out_stride = nq * hd;
+            a.ws = h->p<void>(h->L.pg_ws);
+            a.err = h->err();
+            CK(launch_paged_attention(a, h->st)); debug_wait(h, "launch_paged_attention");
+        } else if (fused) {
             CK(launch_attention_short_fused(qkv, nqkv, M, nq, nkv, (const float*)bw.q_norm + (size_t)l * hd,
                                             (const float*)bw.k_norm + (size_t)l * hd, eps, h->p<float>(h->L.rope),
                                             h->L.rope_rows, Kc + l * kv_layer, Vc + l * kv_layer, cap, trow, tpos, opA,
@@ -337,7 +402,8 @@ int enqueue_layers(q3tts* h, bool talker, int M, float* x, const int* trow, cons
                                  h->L.rope_rows, Kc + l * kv_layer, Vc + l * kv_layer, cap, trow, tpos, h->err(),
                                  h->st)); debug_wait(h, "launch_qk_rope_kv");
         }
-        if (!fused && tiles && c.dtype == Q3_BF16) {
+        if (paged) {
+        } else if (!fused && tiles && c.dtype == Q3_BF16) {
             CK(launch_prefill_attention(c.dtype, qkv, nqkv, M, nq, nkv, Kc + l * kv_layer, Vc + l * kv_layer, cap,
                                         tiles, n_tiles, opA, nq * hd, h->st, presplit_o ? &tcs : nullptr));
             debug_wait(h, "launch_prefill_attention");
@@ -447,7 +513,9 @@ int enqueue_step(q3tts* h) {
     CK(launch_talker_embed(c.dtype, rs, B, h->w.codec_emb, h->w.cp_emb, c.hidden, c.codec_vocab, c.cp_vocab,
                            c.n_groups, codes, h->L.frames_cap, h->p<float>(h->L.text), h->p<float>(h->L.pad), x,
                            c.eos_id, h->err(), h->st)); debug_wait(h, "launch_talker_embed");
-    if ((r = enqueue_layers(h, true, B, x, t_row, t_pos, nullptr, 0, true))) return r;
+    if (h->L.n_pages > 0) { CK(launch_paged_lengths(t_pos, B, h->p<int>(h->L.pg_ctx), h->st)); debug_wait(h, "launch_paged_lengths"); }
+    if ((r = enqueue_layers(h, true, B, x, t_row, t_pos, nullptr, 0, true, h->p<int>(h->L.pg_off),
+                            h->p<int>(h->L.pg_ctx), 1))) return r;
     CK(launch_rmsnorm(x, c.hidden, B, (const float*)h->w.talker.final_norm, c.hidden, c.rms_eps, opA,
                       c.hidden, h->p<float>(h->L.h), c.hidden, nullptr, h->st)); debug_wait(h, "launch_rmsnorm");
     float* logits = h->p<float>(h->L.logits);
@@ -641,7 +709,7 @@ int q3tts_create(const q3tts_config* cfg, const q3tts_weights* w, void* workspac
         cudaGetLastError();
         if (path == Q3_PATH_CLUSTER && !h->cl_ok) { q3tts_destroy(h); return Q3_ERR_ARG; }
         const bool want = path == Q3_PATH_FRAME || path == Q3_PATH_AUTO;
-        h->frame_ok = want && coop && sms >= cfg->n_kv_heads && h->frame_smem > 0 && tiles_fit &&
+        h->frame_ok = want && cfg->kv_page_size == 0 && coop && sms >= cfg->n_kv_heads && h->frame_smem > 0 && tiles_fit &&
                       cfg->cp_vocab <= FRAME_CP_VMAX &&
                       cfg->n_q_heads == 2 * cfg->n_kv_heads;
         if (h->frame_ok && frame_setup(cfg->dtype, h->frame_smem, h->frame_tc) != cudaSuccess) {
@@ -747,6 +815,19 @@ int q3tts_prefill(q3tts_t* h, int batch, const float* prompt, const int32_t* pro
         total_text += nt;
     }
     if (total_text > 0 && !text) return fail(h, Q3_ERR_ARG, "text is NULL but rows have text");
+    // the rows' pages, one row after the other
+    std::vector<int32_t> table;
+    if (h->L.n_pages > 0) {
+        table.assign((size_t)batch * h->L.row_pages, -1);
+        long used = 0;
+        for (int r = 0; r < batch; ++r) {
+            const int need = (prompt_offsets[r + 1] - prompt_offsets[r] + rows_in[r].max_frames + c.kv_page_size - 1) / c.kv_page_size;
+            if (used + need > h->L.n_pages)
+                return fail(h, Q3_ERR_CAPACITY, "row %d: its %d pages are more than the %ld left of %d", r, need,
+                            h->L.n_pages - used, h->L.n_pages);
+            for (int j = 0; j < need; ++j) table[(size_t)r * h->L.row_pages + j] = (int32_t)used++;
+        }
+    }
 
     if (batch != h->graph_batch) invalidate_graph(h);
     h->batch = batch;
@@ -789,6 +870,16 @@ int q3tts_prefill(q3tts_t* h, int batch, const float* prompt, const int32_t* pro
         CK(cudaMemsetAsync(h->p<Word>(h->L.cllg), 0, cl.lg_words * sizeof(Word), h->st));
     }
 
+    std::vector<int> coff(batch + 1), cctx(batch);
+    if (h->L.n_pages > 0) {
+        CK(cudaMemcpyAsync(h->p<int32_t>(h->L.pg_table), table.data(), table.size() * sizeof(int32_t),
+                           cudaMemcpyHostToDevice, h->st));
+        for (int r = 0; r <= batch; ++r) coff[r] = r;   // a step: one token a row
+        CK(cudaMemcpyAsync(h->p<int>(h->L.pg_off), coff.data(), coff.size() * sizeof(int), cudaMemcpyHostToDevice, h->st));
+        CK(cudaMemsetAsync(h->p<void>(h->L.pg_ws), 0, Q3PAGED_COUNTER_BYTES, h->st));
+        CK(cudaStreamSynchronize(h->st));               // the host vector is reused
+    }
+
     // prompt through the talker, in chunks of whole tokens across rows
     const int total = prompt_offsets[batch];
     std::vector<int> trow(h->L.mmax), tpos(h->L.mmax), last(h->L.mmax);
@@ -821,8 +912,24 @@ int q3tts_prefill(q3tts_t* h, int batch, const float* prompt, const int32_t* pro
         CK(cudaMemcpyAsync(h->p<int4>(h->L.ptiles), tiles.data(), tiles.size() * sizeof(int4), cudaMemcpyHostToDevice,
                            h->st));
         CK(cudaMemcpyAsync(x, prompt + (size_t)t0 * H, (size_t)M * H * sizeof(float), cudaMemcpyDefault, h->st));
+        int max_new = 0;
+        if (h->L.n_pages > 0) {
+            for (int r = 0; r < batch; ++r) {
+                // the chunk's tokens of row r
+                const int a = std::min(std::max(prompt_offsets[r] - t0, 0), M), b = std::min(std::max(prompt_offsets[r + 1] - t0, 0), M);
+                coff[r] = a;
+                coff[r + 1] = b;
+                cctx[r] = t0 + b - prompt_offsets[r];
+                if (b <= a) cctx[r] = 0;
+                max_new = std::max(max_new, b - a);
+            }
+            CK(cudaMemcpyAsync(h->p<int>(h->L.pg_coff), coff.data(), coff.size() * sizeof(int), cudaMemcpyHostToDevice,
+                               h->st));
+            CK(cudaMemcpyAsync(h->p<int>(h->L.pg_cctx), cctx.data(), cctx.size() * sizeof(int), cudaMemcpyHostToDevice,
+                               h->st));
+        }
         int r = enqueue_layers(h, true, M, x, h->p<int>(h->L.t_row), h->p<int>(h->L.t_pos), h->p<int4>(h->L.ptiles),
-                               (int)tiles.size());
+                               (int)tiles.size(), false, h->p<int>(h->L.pg_coff), h->p<int>(h->L.pg_cctx), max_new);
         if (r) return r;
         CK(launch_rmsnorm(x, H, M, (const float*)h->w.talker.final_norm, H, c.rms_eps, headop, H,
                           h->p<float>(h->L.h), H, h->p<int>(h->L.last_row), h->st)); debug_wait(h, "launch_rmsnorm");
