@@ -1,4 +1,13 @@
-// Attention of new tokens over a paged cache (q3paged.h).
+// Paged attention (q3paged.h): the choice of kernel, and the one for fp32 pages.
+//
+// fp32 keys and values have no tensor-core form that keeps their 24 bits in
+// fewer than six products, so this kernel multiplies on the CUDA cores.  A CTA
+// of 256 threads takes ROWS query rows of one kv head and walks tiles of 64
+// keys in shared memory: V(t) is on its way (cp.async) while the scores of t
+// are formed, K(t+1) while its outputs are.  A thread forms ROWS/16 x 4 scores
+// and ROWS/16 x 8 outputs, so that a 16-byte shared load serves 8 (ROWS = 64)
+// multiply-adds; K rows are padded by 16 bytes against bank conflicts.  ROWS =
+// 16 serves single tokens, whose bound is the 1 KB read per key and head.
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.h"
@@ -9,74 +18,259 @@ namespace q3 {
 
 namespace {
 
-// One warp for each (token, q head): lane l holds values 4l..4l+3, the keys
-// are walked one at a time with a running maximum and sum.
-template <typename T> __device__ __forceinline__ float4 ld4(const T* p);
-template <> __device__ __forceinline__ float4 ld4<float>(const float* p) { return *(const float4*)p; }
-template <> __device__ __forceinline__ float4 ld4<bf16>(const bf16* p) {
-    const uint2 a = *(const uint2*)p;
-    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u), __uint_as_float(a.y << 16),
-                       __uint_as_float(a.y & 0xffff0000u));
+constexpr int FT = 256;            // threads
+constexpr int FK = 64;             // keys of a tile and of a unit
+constexpr int FKS = HD + 4;        // row of K in shared memory, floats
+constexpr int FPS = FK + 4;        // row of the weights
+constexpr int F_CTAS = 2;          // resident CTAs of an SM
+constexpr int f_smem(int rows) { return (rows * HD + FK * FKS + FK * HD + rows * FPS) * 4; }
+constexpr size_t f_slot(int rows) { return (size_t)rows * (HD + 4); }   // outputs, maxima, sums
+
+__device__ __forceinline__ void cp16(float* dst, const float* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ float fex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-template <typename TA, typename TK>
-__global__ void __launch_bounds__(128) paged_plain_kernel(PagedAttn a) {
+template <int ROWS>
+__global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a, int grid_max) {
     pdl_wait();
     pdl_trigger();
+    constexpr int RT = ROWS / 16;      // rows of a thread
+    extern __shared__ __align__(16) float fs[];
+    float* Qs = fs;                    // [ROWS][128]
+    float* Ks = Qs + ROWS * HD;        // [64][132]
+    float* Vs = Ks + FK * FKS;         // [64][128]
+    float* Ps = Vs + FK * HD;          // [ROWS][68]
+    __shared__ int s_last;
     const PagedView& c = a.c;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int m = (int)(item / c.nq), h = (int)(item % c.nq);
-    if (m >= a.n_tokens) return;
-    int lo = 0, hi = c.n_seqs;   // the last sequence whose rows start at or before m
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.q_off[mid] <= m) lo = mid; else hi = mid;
-    }
-    const int s = lo, end = a.q_off[s + 1];
-    if (m >= end) return;
-    int ctx = a.ctx[s];
-    const int cap = c.max_pages << c.page_shift;
-    if (ctx > cap || end - a.q_off[s] > a.max_q || end > a.n_tokens) {
-        if (lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
-        ctx = min(ctx, cap);
-    }
-    const int n = ctx - (end - m) + 1;   // visible keys
-    const float4 q = ld4((const TA*)a.q + m * a.q_stride + h * HD + lane * 4);
-    float mx = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < n; ++j) {
-        int page = c.table[(int64_t)s * c.max_pages + (j >> c.page_shift)];
-        if (page < 0 || page >= c.n_pages) {
-            if (lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
-            continue;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+
+    const int tpi = ROWS / c.G;        // tokens of an item
+    const PagedRange R = paged_range<FT>(a, grid_max, 1, [&](const PagedSeq& q) { return c.nkv * seq_units<FK>(q, tpi); });
+    if (R.u0 >= R.u1) return;
+    const float sl2 = a.scale * 1.4426950408889634f;
+    int* counters = (int*)a.ws;
+    float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
+
+    Walk w;
+    walk_begin<FK>(w, a, R, tpi);
+    int end;
+    while (w.more && paged_cut(R, w.item0, w.item0 + w.nu, &end)) {
+        const PagedSeq q = w.q;
+        const int s = w.s, h = w.h, tok0 = w.item * tpi, ntok = min(tpi, q.n_new - tok0), rows = ntok * c.G;
+        const int vis = max(0, min(q.ctx, q.ctx - q.n_new + tok0 + ntok));   // keys that the last token sees
+        const int key0 = (w.u - w.item0) * FK, key1 = (int)min((long long)vis, (long long)(end - w.item0) * FK);
+        const int nt = key1 > key0 ? (key1 - key0 + FK - 1) / FK : 0;
+        const int32_t* table = c.table + (int64_t)s * c.max_pages;
+        const int pmask = (1 << c.page_shift) - 1;
+        auto load = [&](float* dst, int stride, const void* pool, int t) {
+#pragma unroll
+            for (int i = 0; i < FK * 32 / FT; ++i) {
+                const int row = (tid + i * FT) >> 5, ch = tid & 31, key = key0 + t * FK + row;
+                const float* src = (const float*)pool;
+                bool ok = key < key1;
+                if (ok) {
+                    const int page = __ldg(table + (key >> c.page_shift));
+                    if ((unsigned)page < (unsigned)c.n_pages)
+                        src += page * c.page_stride + (int64_t)h * c.head_stride + (int64_t)(key & pmask) * c.token_stride + ch * 4;
+                    else {
+                        ok = false;
+                        if (a.err) atomicOr(a.err, ERRB_BOUNDS);
+                    }
+                }
+                cp16(dst + row * stride + ch * 4, src, ok);
+            }
+            cp_commit();
+        };
+        __syncthreads();   // the segment before is done with the buffers
+        if (nt > 0) load(Ks, FKS, c.k, 0);
+        for (int i = tid; i < ROWS * 32; i += FT) {
+            const int r = i >> 5, tok = tok0 + r / c.G;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows)
+                v = *(const float4*)((const float*)a.q + (int64_t)(q.row0 + tok) * a.q_stride +
+                                     (int64_t)(h * c.G + r % c.G) * HD + (i & 31) * 4);
+            *(float4*)(Qs + r * HD + (i & 31) * 4) = v;
         }
-        const int64_t off = page * c.page_stride + (h / c.G) * c.head_stride +
-                            (int64_t)(j & ((1 << c.page_shift) - 1)) * c.token_stride + lane * 4;
-        const float4 k = ld4((const TK*)c.k + off), v = ld4((const TK*)c.v + off);
-        const float sc = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * a.scale;
-        const float nm = fmaxf(mx, sc), f = expf(mx - nm), p = expf(sc - nm);
-        l = l * f + p;
-        o.x = o.x * f + p * v.x; o.y = o.y * f + p * v.y; o.z = o.z * f + p * v.z; o.w = o.w * f + p * v.w;
-        mx = nm;
+        int lim[RT];
+        float m[RT], l[RT], o[RT][8];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int r = ty * RT + i;
+            lim[i] = r < rows ? min(q.ctx - q.n_new + tok0 + r / c.G + 1, key1) : 0;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[i][d] = 0.f;
+        }
+        for (int t = 0; t < nt; ++t) {
+            load(Vs, HD, c.v, t);
+            cp_wait<1>();
+            __syncthreads();
+            float x[RT][4];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < HD; d += 4) {
+                float4 qv[RT], kv[4];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) qv[i] = *(const float4*)(Qs + (ty * RT + i) * HD + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kv[j] = *(const float4*)(Ks + (tx + 16 * j) * FKS + d);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[i][j] = fmaf(qv[i].x, kv[j].x, x[i][j]);
+                        x[i][j] = fmaf(qv[i].y, kv[j].y, x[i][j]);
+                        x[i][j] = fmaf(qv[i].z, kv[j].z, x[i][j]);
+                        x[i][j] = fmaf(qv[i].w, kv[j].w, x[i][j]);
+                    }
+            }
+            const int kb = key0 + t * FK + tx;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                float top = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (kb + 16 * j >= lim[i]) x[i][j] = -INFINITY;
+                    top = fmaxf(top, x[i][j]);
+                }
+#pragma unroll
+                for (int z = 1; z < 16; z <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, z));
+                const float ref = top == -INFINITY ? 0.f : top * sl2;
+                const float f = fex2(m[i] * sl2 - ref);      // nothing seen before: 0
+                m[i] = top;
+                l[i] *= f;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) o[i][d] *= f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = fex2(fmaf(x[i][j], sl2, -ref));
+                    l[i] += p;
+                    Ps[(ty * RT + i) * FPS + tx + 16 * j] = p;
+                }
+            }
+            __syncthreads();   // weights are there, K is free
+            if (t + 1 < nt) {
+                load(Ks, FKS, c.k, t + 1);
+                cp_wait<1>();
+            } else {
+                cp_wait<0>();
+            }
+            __syncthreads();
+#pragma unroll 2
+            for (int k = 0; k < FK; k += 4) {
+                float4 p[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) p[i] = *(const float4*)(Ps + (ty * RT + i) * FPS + k);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const float4 v0 = *(const float4*)(Vs + (k + kk) * HD + tx * 4);
+                    const float4 v1 = *(const float4*)(Vs + (k + kk) * HD + 64 + tx * 4);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        const float pw = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                        o[i][0] = fmaf(pw, v0.x, o[i][0]); o[i][1] = fmaf(pw, v0.y, o[i][1]);
+                        o[i][2] = fmaf(pw, v0.z, o[i][2]); o[i][3] = fmaf(pw, v0.w, o[i][3]);
+                        o[i][4] = fmaf(pw, v1.x, o[i][4]); o[i][5] = fmaf(pw, v1.y, o[i][5]);
+                        o[i][6] = fmaf(pw, v1.z, o[i][6]); o[i][7] = fmaf(pw, v1.w, o[i][7]);
+                    }
+                }
+            }
+            __syncthreads();   // V and the weights are free
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int z = 1; z < 16; z <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], z);
+        auto store = [&](int r, const float (&v)[8], float sum) {
+            const int tok = tok0 + r / c.G;
+            const float f = sum > 0.f ? 1.f / sum : 0.f;
+            float* dst = (float*)a.out + (int64_t)(q.row0 + tok) * a.out_stride + (int64_t)(h * c.G + r % c.G) * HD + tx * 4;
+            *(float4*)dst = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+            *(float4*)(dst + 64) = make_float4(v[4] * f, v[5] * f, v[6] * f, v[7] * f);
+        };
+        if (w.u == w.item0 && end == w.item0 + w.nu) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                if (ty * RT + i < rows) store(ty * RT + i, o[i], l[i]);
+        } else {
+            const int ca = paged_cut_first(R, w.item0), cb = paged_cut_last(R, w.item0 + w.nu);
+            auto part = [&](int cc) { return parts + (size_t)(cc * 2 + (cc == ca ? 1 : 0)) * f_slot(ROWS); };
+            float* slot = part(blockIdx.x);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int r = ty * RT + i;
+                if (r >= rows) continue;
+                *(float4*)(slot + r * HD + tx * 4) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                *(float4*)(slot + r * HD + 64 + tx * 4) = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+                if (tx == 0) { slot[ROWS * HD + r] = m[i]; slot[ROWS * HD + ROWS + r] = l[i]; }
+            }
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                s_last = atomicAdd(&counters[ca], 1) == cb - ca;
+                if (s_last) counters[ca] = 0;
+                __threadfence();
+            }
+            __syncthreads();
+            if (s_last) {
+#pragma unroll 1
+                for (int i = 0; i < RT; ++i) {
+                    const int r = ty * RT + i;
+                    if (r >= rows) continue;
+                    float top = -INFINITY, sum = 0.f, v[8] = {};
+#pragma unroll 4
+                    for (int cc = ca; cc <= cb; ++cc) {
+                        const float* p = part(cc);
+                        const float pm = __ldcg(p + ROWS * HD + r), pl = __ldcg(p + ROWS * HD + ROWS + r);
+                        const float4 v0 = __ldcg((const float4*)(p + r * HD + tx * 4));
+                        const float4 v1 = __ldcg((const float4*)(p + r * HD + 64 + tx * 4));
+                        const float nm = fmaxf(top, pm), ref = nm == -INFINITY ? 0.f : nm;
+                        const float f0 = fex2((top - ref) * sl2), f1 = fex2((pm - ref) * sl2);
+                        top = nm;
+                        sum = sum * f0 + pl * f1;
+                        v[0] = v[0] * f0 + v0.x * f1; v[1] = v[1] * f0 + v0.y * f1;
+                        v[2] = v[2] * f0 + v0.z * f1; v[3] = v[3] * f0 + v0.w * f1;
+                        v[4] = v[4] * f0 + v1.x * f1; v[5] = v[5] * f0 + v1.y * f1;
+                        v[6] = v[6] * f0 + v1.z * f1; v[7] = v[7] * f0 + v1.w * f1;
+                    }
+                    store(r, v, sum);
+                }
+            }
+        }
+        if (end < w.item0 + w.nu) return;
+        walk_step<FK>(w, a, R, tpi);
     }
-    const float r = l > 0.f ? 1.f / l : 0.f;
-    TA* dst = (TA*)a.out + m * a.out_stride + h * HD + lane * 4;
-    dst[0] = from_f<TA>(o.x * r); dst[1] = from_f<TA>(o.y * r); dst[2] = from_f<TA>(o.z * r); dst[3] = from_f<TA>(o.w * r);
+}
+
+template <int ROWS>
+cudaError_t launch_f32(const PagedAttn& a, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(paged_f32_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, f_smem(ROWS));
+    if (e != cudaSuccess) return e;
+    const int grid = min(device_sm_count(), 160) * F_CTAS;
+    return launch_pdl(paged_f32_kernel<ROWS>, grid, FT, f_smem(ROWS), st, a, grid);
 }
 
 }  // namespace
 
-size_t paged_workspace_bytes() { return PAGED_COUNTER_BYTES + max(paged_decode_ws(), paged_chunk_ws()); }
+size_t paged_workspace_bytes() {
+    return PAGED_COUNTER_BYTES + max(max(paged_decode_ws(), paged_chunk_ws()), (size_t)160 * F_CTAS * 2 * f_slot(64) * sizeof(float));
+}
 
 cudaError_t launch_paged_attention(const PagedAttn& a, cudaStream_t st) {
-    if (paged_decode_takes(a)) return launch_paged_decode(a, st);
-    if (a.kv == Q3_BF16) return launch_paged_chunk(a, st);
-    const int64_t blocks = ((int64_t)a.n_tokens * a.c.nq + 3) / 4;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (a.act == Q3_BF16) return launch_pdl(paged_plain_kernel<bf16, bf16>, (unsigned)blocks, 128, 0, st, a);
-    if (a.kv == Q3_BF16) return launch_pdl(paged_plain_kernel<float, bf16>, (unsigned)blocks, 128, 0, st, a);
-    return launch_pdl(paged_plain_kernel<float, float>, (unsigned)blocks, 128, 0, st, a);
+    if (a.kv == Q3_F32) return (int64_t)a.max_q * a.c.G <= 16 ? launch_f32<16>(a, st) : launch_f32<64>(a, st);
+    return paged_decode_takes(a) ? launch_paged_decode(a, st) : launch_paged_chunk(a, st);
 }
 
 }  // namespace q3

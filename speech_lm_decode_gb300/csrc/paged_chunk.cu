@@ -181,59 +181,6 @@ struct Seg {
     int ca, cb;           // CTAs of the item
 };
 
-struct Walk {
-    PagedSeq q;
-    int u, item0;         // unit to begin at, first unit of the item
-    int s, h, item, nu;   // nu: units of the item
-    bool more;
-};
-
-// tokens of an item (tpi) and the key tiles that item i of a sequence reads
-__device__ __forceinline__ int item_units(const PagedSeq& q, int tpi, int i) {
-    const int last = min(q.n_new, (i + 1) * tpi);
-    const int vis = min(q.ctx - q.n_new + last, q.ctx);
-    return max(1, (vis + CT - 1) / CT);
-}
-__device__ __forceinline__ long long seq_units(const PagedSeq& q, int tpi) {
-    long long n = 0;
-    for (int i = 0; i * tpi < q.n_new; ++i) n += item_units(q, tpi, i);
-    return n;
-}
-
-// on to the next item
-__device__ __forceinline__ void walk_step(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
-    w.item0 += w.nu;
-    w.u = w.item0;
-    if (w.item0 >= R.u1) { w.more = false; return; }
-    if (++w.item * tpi >= w.q.n_new) {
-        w.item = 0;
-        if (++w.h == a.c.nkv) {
-            w.h = 0;
-            do { w.q = paged_seq(a, ++w.s, false); } while (w.q.n_new <= 0);
-        }
-    }
-    w.nu = item_units(w.q, tpi, w.item);
-}
-__device__ __forceinline__ void walk_begin(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
-    w.s = R.s;
-    w.q = R.q;
-    w.more = true;
-    const int per = (int)seq_units(w.q, tpi);
-    int rel = R.u0 - R.start;
-    w.h = rel / per;
-    rel -= w.h * per;
-    w.item0 = R.start + w.h * per;
-    w.item = 0;
-    for (;;) {
-        w.nu = item_units(w.q, tpi, w.item);
-        if (rel < w.nu) break;
-        rel -= w.nu;
-        w.item0 += w.nu;
-        ++w.item;
-    }
-    w.u = paged_begin(R, w.item0, w.item0 + w.nu);
-    if (w.u == w.item0 + w.nu) walk_step(w, a, R, tpi);
-}
 // the part of the walk's item that this CTA takes
 __device__ __forceinline__ bool walk_seg(Walk& w, const PagedRange& R, int tpt, int tpi, Seg& g) {
     int end;
@@ -269,7 +216,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     const int tpt = CT / c.G, tpi = F32 ? tpt : 2 * tpt;   // tokens of a tile, of an item
 
     const PagedRange R = paged_range<C_THREADS>(a, gridDim.x, C_MIN_UNITS,
-                                                [&](const PagedSeq& q) { return c.nkv * seq_units(q, tpi); });
+                                                [&](const PagedSeq& q) { return c.nkv * seq_units<CT>(q, tpi); });
     if (R.u0 >= R.u1) return;
 
     if (threadIdx.x == 0) {
@@ -292,7 +239,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     const uint32_t tmem = sm.tmem;
 
     Walk w;
-    walk_begin(w, a, R, tpi);
+    walk_begin<CT>(w, a, R, tpi);
     Seg g;
 
     if (warp == 0) {
@@ -329,7 +276,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 load(&mapV, g.kt0 + i);
                 if (i + lead < g.n) load(&mapK, g.kt0 + i + lead);
             }
-            if (w.more) walk_step(w, a, R, tpi);
+            if (w.more) walk_step<CT>(w, a, R, tpi);
         }
         // given up: nothing may still be writing this CTA's shared memory when it leaves
         if (*(volatile int*)&sm.dead)
@@ -437,7 +384,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 if (ok && lane == 0) commit(&sm.o_full);
                 __syncwarp();
             }
-            if (w.more) walk_step(w, a, R, tpi);
+            if (w.more) walk_step<CT>(w, a, R, tpi);
         }
         if (!ok && lane == 0) {   // products in flight end before the tensor memory goes
             commit(&sm.drain);
@@ -691,7 +638,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                 }
             }
-            if (w.more) walk_step(w, a, R, tpi);
+            if (w.more) walk_step<CT>(w, a, R, tpi);
         }
     }
     __syncwarp();

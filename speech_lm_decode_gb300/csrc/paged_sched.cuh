@@ -137,6 +137,65 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int
     return r;
 }
 
+// Items of tpi tokens (of one kv head), units of KEYS keys that their last token
+// sees at most; in the order sequence, head, item.
+struct Walk {
+    PagedSeq q;
+    int u, item0;         // unit to begin at, first unit of the item
+    int s, h, item, nu;   // nu: units of the item
+    bool more;
+};
+
+// tokens of an item (tpi) and the key tiles that item i of a sequence reads
+template <int KEYS>
+__device__ __forceinline__ int item_units(const PagedSeq& q, int tpi, int i) {
+    const int last = min(q.n_new, (i + 1) * tpi);
+    const int vis = min(q.ctx - q.n_new + last, q.ctx);
+    return max(1, (vis + KEYS - 1) / KEYS);
+}
+template <int KEYS>
+__device__ __forceinline__ long long seq_units(const PagedSeq& q, int tpi) {
+    long long n = 0;
+    for (int i = 0; i * tpi < q.n_new; ++i) n += item_units<KEYS>(q, tpi, i);
+    return n;
+}
+
+// on to the next item
+template <int KEYS>
+__device__ __forceinline__ void walk_step(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
+    w.item0 += w.nu;
+    w.u = w.item0;
+    if (w.item0 >= R.u1) { w.more = false; return; }
+    if (++w.item * tpi >= w.q.n_new) {
+        w.item = 0;
+        if (++w.h == a.c.nkv) {
+            w.h = 0;
+            do { w.q = paged_seq(a, ++w.s, false); } while (w.q.n_new <= 0);
+        }
+    }
+    w.nu = item_units<KEYS>(w.q, tpi, w.item);
+}
+template <int KEYS>
+__device__ __forceinline__ void walk_begin(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
+    w.s = R.s;
+    w.q = R.q;
+    w.more = true;
+    const int per = (int)seq_units<KEYS>(w.q, tpi);
+    int rel = R.u0 - R.start;
+    w.h = rel / per;
+    rel -= w.h * per;
+    w.item0 = R.start + w.h * per;
+    w.item = 0;
+    for (;;) {
+        w.nu = item_units<KEYS>(w.q, tpi, w.item);
+        if (rel < w.nu) break;
+        rel -= w.nu;
+        w.item0 += w.nu;
+        ++w.item;
+    }
+    w.u = paged_begin(R, w.item0, w.item0 + w.nu);
+    if (w.u == w.item0 + w.nu) walk_step<KEYS>(w, a, R, tpi);
+}
 // Workspace of the paged attention: counters, then two partial slots a CTA.
 constexpr int PAGED_MAX_CTAS = 1024;
 constexpr size_t PAGED_COUNTER_BYTES = Q3PAGED_COUNTER_BYTES;
