@@ -45,11 +45,26 @@ constexpr int c_stages(bool f32) { return f32 ? 4 : 5; }
 constexpr int c_qbytes(bool f32) { return f32 ? 3 * STAGE : 2 * STAGE; }
 constexpr size_t C_SLOT = (size_t)2 * CT * (HD + 2);   // floats of a partial
 
+// One cut of an item that a CTA works on.
+struct Seg {
+    int s, h;             // sequence, kv head
+    int tok0, ntok;       // first token (of the sequence's new ones) and tokens of the item
+    int n;                // key tiles of this cut (0: the item sees no key)
+    int kt0;              // first of them
+    bool two;             // two tiles of rows
+    bool whole;           // the cut is the item
+    int ca, cb;           // CTAs of the item
+};
+
 struct ChunkSmem {
     uint64_t full[5], empty[5], s_full[2], p_full[2], q_full, o_full, drain;
     uint32_t tmem;
     int dead, last;
     float m[CT], l[CT];      // slot 1's statistics for slot 0
+    PagedRange range;        // the softmax warps' walk, kept here to save them the registers
+    Walk walk;
+    Seg seg;
+    int more;
 };
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -89,18 +104,30 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar)) : "memory");
 }
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int acc) {
+// One product of the chain; a, b: low words of the operands' descriptors (a of
+// umma_ts: an address in tensor memory).  The upper words are constants, so
+// that an instruction's operands are one uniform add away from the last one's.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HI) : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(DESC_HI) : "memory");
 }
+// one thread of the warp, always the same
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+// a value that all lanes have, made known as such
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
 }
@@ -119,14 +146,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {   // and waits for it
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-        ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-          "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-          "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-          "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr) : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -147,14 +173,11 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Descriptor of a tile in shared memory, rows of 128 bytes, 128-byte swizzle.
-// K-major (Q, K): eight-row groups 1024 bytes apart.  MN-major (V: the 128
-// bytes run along the head): eight-key groups 1024 bytes apart, the second half
-// of the head `lead` bytes on.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t lead) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Low word of the descriptor of a tile in shared memory, rows of 128 bytes,
+// 128-byte swizzle.  K-major (Q, K): eight-row groups 1024 bytes apart.
+// MN-major (V: the 128 bytes run along the head): eight-key groups 1024 bytes
+// apart, the second half of the head `lead` bytes on.
+__device__ __forceinline__ uint32_t tile_desc(uint32_t saddr, uint32_t lead) { return (saddr >> 4) | (lead >> 4) << 16; }
 // fp32 D, bf16 A and B, M = N = 128; bit 16: B is MN-major
 constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(CT >> 3) << 17) | ((uint32_t)(CT >> 4) << 24);
 constexpr uint32_t IDESC_V = IDESC | (1u << 16);
@@ -164,23 +187,30 @@ __device__ __forceinline__ float ex2f(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// two fp32 values side by side: one instruction works on both
+using f2c = unsigned long long;
+__device__ __forceinline__ f2c pair(float a, float b) {
+    f2c r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(f2c v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2c fma_pair(f2c a, f2c b, f2c c) {
+    f2c r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2c add_pair(f2c a, f2c b) {
+    f2c r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *(const uint32_t*)&v;
 }
 
 // ------------------------------------------------------------------ items
-// One cut of an item that a CTA works on.
-struct Seg {
-    int s, h;             // sequence, kv head
-    int tok0, ntok;       // first token (of the sequence's new ones) and tokens of the item
-    int n;                // key tiles of this cut (0: the item sees no key)
-    int kt0;              // first of them
-    bool two;             // two tiles of rows
-    bool whole;           // the cut is the item
-    int ca, cb;           // CTAs of the item
-};
-
 // the part of the walk's item that this CTA takes
 __device__ __forceinline__ bool walk_seg(Walk& w, const PagedRange& R, int tpt, int tpi, Seg& g) {
     int end;
@@ -212,7 +242,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     unsigned char* qs = base;                       // Q tiles (bf16: per slot; fp32: per part)
     unsigned char* ring = base + c_qbytes(F32);
     const PagedView& c = a.c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tpt = CT / c.G, tpi = F32 ? tpt : 2 * tpt;   // tokens of a tile, of an item
 
     const PagedRange R = paged_range<C_THREADS>(a, gridDim.x, C_MIN_UNITS,
@@ -240,8 +270,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
 
     Walk w;
     walk_begin<CT>(w, a, R, tpi);
-    Seg g;
+    if (threadIdx.x == 128) { sm.range = R; sm.walk = w; }
 
+    // registers: 384 threads x 168 at launch = 128 x 72 + 256 x 216 (the launcher checks the 168)
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    Seg g;
     if (warp == 0) {
         // ---------------------------------------------------------- K and V tiles
         int cnt = 0, issued = 0;
@@ -297,36 +331,37 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
         };
-        auto release = [&](int i) { if (ok && lane == 0) commit(&sm.empty[i % ST]); };
+        auto release = [&](int i) {
+            if (ok && elect_one()) commit(&sm.empty[i % ST]);
+            __syncwarp();
+        };
         // S of slot t from the K tile of ring entry i
         auto scores = [&](int t, int i) {
-            if (ok && lane == 0) {
-                const uint32_t kb = ring0 + (i % ST) * STAGE;
+            const uint32_t kd = uniform(tile_desc(ring0 + (i % ST) * STAGE, 16));
+            const uint32_t qd = uniform(tile_desc(q0 + (!F32 && g.two ? t : 0) * STAGE, 16)), d = uniform(tmem + t * CT);
+            if (ok && elect_one()) {
 #pragma unroll
-                for (int p = 0; p < QP; ++p) {
-                    const uint32_t qb = q0 + (F32 ? p : (g.two ? t : 0)) * STAGE;
+                for (int p = 0; p < QP; ++p)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t off = (ks >> 2) * (STAGE / 2) + (ks & 3) * 32;
-                        umma_ss(tmem + t * CT, tile_desc(qb + off, 16), tile_desc(kb + off, 16), IDESC, (p | ks) != 0);
+                        const uint32_t off = ((ks >> 2) * (STAGE / 2) + (ks & 3) * 32) >> 4;
+                        umma_ss(d, qd + p * (STAGE >> 4) + off, kd + off, IDESC, (p | ks) != 0);
                     }
-                }
                 commit(&sm.s_full[t]);
             }
             __syncwarp();
         };
         // O of slot t += P V
         auto outputs = [&](int t, int i, bool acc) {
-            if (ok && lane == 0) {
-                const uint32_t vb = ring0 + (i % ST) * STAGE;
+            const uint32_t vd = uniform(tile_desc(ring0 + (i % ST) * STAGE, STAGE / 2));
+            const uint32_t pa = uniform(tmem + t * CT), d = uniform(tmem + 2 * CT + t * CT), first = uniform(acc);
+            if (ok && elect_one()) {
 #pragma unroll
                 for (int p = 0; p < PP; ++p)
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t pa = F32 ? 32 * (ks >> 1) + 8 * (ks & 1) + 16 * p : 8 * ks;
-                        umma_ts(tmem + 2 * CT + t * CT, tmem + t * CT + pa, tile_desc(vb + ks * 2048, STAGE / 2), IDESC_V,
-                                (acc || (p | ks) != 0) ? 1 : 0);
-                    }
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_ts(d, pa + (F32 ? 32 * (ks >> 1) + 8 * (ks & 1) + 16 * p : 8 * ks), vd + ks * (2048 >> 4), IDESC_V,
+                                (p | ks) != 0 ? 1u : first);
             }
             __syncwarp();
         };
@@ -381,16 +416,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                     cnt += more ? 2 : 1;
                 }
-                if (ok && lane == 0) commit(&sm.o_full);
+                if (ok && elect_one()) commit(&sm.o_full);
                 __syncwarp();
             }
             if (w.more) walk_step<CT>(w, a, R, tpi);
         }
-        if (!ok && lane == 0) {   // products in flight end before the tensor memory goes
+        if (!ok && elect_one()) {   // products in flight end before the tensor memory goes
             commit(&sm.drain);
             bar_wait(&sm.drain, 0, sm, a.err, false);
         }
-    } else if (warp >= 4) {
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---------------------------------------------------------- softmax
         const int t = warp >= 8 ? 1 : 0;
         const int r = (threadIdx.x & 127);                 // this thread's row of a tile
@@ -401,13 +438,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
         int sc = 0, oc = 0;
         bool ok = true;
-        while (walk_seg(w, R, tpt, tpi, g)) {
+        for (;;) {
             // both slots are done with Q and with the tensor memory of the item before
             wg_sync(1);
+            if (threadIdx.x == 128) sm.more = walk_seg(sm.walk, sm.range, tpt, tpi, sm.seg);
+            wg_sync(1);
+            if (!sm.more) break;
+            const Seg& g = sm.seg;
+            const PagedSeq& wq = sm.walk.q;
             const int tile = g.two ? t : 0;
             const int tok = g.tok0 + tile * tpt + r / c.G, head = g.h * c.G + r % c.G;
             const bool live = r < tpt * c.G && tok < g.tok0 + g.ntok;
-            const int lim = live ? min(w.q.ctx - w.q.n_new + tok + 1, w.q.ctx) : 0;
+            const int lim = live ? min(wq.ctx - wq.n_new + tok + 1, wq.ctx) : 0;
             float mx = -INFINITY, l = 0.f;
             if (g.n > 0) {
                 // ---- query rows: 16 threads a row, 16 bytes of bf16 each
@@ -416,7 +458,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     const int row = first + (i >> 4), ch = i & 15;
                     const int rt = g.tok0 + tile * tpt + row / c.G;
                     const bool there = row < tpt * c.G && rt < g.tok0 + g.ntok;
-                    const TA* src = (const TA*)a.q + (int64_t)(w.q.row0 + (there ? rt : 0)) * a.q_stride +
+                    const TA* src = (const TA*)a.q + (int64_t)(wq.row0 + (there ? rt : 0)) * a.q_stride +
                                     (int64_t)(g.h * c.G + (there ? row % c.G : 0)) * HD + ch * 8;
                     const uint32_t off = (uint32_t)((ch >> 3) * (STAGE / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
                     if constexpr (F32) {
@@ -451,21 +493,28 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 ok = __all_sync(0xffffffffu, ok);
                 fence_after();
                 const int seen = lim - k0;                         // columns that the row sees
-                const bool masked = __any_sync(0xffffffffu, seen < CT);
-                float top = -INFINITY;
+                uint32_t x[4][32];
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t x[32];
-                    tmem_ld32(tS + 32 * cc, x);
-                    tmem_wait_ld(x);
-                    if (masked) {
+                for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, x[cc]);
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(x[cc]);
+                if (__any_sync(0xffffffffu, seen < CT)) {
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (32 * cc + i >= seen) x[i] = 0xff800000u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[i]));
+                            if (32 * cc + i >= seen) x[cc][i] = 0xff800000u;
                 }
+                float tops[4];
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {
+                    tops[cc] = __uint_as_float(x[cc][0]);
+#pragma unroll
+                    for (int i = 1; i < 31; i += 2)
+                        tops[cc] = fmaxf(fmaxf(tops[cc], __uint_as_float(x[cc][i])), __uint_as_float(x[cc][i + 1]));
+                    tops[cc] = fmaxf(tops[cc], __uint_as_float(x[cc][31]));
+                }
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // The maximum that the weights refer to moves only when a score passes it by 2^8.
                 const bool grew = top > mx + slack;
                 if (__any_sync(0xffffffffu, grew)) {
@@ -475,47 +524,43 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     l *= f;
                     if (j > 0) {
 #pragma unroll 1
-                        for (int cc = 0; cc < 4; ++cc) {
-                            uint32_t x[32];
-                            tmem_ld32(tO + 32 * cc, x);
-                            tmem_wait_ld(x);
+                        for (int cc = 0; cc < 8; ++cc) {
+                            uint32_t y[16];
+                            tmem_ld16(tO + 16 * cc, y);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                            tmem_st32(tO + 32 * cc, x);
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                            tmem_st16(tO + 16 * cc, y);
                         }
                     }
                 }
                 const float ref = mx == -INFINITY ? 0.f : -mx * sl2;
+                const f2c sl = pair(sl2, sl2), rf = pair(ref, ref);
+                f2c sums = pair(0.f, 0.f);
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t x[32], hi[16];
-                    tmem_ld32(tS + 32 * cc, x);
-                    tmem_wait_ld(x);
-                    if (masked) {
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * cc + i >= seen) x[i] = 0xff800000u;
+                    for (int i = 0; i < 16; ++i) {
+                        float p0, p1;
+                        unpair(fma_pair(pair(__uint_as_float(x[cc][2 * i]), __uint_as_float(x[cc][2 * i + 1])), sl, rf), p0, p1);
+                        p0 = ex2f(p0);
+                        p1 = ex2f(p1);
+                        sums = add_pair(sums, pair(p0, p1));
+                        hi[i] = pack_bf16(p0, p1);
+                        if constexpr (F32)
+                            lo[i] = pack_bf16(p0 - __uint_as_float(hi[i] << 16), p1 - __uint_as_float(hi[i] & 0xffff0000u));
                     }
-                    float p[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) p[i] = ex2f(fmaf(__uint_as_float(x[i]), sl2, ref));
-                    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) { s0 += p[i]; s1 += p[i + 1]; }
-                    l += s0 + s1;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) hi[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
                     if constexpr (F32) {
-                        uint32_t lo[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            lo[i] = pack_bf16(p[2 * i] - __uint_as_float(hi[i] << 16),
-                                              p[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u));
                         tmem_st16(tS + 32 * cc, hi);
                         tmem_st16(tS + 32 * cc + 16, lo);
                     } else {
                         tmem_st16(tS + 16 * cc, hi);
                     }
+                }
+                {
+                    float s0, s1;
+                    unpair(sums, s0, s1);
+                    l += s0 + s1;
                 }
                 tmem_wait_st();
                 fence_before();
@@ -545,7 +590,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             }
             const bool mine = g.two || t == 0;
             const bool second = !g.two && g.n > 1;     // slot 1 has an output
-            TA* dst = (TA*)a.out + (int64_t)(w.q.row0 + tok) * a.out_stride + (int64_t)head * HD;
+            TA* dst = (TA*)a.out + (int64_t)(wq.row0 + tok) * a.out_stride + (int64_t)head * HD;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             auto put = [&](int col, const float (&v)[32]) {      // 32 values of the row
                 if (!live) return;
@@ -638,7 +683,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                 }
             }
-            if (w.more) walk_step<CT>(w, a, R, tpi);
+            wg_sync(1);
+            if (threadIdx.x == 128 && sm.walk.more) walk_step<CT>(sm.walk, a, sm.range, tpi);
         }
     }
     __syncwarp();
@@ -682,6 +728,12 @@ cudaError_t launch_t(const PagedAttn& a, cudaStream_t st) {
     // a per-device attribute: set on every call (a host-side table lookup)
     cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<TA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // the kernel's warps redistribute exactly this many registers; with fewer they would wait for ever
+    static const bool regs_ok = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, paged_chunk_kernel<TA>) == cudaSuccess && at.numRegs == 168;
+    }();
+    if (!regs_ok) return cudaErrorInvalidConfiguration;
     const int grid = min(device_sm_count(), C_MAX_CTAS);
     paged_chunk_kernel<TA><<<grid, C_THREADS, smem, st>>>(mk, mv, a);
     return cudaGetLastError();
