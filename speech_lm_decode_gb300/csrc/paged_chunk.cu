@@ -251,7 +251,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) { bar_init(&sm.full[i], 1); bar_init(&sm.empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { bar_init(&sm.s_full[i], 1); bar_init(&sm.p_full[i], CT); }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sm.s_full[i], 1);
+            bar_init(&sm.p_full[i], CT / 32);   // a warp each
+        }
         bar_init(&sm.q_full, 2 * CT);
         bar_init(&sm.o_full, 1);
         bar_init(&sm.drain, 1);
@@ -351,10 +354,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             }
             __syncwarp();
         };
-        // O of slot t += P V
+        // O of slot t += P V, once P is there
         auto outputs = [&](int t, int i, bool acc) {
             const uint32_t vd = uniform(tile_desc(ring0 + (i % ST) * STAGE, STAGE / 2));
             const uint32_t pa = uniform(tmem + t * CT), d = uniform(tmem + 2 * CT + t * CT), first = uniform(acc);
+            p_ready(t);
             if (ok && elect_one()) {
 #pragma unroll
                 for (int p = 0; p < PP; ++p)
@@ -395,21 +399,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 for (int i = 0; i < g.n; ++i) {
                     const int v = cnt, k = cnt + 1;
                     const bool more = i + lead < g.n;
+                    full(v);
+                    clear_tail(g.kt0 + i, v);
                     if (g.two) {
-                        p_ready(0);
-                        full(v);
-                        clear_tail(g.kt0 + i, v);
                         outputs(0, v, i > 0);
                         if (more) { full(k); scores(0, k); }
-                        p_ready(1);
                         outputs(1, v, i > 0);
                         release(v);
                         if (more) { scores(1, k); release(k); }
                     } else {
                         const int t = i & 1;
-                        p_ready(t);
-                        full(v);
-                        clear_tail(g.kt0 + i, v);
                         outputs(t, v, i > 1);
                         release(v);
                         if (more) { full(k); scores(t, k); release(k); }
@@ -452,34 +451,45 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const int lim = live ? min(wq.ctx - wq.n_new + tok + 1, wq.ctx) : 0;
             float mx = -INFINITY, l = 0.f;
             if (g.n > 0) {
-                // ---- query rows: 16 threads a row, 16 bytes of bf16 each
-                const int first = g.two ? 0 : t * 64, count = g.two ? CT : 64;
-                for (int i = r; i < count * 16; i += CT) {
-                    const int row = first + (i >> 4), ch = i & 15;
-                    const int rt = g.tok0 + tile * tpt + row / c.G;
-                    const bool there = row < tpt * c.G && rt < g.tok0 + g.ntok;
-                    const TA* src = (const TA*)a.q + (int64_t)(wq.row0 + (there ? rt : 0)) * a.q_stride +
-                                    (int64_t)(g.h * c.G + (there ? row % c.G : 0)) * HD + ch * 8;
-                    const uint32_t off = (uint32_t)((ch >> 3) * (STAGE / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-                    if constexpr (F32) {
-                        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                        const float4 f0 = there ? *(const float4*)src : z, f1 = there ? *(const float4*)(src + 4) : z;
-                        float x[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                // ---- query rows: 16 threads a row, 8 values each, loads of a batch in flight together
+                constexpr int NB = F32 ? 4 : 8, V4 = F32 ? 2 : 1;
+                const int first = g.two ? 0 : t * 64, count = g.two ? CT : 64, ch = r & 15;
+                for (int b0 = 0; b0 < count / 8; b0 += NB) {
+                    uint4 raw[NB][V4];
 #pragma unroll
-                        for (int p = 0; p < 3; ++p) {
-                            uint32_t d[4];
+                    for (int b = 0; b < NB; ++b) {
+                        const int row = first + (r >> 4) + 8 * (b0 + b), rt = g.tok0 + tile * tpt + row / c.G;
+                        const bool there = row < tpt * c.G && rt < g.tok0 + g.ntok;
+                        const uint4* src = (const uint4*)((const TA*)a.q + (int64_t)(wq.row0 + (there ? rt : 0)) * a.q_stride +
+                                                          (int64_t)(g.h * c.G + (there ? row % c.G : 0)) * HD + ch * 8);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float h0 = __bfloat162float(__float2bfloat16_rn(x[2 * j]));
-                                const float h1 = __bfloat162float(__float2bfloat16_rn(x[2 * j + 1]));
-                                d[j] = pack_bf16(h0, h1);
-                                x[2 * j] -= h0;
-                                x[2 * j + 1] -= h1;
+                        for (int j = 0; j < V4; ++j) raw[b][j] = there ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const int row = first + (r >> 4) + 8 * (b0 + b);
+                        const uint32_t off = (uint32_t)((ch >> 3) * (STAGE / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+                        if constexpr (F32) {
+                            float x[8];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                x[4 * j] = __uint_as_float(raw[b][j].x); x[4 * j + 1] = __uint_as_float(raw[b][j].y);
+                                x[4 * j + 2] = __uint_as_float(raw[b][j].z); x[4 * j + 3] = __uint_as_float(raw[b][j].w);
                             }
-                            *(uint4*)(qs + (size_t)p * STAGE + off) = make_uint4(d[0], d[1], d[2], d[3]);
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) {
+                                uint32_t d[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    d[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                                    x[2 * j] -= __uint_as_float(d[j] << 16);
+                                    x[2 * j + 1] -= __uint_as_float(d[j] & 0xffff0000u);
+                                }
+                                *(uint4*)(qs + (size_t)p * STAGE + off) = make_uint4(d[0], d[1], d[2], d[3]);
+                            }
+                        } else {
+                            *(uint4*)(qs + (size_t)tile * STAGE + off) = raw[b][0];
                         }
-                    } else {
-                        *(uint4*)(qs + (size_t)tile * STAGE + off) = there ? *(const uint4*)src : make_uint4(0, 0, 0, 0);
                     }
                 }
                 fence_async_smem();
@@ -557,14 +567,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         tmem_st16(tS + 16 * cc, hi);
                     }
                 }
+                tmem_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sm.p_full[t]);
                 {
                     float s0, s1;
                     unpair(sums, s0, s1);
                     l += s0 + s1;
                 }
-                tmem_wait_st();
-                fence_before();
-                bar_arrive(&sm.p_full[t]);
             }
             // ---- the item's (or the cut's) output
             float l1 = 0.f, f0 = 1.f, f1 = 0.f;
@@ -650,33 +661,43 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     __threadfence();
                 }
                 wg_sync(3);
-                if (sm.last && mine) {
-                    float m = -INFINITY;
-                    for (int cc = g.ca; cc <= g.cb; ++cc)
-                        m = fmaxf(m, __ldcg(parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT + 2 * CT * HD + prow));
+                if (sm.last) {
+                    // every row by its thread; with one tile of rows, slot 1's thread takes the upper half of the head
+                    const int mrow = tile * CT + r, b0 = g.two ? 0 : 2 * t, b1 = g.two ? 4 : b0 + 2;
+                    auto part = [&](int cc) { return parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT; };
+                    float m = -INFINITY, sum = 0.f;
+                    for (int cc = g.ca; cc <= g.cb; ++cc) m = fmaxf(m, __ldcg(part(cc) + 2 * CT * HD + mrow));
                     const float ms = m == -INFINITY ? 0.f : m;
-                    float sum = 0.f;
+#pragma unroll 4
+                    for (int cc = g.ca; cc <= g.cb; ++cc)
+                        sum += ex2f((__ldcg(part(cc) + 2 * CT * HD + mrow) - ms) * sl2) * __ldcg(part(cc) + 2 * CT * HD + 2 * CT + mrow);
+                    const float rs = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
+                    for (int b = b0; b < b1; ++b) {
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                        sum = 0.f;
 #pragma unroll 1
-                        for (int cc = g.ca; cc <= g.cb; ++cc) {
-                            const float* p = parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT;
-                            const float f = ex2f((__ldcg(p + 2 * CT * HD + prow) - ms) * sl2);
-                            sum += f * __ldcg(p + 2 * CT * HD + 2 * CT + prow);
+                        for (int cc = g.ca; cc <= g.cb; cc += 2) {
+                            const bool both = cc < g.cb;
+                            const float* p0 = part(cc);
+                            const float* p1 = part(both ? cc + 1 : cc);
+                            float4 z0[8], z1[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 z = __ldcg((const float4*)(p + ((size_t)(8 * b + i) * 2 * CT + prow) * 4));
-                                v[4 * i] = fmaf(z.x, f, v[4 * i]);
-                                v[4 * i + 1] = fmaf(z.y, f, v[4 * i + 1]);
-                                v[4 * i + 2] = fmaf(z.z, f, v[4 * i + 2]);
-                                v[4 * i + 3] = fmaf(z.w, f, v[4 * i + 3]);
+                                z0[i] = __ldcg((const float4*)(p0 + ((size_t)(8 * b + i) * 2 * CT + mrow) * 4));
+                                z1[i] = __ldcg((const float4*)(p1 + ((size_t)(8 * b + i) * 2 * CT + mrow) * 4));
+                            }
+                            const float w0 = ex2f((__ldcg(p0 + 2 * CT * HD + mrow) - ms) * sl2);
+                            const float w1 = both ? ex2f((__ldcg(p1 + 2 * CT * HD + mrow) - ms) * sl2) : 0.f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                v[4 * i] = fmaf(z1[i].x, w1, fmaf(z0[i].x, w0, v[4 * i]));
+                                v[4 * i + 1] = fmaf(z1[i].y, w1, fmaf(z0[i].y, w0, v[4 * i + 1]));
+                                v[4 * i + 2] = fmaf(z1[i].z, w1, fmaf(z0[i].z, w0, v[4 * i + 2]));
+                                v[4 * i + 3] = fmaf(z1[i].w, w1, fmaf(z0[i].w, w0, v[4 * i + 3]));
                             }
                         }
-                        const float rs = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] *= rs;
                         put(32 * b, v);
