@@ -20,6 +20,7 @@ namespace {
 
 constexpr int FT = 256;            // threads
 constexpr int FK = 64;             // keys of a tile and of a unit
+constexpr int F_OVER = 0;          // units that an item costs besides its keys (1 and 2 were slower)
 constexpr int FKS = HD + 4;        // row of K in shared memory, floats
 constexpr int FPS = FK + 4;        // row of the weights
 constexpr int F_CTAS = 2;          // resident CTAs of an SM
@@ -53,20 +54,21 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
 
     const int tpi = ROWS / c.G;        // tokens of an item
-    const PagedRange R = paged_range<FT>(a, grid_max, 1, [&](const PagedSeq& q) { return c.nkv * seq_units<FK>(q, tpi); });
+    const PagedRange R = paged_range<FT>(a, grid_max, F_OVER + 1, F_OVER, [&](const PagedSeq& q) { return c.nkv * seq_units<FK, F_OVER>(q, tpi); });
     if (R.u0 >= R.u1) return;
     const float sl2 = a.scale * 1.4426950408889634f;
     int* counters = (int*)a.ws;
     float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
 
     Walk w;
-    walk_begin<FK>(w, a, R, tpi);
+    walk_begin<FK, F_OVER>(w, a, R, tpi);
     int end;
     while (w.more && paged_cut(R, w.item0, w.item0 + w.nu, &end)) {
         const PagedSeq q = w.q;
         const int s = w.s, h = w.h, tok0 = w.item * tpi, ntok = min(tpi, q.n_new - tok0), rows = ntok * c.G;
         const int vis = max(0, min(q.ctx, q.ctx - q.n_new + tok0 + ntok));   // keys that the last token sees
-        const int key0 = (w.u - w.item0) * FK, key1 = (int)min((long long)vis, (long long)(end - w.item0) * FK);
+        const int key0 = w.u == w.item0 ? 0 : (w.u - w.item0 - F_OVER) * FK;
+        const int key1 = (int)min((long long)vis, (long long)(end - w.item0 - F_OVER) * FK);
         const int nt = key1 > key0 ? (key1 - key0 + FK - 1) / FK : 0;
         const int32_t* table = c.table + (int64_t)s * c.max_pages;
         const int pmask = (1 << c.page_shift) - 1;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
             }
         }
         if (end < w.item0 + w.nu) return;
-        walk_step<FK>(w, a, R, tpi);
+        walk_step<FK, F_OVER>(w, a, R, tpi);
     }
 }
 

@@ -39,7 +39,8 @@ constexpr int CT = 128;                    // rows of a tile, keys of a unit
 constexpr int STAGE = CT * HD * 2;         // bytes of a K or V tile
 constexpr int C_THREADS = 384;
 constexpr int C_MAX_CTAS = 192;
-constexpr int C_MIN_UNITS = 2;
+constexpr int C_OVER = 4;                  // units that an item costs besides its keys
+constexpr int C_MIN_UNITS = C_OVER + 2;
 constexpr long long C_WAIT_LIMIT = 2000000000LL;
 constexpr int c_stages(bool f32) { return f32 ? 4 : 5; }
 constexpr int c_qbytes(bool f32) { return f32 ? 3 * STAGE : 2 * STAGE; }
@@ -220,8 +221,8 @@ __device__ __forceinline__ bool walk_seg(Walk& w, const PagedRange& R, int tpt, 
     g.tok0 = w.item * tpi;
     g.ntok = min(tpi, w.q.n_new - g.tok0);
     g.two = g.ntok > tpt;
-    g.kt0 = w.u - w.item0;
-    g.n = end - w.u;
+    g.kt0 = w.u == w.item0 ? 0 : w.u - w.item0 - C_OVER;
+    g.n = end - w.item0 - C_OVER - g.kt0;
     if (w.q.ctx - w.q.n_new + g.tok0 + g.ntok <= 0 || w.q.ctx <= 0) g.n = 0;
     g.whole = w.u == w.item0 && end == w.item0 + w.nu;
     g.ca = paged_cut_first(R, w.item0);
@@ -244,9 +245,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     const PagedView& c = a.c;
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tpt = CT / c.G, tpi = F32 ? tpt : 2 * tpt;   // tokens of a tile, of an item
+    const uint32_t ginv = 65536u / c.G + 1;                // row / G for rows below 256 and G <= 16: row * ginv >> 16
 
-    const PagedRange R = paged_range<C_THREADS>(a, gridDim.x, C_MIN_UNITS,
-                                                [&](const PagedSeq& q) { return c.nkv * seq_units<CT>(q, tpi); });
+    const PagedRange R = paged_range<C_THREADS>(a, gridDim.x, C_MIN_UNITS, C_OVER,
+                                                [&](const PagedSeq& q) { return c.nkv * seq_units<CT, C_OVER>(q, tpi); });
     if (R.u0 >= R.u1) return;
 
     if (threadIdx.x == 0) {
@@ -272,7 +274,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     const uint32_t tmem = sm.tmem;
 
     Walk w;
-    walk_begin<CT>(w, a, R, tpi);
+    walk_begin<CT, C_OVER>(w, a, R, tpi);
     if (threadIdx.x == 128) { sm.range = R; sm.walk = w; }
 
     // registers: 384 threads x 168 at launch = 128 x 72 + 256 x 216 (the launcher checks the 168)
@@ -313,7 +315,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 load(&mapV, g.kt0 + i);
                 if (i + lead < g.n) load(&mapK, g.kt0 + i + lead);
             }
-            if (w.more) walk_step<CT>(w, a, R, tpi);
+            if (w.more) walk_step<CT, C_OVER>(w, a, R, tpi);
         }
         // given up: nothing may still be writing this CTA's shared memory when it leaves
         if (*(volatile int*)&sm.dead)
@@ -418,7 +420,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 if (ok && elect_one()) commit(&sm.o_full);
                 __syncwarp();
             }
-            if (w.more) walk_step<CT>(w, a, R, tpi);
+            if (w.more) walk_step<CT, C_OVER>(w, a, R, tpi);
         }
         if (!ok && elect_one()) {   // products in flight end before the tensor memory goes
             commit(&sm.drain);
@@ -446,22 +448,23 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const Seg& g = sm.seg;
             const PagedSeq& wq = sm.walk.q;
             const int tile = g.two ? t : 0;
-            const int tok = g.tok0 + tile * tpt + r / c.G, head = g.h * c.G + r % c.G;
+            const int rg = (int)(r * ginv >> 16), tok = g.tok0 + tile * tpt + rg, head = g.h * c.G + r - rg * c.G;
             const bool live = r < tpt * c.G && tok < g.tok0 + g.ntok;
             const int lim = live ? min(wq.ctx - wq.n_new + tok + 1, wq.ctx) : 0;
             float mx = -INFINITY, l = 0.f;
             if (g.n > 0) {
                 // ---- query rows: 16 threads a row, 8 values each, loads of a batch in flight together
-                constexpr int NB = F32 ? 4 : 8, V4 = F32 ? 2 : 1;
+                constexpr int NB = 8, V4 = F32 ? 2 : 1;
                 const int first = g.two ? 0 : t * 64, count = g.two ? CT : 64, ch = r & 15;
                 for (int b0 = 0; b0 < count / 8; b0 += NB) {
                     uint4 raw[NB][V4];
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        const int row = first + (r >> 4) + 8 * (b0 + b), rt = g.tok0 + tile * tpt + row / c.G;
+                        const int row = first + (r >> 4) + 8 * (b0 + b), rg = (int)(row * ginv >> 16);
+                        const int rt = g.tok0 + tile * tpt + rg;
                         const bool there = row < tpt * c.G && rt < g.tok0 + g.ntok;
                         const uint4* src = (const uint4*)((const TA*)a.q + (int64_t)(wq.row0 + (there ? rt : 0)) * a.q_stride +
-                                                          (int64_t)(g.h * c.G + (there ? row % c.G : 0)) * HD + ch * 8);
+                                                          (int64_t)(g.h * c.G + (there ? row - rg * c.G : 0)) * HD + ch * 8);
 #pragma unroll
                         for (int j = 0; j < V4; ++j) raw[b][j] = there ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
                     }
@@ -603,50 +606,79 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const bool second = !g.two && g.n > 1;     // slot 1 has an output
             TA* dst = (TA*)a.out + (int64_t)(wq.row0 + tok) * a.out_stride + (int64_t)head * HD;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            auto put = [&](int col, const float (&v)[32]) {      // 32 values of the row
-                if (!live) return;
-                if constexpr (F32) {
+            // The output leaves through the tile's place for Q, whose products are done: a thread puts 32 values of its
+            // row, then the warp stores its rows side by side (16-byte pieces at places that depend on the row).
+            constexpr int PR = HD * (int)sizeof(TA) / 16, PB = PR / 4;   // pieces of a row, of 32 values
+            unsigned char* stage = qs + (size_t)(F32 ? 0 : tile) * STAGE;
+            auto put = [&](int blk, const float (&v)[32]) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *(float4*)(dst + col + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        *(uint4*)(dst + col + i) = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
-                                                              pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+                for (int i = 0; i < PB; ++i) {
+                    uint4 d;
+                    if constexpr (F32)
+                        d = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                       __float_as_uint(v[4 * i + 3]));
+                    else
+                        d = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                                       pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+                    *(uint4*)(stage + (size_t)(r * PR + ((blk * PB + i) ^ (r & (PR - 1)))) * 16) = d;
                 }
+            };
+            auto flush = [&](int blk0, int blk1) {     // blocks [blk0, blk1) of the warp's 32 rows
+                __syncwarp();
+                const int n = (blk1 - blk0) * PB, per = 32 / n, piece = blk0 * PB + lane % n;
+#pragma unroll 4
+                for (int i0 = 0; i0 < 32; i0 += per) {
+                    const int i = i0 + lane / n;
+                    TA* to = (TA*)__shfl_sync(0xffffffffu, (unsigned long long)dst, i);
+                    const bool there = __shfl_sync(0xffffffffu, (int)live, i);
+                    const int row = (r & ~31) + i;
+                    const uint4 d = *(const uint4*)(stage + (size_t)(row * PR + (piece ^ (row & (PR - 1)))) * 16);
+                    if (there) *((uint4*)to + piece) = d;
+                }
+                __syncwarp();
             };
             // partials: [32 groups of 4 values][256 rows], then maxima and sums
             const int prow = tile * CT + r;
             float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == g.ca ? 1 : 0)) * C_SLOT;
             if (mine) {
+                const float w0 = g.whole ? f0 * inv : f0, w1 = g.whole ? f1 * inv : f1;
 #pragma unroll 1
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t x[32], y[32];
-                    float v[32];
+                for (int c2 = 0; c2 < 4; c2 += 2) {
+                    uint32_t x[2][32];
                     if (g.n > 0) {
-                        tmem_ld32(tO + 32 * cc, x);
-                        if (second) tmem_ld32(tO1 + 32 * cc, y);
-                        tmem_wait_ld(x);
-                        if (second) tmem_wait_ld(y);
+                        tmem_ld32(tO + 32 * c2, x[0]);
+                        tmem_ld32(tO + 32 * c2 + 32, x[1]);
+                        tmem_wait_ld(x[0]);
+                        tmem_wait_ld(x[1]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        v[i] = l > 0.f ? __uint_as_float(x[i]) * f0 : 0.f;
-                        if (second && l > 0.f) v[i] = fmaf(__uint_as_float(y[i]), f1, v[i]);
-                    }
-                    if (g.whole) {
+                    for (int e = 0; e < 2; ++e) {
+                        const int cc = c2 + e;
+                        float v[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= inv;
-                        put(32 * cc, v);
-                    } else {
+                        for (int i = 0; i < 32; ++i) v[i] = l > 0.f ? __uint_as_float(x[e][i]) * w0 : 0.f;
+                        if (second) {
+                            uint32_t y[32];
+                            tmem_ld32(tO1 + 32 * cc, y);
+                            tmem_wait_ld(y);
+                            if (l > 0.f) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *(float4*)(slot + ((size_t)(8 * cc + i / 4) * 2 * CT + prow) * 4) =
-                                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                                for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(y[i]), w1, v[i]);
+                            }
+                        }
+                        if (g.whole) {
+                            put(cc, v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                *(float4*)(slot + ((size_t)(8 * cc + i / 4) * 2 * CT + prow) * 4) =
+                                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
                     }
                 }
-                if (!g.whole) {
+                if (g.whole) {
+                    flush(0, 4);
+                } else {
                     slot[2 * CT * HD + prow] = mx;
                     slot[2 * CT * HD + 2 * CT + prow] = l;
                 }
@@ -666,46 +698,63 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     const int mrow = tile * CT + r, b0 = g.two ? 0 : 2 * t, b1 = g.two ? 4 : b0 + 2;
                     auto part = [&](int cc) { return parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT; };
                     float m = -INFINITY, sum = 0.f;
-                    for (int cc = g.ca; cc <= g.cb; ++cc) m = fmaxf(m, __ldcg(part(cc) + 2 * CT * HD + mrow));
-                    const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-                    for (int cc = g.ca; cc <= g.cb; ++cc)
-                        sum += ex2f((__ldcg(part(cc) + 2 * CT * HD + mrow) - ms) * sl2) * __ldcg(part(cc) + 2 * CT * HD + 2 * CT + mrow);
-                    const float rs = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll 1
+                    for (int c0 = g.ca; c0 <= g.cb; c0 += 8) {
+                        float pm[8], pl[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float* p = part(min(c0 + j, g.cb)) + 2 * CT * HD + mrow;
+                            pm[j] = __ldcg(p);
+                            pl[j] = __ldcg(p + 2 * CT);
+                        }
+                        const float was = m;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) m = fmaxf(m, pm[j]);
+                        const float ms = m == -INFINITY ? 0.f : m;
+                        sum *= ex2f((was - ms) * sl2);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c0 + j <= g.cb) sum = fmaf(ex2f((pm[j] - ms) * sl2), pl[j], sum);
+                    }
+                    const float ms = m == -INFINITY ? 0.f : m, rs = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
                     for (int b = b0; b < b1; ++b) {
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll 1
-                        for (int cc = g.ca; cc <= g.cb; cc += 2) {
-                            const bool both = cc < g.cb;
-                            const float* p0 = part(cc);
-                            const float* p1 = part(both ? cc + 1 : cc);
-                            float4 z0[8], z1[8];
+                        for (int c0 = g.ca; c0 <= g.cb; c0 += 2) {
+                            float4 z[2][8];
+                            float f[2];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                z0[i] = __ldcg((const float4*)(p0 + ((size_t)(8 * b + i) * 2 * CT + mrow) * 4));
-                                z1[i] = __ldcg((const float4*)(p1 + ((size_t)(8 * b + i) * 2 * CT + mrow) * 4));
+                            for (int j = 0; j < 2; ++j) {
+                                const float* p = part(min(c0 + j, g.cb));
+                                f[j] = __ldcg(p + 2 * CT * HD + mrow);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    z[j][i] = __ldcg((const float4*)(p + ((size_t)(8 * b + i) * 2 * CT + mrow) * 4));
                             }
-                            const float w0 = ex2f((__ldcg(p0 + 2 * CT * HD + mrow) - ms) * sl2);
-                            const float w1 = both ? ex2f((__ldcg(p1 + 2 * CT * HD + mrow) - ms) * sl2) : 0.f;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                v[4 * i] = fmaf(z1[i].x, w1, fmaf(z0[i].x, w0, v[4 * i]));
-                                v[4 * i + 1] = fmaf(z1[i].y, w1, fmaf(z0[i].y, w0, v[4 * i + 1]));
-                                v[4 * i + 2] = fmaf(z1[i].z, w1, fmaf(z0[i].z, w0, v[4 * i + 2]));
-                                v[4 * i + 3] = fmaf(z1[i].w, w1, fmaf(z0[i].w, w0, v[4 * i + 3]));
+                            for (int j = 0; j < 2; ++j) {
+                                const float wj = c0 + j <= g.cb ? ex2f((f[j] - ms) * sl2) : 0.f;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    v[4 * i] = fmaf(z[j][i].x, wj, v[4 * i]);
+                                    v[4 * i + 1] = fmaf(z[j][i].y, wj, v[4 * i + 1]);
+                                    v[4 * i + 2] = fmaf(z[j][i].z, wj, v[4 * i + 2]);
+                                    v[4 * i + 3] = fmaf(z[j][i].w, wj, v[4 * i + 3]);
+                                }
                             }
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] *= rs;
-                        put(32 * b, v);
+                        put(b, v);
                     }
+                    flush(b0, b1);
                 }
             }
             wg_sync(1);
-            if (threadIdx.x == 128 && sm.walk.more) walk_step<CT>(sm.walk, a, sm.range, tpi);
+            if (threadIdx.x == 128 && sm.walk.more) walk_step<CT, C_OVER>(sm.walk, a, sm.range, tpi);
         }
     }
     __syncwarp();

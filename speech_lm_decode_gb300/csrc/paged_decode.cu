@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
         const int groups = (q.n_new * c.G + RG - 1) / RG;
         return (long long)c.nkv * groups * max(1, (q.ctx + DU - 1) / DU);
     };
-    const PagedRange R = paged_range<DW * 32>(a, grid_max, D_MIN_UNITS, units_of);
+    const PagedRange R = paged_range<DW * 32>(a, grid_max, D_MIN_UNITS, 0, units_of);
     if (R.u0 >= R.u1) return;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in powers of two
     const float slack = 8.f / sl2;

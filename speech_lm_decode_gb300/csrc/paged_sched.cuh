@@ -3,11 +3,14 @@
 //
 // The keys that the items of a call have to read are numbered as one list of
 // units (an item: a kv head and a tile of query rows of one sequence; a unit:
-// a fixed number of its keys), and CTA c of P takes units
-// [c W / P, (c + 1) W / P).  So every CTA has the same amount to read however
-// the lengths differ, and an item is cut only at a CTA's ends: a CTA has at
-// most two cut items, one that it continues (partial slot 0) and one that it
-// begins (slot 1).  The CTAs of a cut item are consecutive; each stores its
+// a fixed number of its keys), of which each of P CTAs takes an equal run.  So
+// every CTA has the same amount to read however the lengths differ, and an item
+// is cut only at a CTA's ends; a cut that would fall near the item's own ends
+// is moved there, as joining costs more than the imbalance.  An item may count
+// for `over` units more than it reads, for what it costs besides (its query
+// rows, its output).  A CTA has at most two cut items, one that it continues
+// (partial slot 0) and one that it begins (slot 1).  The CTAs of a cut item are
+// consecutive; each stores its
 // unnormalised output, maximum and sum, and the last one to arrive (a counter
 // that belongs to the first of them, reset by the last) joins them in CTA
 // order, so results do not depend on timing.  No CTA waits for another.
@@ -74,7 +77,7 @@ __device__ __forceinline__ int paged_cut_last(const PagedRange& r, int b) { retu
 // This CTA's range.  units(q): units of a sequence, all kv heads.  NT threads
 // call it; min_units: units that a CTA gets at least (fewer CTAs then work).
 template <int NT, class F>
-__device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int min_units, F units) {
+__device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int min_units, int over, F units) {
     __shared__ long long warp_sum_s[NT / 32];
     __shared__ int found_start, found_s;
     __shared__ PagedSeq found_q;
@@ -111,7 +114,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int
     r.P = min(P, max(1, r.W / min_units));
     r.quota = r.W / r.P;
     r.extra = r.W - r.quota * r.P;
-    r.snap = min(r.quota / 4, 2);
+    r.snap = over + min(r.quota / 4, 2);   // (a cut never falls into the `over` units)
     const int c = blockIdx.x;
     r.u0 = c < r.P ? paged_first(r, c) : r.W;
     r.u1 = c < r.P ? paged_first(r, c + 1) : r.W;
@@ -138,7 +141,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttn& a, int P, int
 }
 
 // Items of tpi tokens (of one kv head), units of KEYS keys that their last token
-// sees at most; in the order sequence, head, item.
+// sees at most, and OVER more; in the order sequence, head, item.
 struct Walk {
     PagedSeq q;
     int u, item0;         // unit to begin at, first unit of the item
@@ -147,21 +150,21 @@ struct Walk {
 };
 
 // tokens of an item (tpi) and the key tiles that item i of a sequence reads
-template <int KEYS>
+template <int KEYS, int OVER>
 __device__ __forceinline__ int item_units(const PagedSeq& q, int tpi, int i) {
     const int last = min(q.n_new, (i + 1) * tpi);
     const int vis = min(q.ctx - q.n_new + last, q.ctx);
-    return max(1, (vis + KEYS - 1) / KEYS);
+    return max(1, (vis + KEYS - 1) / KEYS) + OVER;
 }
-template <int KEYS>
+template <int KEYS, int OVER>
 __device__ __forceinline__ long long seq_units(const PagedSeq& q, int tpi) {
     long long n = 0;
-    for (int i = 0; i * tpi < q.n_new; ++i) n += item_units<KEYS>(q, tpi, i);
+    for (int i = 0; i * tpi < q.n_new; ++i) n += item_units<KEYS, OVER>(q, tpi, i);
     return n;
 }
 
 // on to the next item
-template <int KEYS>
+template <int KEYS, int OVER>
 __device__ __forceinline__ void walk_step(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
     w.item0 += w.nu;
     w.u = w.item0;
@@ -173,28 +176,28 @@ __device__ __forceinline__ void walk_step(Walk& w, const PagedAttn& a, const Pag
             do { w.q = paged_seq(a, ++w.s, false); } while (w.q.n_new <= 0);
         }
     }
-    w.nu = item_units<KEYS>(w.q, tpi, w.item);
+    w.nu = item_units<KEYS, OVER>(w.q, tpi, w.item);
 }
-template <int KEYS>
+template <int KEYS, int OVER>
 __device__ __forceinline__ void walk_begin(Walk& w, const PagedAttn& a, const PagedRange& R, int tpi) {
     w.s = R.s;
     w.q = R.q;
     w.more = true;
-    const int per = (int)seq_units<KEYS>(w.q, tpi);
+    const int per = (int)seq_units<KEYS, OVER>(w.q, tpi);
     int rel = R.u0 - R.start;
     w.h = rel / per;
     rel -= w.h * per;
     w.item0 = R.start + w.h * per;
     w.item = 0;
     for (;;) {
-        w.nu = item_units<KEYS>(w.q, tpi, w.item);
+        w.nu = item_units<KEYS, OVER>(w.q, tpi, w.item);
         if (rel < w.nu) break;
         rel -= w.nu;
         w.item0 += w.nu;
         ++w.item;
     }
     w.u = paged_begin(R, w.item0, w.item0 + w.nu);
-    if (w.u == w.item0 + w.nu) walk_step<KEYS>(w, a, R, tpi);
+    if (w.u == w.item0 + w.nu) walk_step<KEYS, OVER>(w, a, R, tpi);
 }
 // Workspace of the paged attention: counters, then two partial slots a CTA.
 constexpr int PAGED_MAX_CTAS = 1024;
