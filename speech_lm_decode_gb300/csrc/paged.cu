@@ -26,42 +26,49 @@ int paged_fail(int code, const char* fmt, ...) {
 namespace {
 
 // ------------------------------------------------------------------ append
-// A warp takes HPW heads of one token (q, k, then v heads).  Lane l holds the
-// four values 4l..4l+3 of a head, so the rotation's pair (j, j+64) lies in
-// lanes l and l ^ 16, and every load and store of a head is one 512-byte (fp32)
-// or 256-byte (bf16) access of the warp.
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-    const float4 a = *(const float4*)p;
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-}
-__device__ __forceinline__ void load4(const bf16* p, float (&v)[4]) {
-    const uint2 a = *(const uint2*)p;
-    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
-    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
-    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store4(bf16* p, const float (&v)[4]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    *(uint2*)p = make_uint2(*(const uint32_t*)&a, *(const uint32_t*)&b);
-}
-
+// Bound by the bytes moved: 12 KB in and out a token (16/8 heads, bf16).  A warp
+// takes NL 16-byte loads of one token, all in flight together; a head is 16
+// lanes of 8 bf16 or 32 lanes of 4 fp32 values, so a load brings two heads or
+// one.  The rotation's pair (j, j + 64) lies half a head's lanes apart.
+// With few tokens a warp takes one load, so that the heads of a token run
+// beside each other; with many, eight (prompts of 32 sequences, 9 thousand
+// tokens, bf16: 55 us with 256-byte loads of four heads, see launch).
 constexpr int APPEND_WARPS = 4;
 
-template <typename TA, typename TK, int HPW>
+// 16 bytes of activations as fp32 values
+__device__ __forceinline__ void expand(const uint4& r, float (&v)[8]) { unpack_bf16x8(r, v); }
+__device__ __forceinline__ void expand(const uint4& r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ uint32_t two(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t*)&v;
+}
+__device__ __forceinline__ void put(bf16* p, const float (&v)[8]) {
+    *(uint4*)p = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
+}
+__device__ __forceinline__ void put(bf16* p, const float (&v)[4]) { *(uint2*)p = make_uint2(two(v[0], v[1]), two(v[2], v[3])); }
+__device__ __forceinline__ void put(float* p, const float (&v)[4]) { *(float4*)p = make_float4(v[0], v[1], v[2], v[3]); }
+
+template <typename TA, typename TK, int NL>
 __global__ void __launch_bounds__(APPEND_WARPS * 32)
 paged_append_kernel(PagedView c, int n_tokens, const TA* qkv, int64_t ldq, const int32_t* __restrict__ tok_seq,
                     const int32_t* __restrict__ tok_pos, const float* __restrict__ qn, const float* __restrict__ kn,
                     float eps, const float2* __restrict__ rope, int rope_rows, TA* q_out, int64_t ldo, int* err) {
     pdl_wait();
     pdl_trigger();
-    const int heads = c.nq + 2 * c.nkv, groups = (heads + HPW - 1) / HPW;
-    const int lane = threadIdx.x & 31;
+    constexpr int VL = 16 / (int)sizeof(TA), LPH = HD / VL, HPL = 32 / LPH;   // values of a lane, lanes of a head, heads of a load
+    const int heads = c.nq + 2 * c.nkv, groups = (heads + NL * HPL - 1) / (NL * HPL);
+    const int lane = threadIdx.x & 31, sub = lane & (LPH - 1);
     const int64_t item = (int64_t)blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5);
     const int64_t m = item / groups;
-    const int h0 = (int)(item - m * groups) * HPW;
+    const int h0 = (int)(item - m * groups) * NL * HPL + lane / LPH;
     if (m >= n_tokens) return;
+    const TA* row = qkv + m * ldq;
+    uint4 raw[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+        raw[i] = h0 + i * HPL < heads ? *(const uint4*)(row + (h0 + i * HPL) * HD + sub * VL) : make_uint4(0, 0, 0, 0);
     const int pos = tok_pos[m], seq = tok_seq[m];
     if (pos < 0) return;
     const int pi = pos >> c.page_shift;
@@ -71,53 +78,56 @@ paged_append_kernel(PagedView c, int n_tokens, const TA* qkv, int64_t ldq, const
         if (lane == 0 && err) atomicOr(err, ERRB_BOUNDS);
         return;
     }
-    const TA* row = qkv + m * ldq;
-    float x[HPW][4];
+    // cosine and sine of this lane's pairs; the lower half of a head subtracts, the upper adds
+    float co[VL], si[VL];
+    {
+        const float4* cs = (const float4*)(rope + (int64_t)pos * (HD / 2) + (sub & (LPH / 2 - 1)) * VL);
+        const float sign = sub < LPH / 2 ? -1.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < HPW; ++i)
-        if (h0 + i < heads) load4(row + (h0 + i) * HD + lane * 4, x[i]);
-    // cosine and sine of this lane's four pairs
-    const float4* cs = (const float4*)(rope + (int64_t)pos * (HD / 2) + (lane & 15) * 4);
-    const float4 c01 = cs[0], c23 = cs[1];
-    const float co[4] = {c01.x, c01.z, c23.x, c23.z}, si[4] = {c01.y, c01.w, c23.y, c23.w};
-    const int64_t base = page * c.page_stride + (int64_t)(pos & ((1 << c.page_shift) - 1)) * c.token_stride + lane * 4;
-#pragma unroll
-    for (int i = 0; i < HPW; ++i) {
-        const int h = h0 + i;
-        if (h >= heads) break;
-        if (h >= c.nq + c.nkv) {
-            store4((TK*)c.v + base + (h - c.nq - c.nkv) * c.head_stride, x[i]);
-            continue;
+        for (int j = 0; j < VL; j += 2) {
+            const float4 f = cs[j / 2];
+            co[j] = f.x; si[j] = sign * f.y; co[j + 1] = f.z; si[j + 1] = sign * f.w;
         }
-        const bool is_q = h < c.nq;
-        const float* wn = is_q ? qn : kn;
-        if (wn) {
-            const float ss = warp_sum(x[i][0] * x[i][0] + x[i][1] * x[i][1] + x[i][2] * x[i][2] + x[i][3] * x[i][3]);
+    }
+    const int64_t base = page * c.page_stride + (int64_t)(pos & ((1 << c.page_shift) - 1)) * c.token_stride + sub * VL;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int h = h0 + i * HPL;
+        float x[VL], y[VL];
+        expand(raw[i], x);
+        if (qn) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < VL; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+            for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             const float r = 1.0f / sqrtf(ss / (float)HD + eps);
-            float w[4];
-            load4(wn + lane * 4, w);
+            if (h < c.nq + c.nkv) {
+                const float4* w = (const float4*)((h < c.nq ? qn : kn) + sub * VL);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[i][j] = x[i][j] * r * w[j];
+                for (int j = 0; j < VL; j += 4) {
+                    const float4 f = w[j / 4];
+                    x[j] *= r * f.x; x[j + 1] *= r * f.y; x[j + 2] *= r * f.z; x[j + 3] *= r * f.w;
+                }
+            }
         }
-        float y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float other = __shfl_xor_sync(0xffffffffu, x[i][j], 16);
-            y[j] = lane < 16 ? x[i][j] * co[j] - other * si[j] : x[i][j] * co[j] + other * si[j];
-        }
-        if (is_q) store4(q_out + m * ldo + h * HD + lane * 4, y);
-        else store4((TK*)c.k + base + (h - c.nq) * c.head_stride, y);
+        for (int j = 0; j < VL; ++j) y[j] = fmaf(x[j], co[j], __shfl_xor_sync(0xffffffffu, x[j], LPH / 2) * si[j]);
+        if (h < c.nq) put(q_out + m * ldo + h * HD + sub * VL, y);
+        else if (h < c.nq + c.nkv) put((TK*)c.k + base + (h - c.nq) * c.head_stride, y);
+        else if (h < heads) put((TK*)c.v + base + (h - c.nq - c.nkv) * c.head_stride, x);
     }
 }
 
-template <typename TA, typename TK, int HPW>
+template <typename TA, typename TK, int NL>
 cudaError_t append_t(const PagedView& c, int n_tokens, const void* qkv, int64_t ldq, const int32_t* seq,
                      const int32_t* pos, const float* qn, const float* kn, float eps, const float* rope, int rope_rows,
                      void* q_out, int64_t ldo, int* err, cudaStream_t st) {
-    const int groups = (c.nq + 2 * c.nkv + HPW - 1) / HPW;
+    constexpr int per = NL * (sizeof(TA) == 2 ? 2 : 1);   // heads of a warp
+    const int groups = (c.nq + 2 * c.nkv + per - 1) / per;
     const int64_t blocks = ((int64_t)n_tokens * groups + APPEND_WARPS - 1) / APPEND_WARPS;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_pdl(paged_append_kernel<TA, TK, HPW>, (unsigned)blocks, APPEND_WARPS * 32, 0, st, c, n_tokens,
+    return launch_pdl(paged_append_kernel<TA, TK, NL>, (unsigned)blocks, APPEND_WARPS * 32, 0, st, c, n_tokens,
                       (const TA*)qkv, ldq, seq, pos, qn, kn, eps, (const float2*)rope, rope_rows, (TA*)q_out, ldo, err);
 }
 
@@ -130,9 +140,10 @@ cudaError_t launch_paged_append(const PagedView& c, int act, int kv, int n_token
     if (n_tokens <= 0) return cudaSuccess;
     auto go = [&](auto f) { return f(c, n_tokens, qkv, qkv_stride, tok_seq, tok_pos, q_norm, k_norm, eps, rope_cs,
                                      rope_rows, q_out, q_stride, err, st); };
-    if (act == Q3_BF16) return go(append_t<bf16, bf16, 4>);
-    if (kv == Q3_BF16) return go(append_t<float, bf16, 4>);
-    return go(append_t<float, float, 4>);
+    const bool many = n_tokens >= 1024;
+    if (act == Q3_BF16) return many ? go(append_t<bf16, bf16, 8>) : go(append_t<bf16, bf16, 1>);
+    if (kv == Q3_BF16) return many ? go(append_t<float, bf16, 8>) : go(append_t<float, bf16, 1>);
+    return many ? go(append_t<float, float, 8>) : go(append_t<float, float, 1>);
 }
 
 namespace {

@@ -14,11 +14,11 @@
 // The two slots alternate on the tensor cores, so that one's softmax runs while
 // the other's products do.  With two tiles of rows, a slot is a tile and both
 // read the same keys; with one tile (few rows, or fp32 activations), the slots
-// take the tile's even and odd key tiles, each with its own maximum, sum and
-// output, joined at the end from tensor memory.
+// take the tile's even and odd key tiles, with one output and one reference
+// maximum that is handed on from step to step.
 //
-// fp32 activations enter as three bf16 parts of q (24 bits: exact) and two of p
-// (16 bits): 5 products for 2.
+// fp32 activations enter as three bf16 parts of q and of p (24 bits): 6 products
+// for 2.
 //
 // Every wait is bounded: one that runs out sets the timeout bit, after which
 // the CTA goes through its remaining steps without waiting or issuing, drains
@@ -58,10 +58,11 @@ struct Seg {
 };
 
 struct ChunkSmem {
-    uint64_t full[5], empty[5], s_full[2], p_full[2], q_full, o_full, drain;
+    uint64_t full[5], empty[5], s_full[2], p_full[2], r_full[2], pv_full, q_full, o_full, drain;
     uint32_t tmem;
     int dead, last;
-    float m[CT], l[CT];      // slot 1's statistics for slot 0
+    float ref[CT];           // one tile of rows: the maxima that both slots' weights refer to
+    float m[CT], l[CT];      // slot 1's maximum and sum for slot 0
     PagedRange range;        // the softmax warps' walk, kept here to save them the registers
     Walk walk;
     Seg seg;
@@ -236,7 +237,10 @@ __global__ void __launch_bounds__(C_THREADS, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                    const __grid_constant__ PagedAttn a) {
     constexpr bool F32 = sizeof(TA) == 4;
-    constexpr int ST = c_stages(F32), QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;
+    constexpr int ST = c_stages(F32), QP = F32 ? 3 : 1, PP = F32 ? 3 : 1;
+    // tensor memory: the slots' scores (and weights over them), then their outputs; fp32 has one output, but weights
+    // of three parts
+    constexpr int SLOT = F32 ? 192 : CT, OUT = 2 * SLOT;
     extern __shared__ __align__(1024) unsigned char raw[];
     __shared__ ChunkSmem sm;
     unsigned char* base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -256,9 +260,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         for (int i = 0; i < 2; ++i) {
             bar_init(&sm.s_full[i], 1);
             bar_init(&sm.p_full[i], CT / 32);   // a warp each
+            bar_init(&sm.r_full[i], CT / 32);
         }
         bar_init(&sm.q_full, 2 * CT);
         bar_init(&sm.o_full, 1);
+        bar_init(&sm.pv_full, 1);
         bar_init(&sm.drain, 1);
         sm.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -343,7 +349,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         // S of slot t from the K tile of ring entry i
         auto scores = [&](int t, int i) {
             const uint32_t kd = uniform(tile_desc(ring0 + (i % ST) * STAGE, 16));
-            const uint32_t qd = uniform(tile_desc(q0 + (!F32 && g.two ? t : 0) * STAGE, 16)), d = uniform(tmem + t * CT);
+            const uint32_t qd = uniform(tile_desc(q0 + (!F32 && g.two ? t : 0) * STAGE, 16)), d = uniform(tmem + t * SLOT);
             if (ok && elect_one()) {
 #pragma unroll
                 for (int p = 0; p < QP; ++p)
@@ -359,14 +365,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         // O of slot t += P V, once P is there
         auto outputs = [&](int t, int i, bool acc) {
             const uint32_t vd = uniform(tile_desc(ring0 + (i % ST) * STAGE, STAGE / 2));
-            const uint32_t pa = uniform(tmem + t * CT), d = uniform(tmem + 2 * CT + t * CT), first = uniform(acc);
+            const uint32_t pa = uniform(tmem + t * SLOT), d = uniform(tmem + OUT + (g.two ? t * CT : 0)), first = uniform(acc);
             p_ready(t);
             if (ok && elect_one()) {
 #pragma unroll
                 for (int p = 0; p < PP; ++p)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_ts(d, pa + (F32 ? 32 * (ks >> 1) + 8 * (ks & 1) + 16 * p : 8 * ks), vd + ks * (2048 >> 4), IDESC_V,
+                        umma_ts(d, pa + 64 * p + 8 * ks, vd + ks * (2048 >> 4), IDESC_V,
                                 (p | ks) != 0 ? 1u : first);
             }
             __syncwarp();
@@ -411,7 +417,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         if (more) { scores(1, k); release(k); }
                     } else {
                         const int t = i & 1;
-                        outputs(t, v, i > 1);
+                        outputs(t, v, i > 0);
+                        if (ok && elect_one()) commit(&sm.pv_full);
+                        __syncwarp();
                         release(v);
                         if (more) { full(k); scores(t, k); release(k); }
                     }
@@ -433,11 +441,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         const int t = warp >= 8 ? 1 : 0;
         const int r = (threadIdx.x & 127);                 // this thread's row of a tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lanes + t * CT, tO = tmem + lanes + 2 * CT + t * CT, tO1 = tmem + lanes + 3 * CT;
+        const uint32_t tS = tmem + lanes + t * SLOT;
         const float sl2 = a.scale * 1.4426950408889634f, slack = 8.f / sl2;
         int* counters = (int*)a.ws;
         float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
-        int sc = 0, oc = 0;
+        int sc = 0, oc = 0, rc = 0, pvc = 0;   // steps of this slot, items; of the other slot and products (one tile)
         bool ok = true;
         for (;;) {
             // both slots are done with Q and with the tensor memory of the item before
@@ -448,6 +456,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const Seg& g = sm.seg;
             const PagedSeq& wq = sm.walk.q;
             const int tile = g.two ? t : 0;
+            const uint32_t tO = tmem + lanes + OUT + tile * CT;
             const int rg = (int)(r * ginv >> 16), tok = g.tok0 + tile * tpt + rg, head = g.h * c.G + r - rg * c.G;
             const bool live = r < tpt * c.G && tok < g.tok0 + g.ntok;
             const int lim = live ? min(wq.ctx - wq.n_new + tok + 1, wq.ctx) : 0;
@@ -528,14 +537,28 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     tops[cc] = fmaxf(tops[cc], __uint_as_float(x[cc][31]));
                 }
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                // The maximum that the weights refer to moves only when a score passes it by 2^8.
+                // The maximum that the weights refer to moves only when a score passes it by 2^8.  Two slots with one
+                // tile share it: a step takes it over from the step before, which is the other slot's.
+                const int step = g.two ? j : 2 * j + t;
+                if (!g.two && step > 0) {
+                    ok = ok && bar_wait(&sm.r_full[1 - t], (rc + ((step - 1) >> 1)) & 1, sm, a.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    const float now = sm.ref[r];
+                    if (now != mx) l *= ex2f((mx - now) * sl2);    // (never back to -inf)
+                    mx = now;
+                }
                 const bool grew = top > mx + slack;
                 if (__any_sync(0xffffffffu, grew)) {
                     const float nm = fmaxf(mx, top);
                     const float f = nm == -INFINITY ? 1.f : ex2f((mx - nm) * sl2);
                     mx = nm;
                     l *= f;
-                    if (j > 0) {
+                    if (step > 0) {
+                        if (!g.two) {      // the products of the step before are in
+                            ok = ok && bar_wait(&sm.pv_full, (pvc + step - 1) & 1, sm, a.err);
+                            ok = __all_sync(0xffffffffu, ok);
+                            fence_after();
+                        }
 #pragma unroll 1
                         for (int cc = 0; cc < 8; ++cc) {
                             uint32_t y[16];
@@ -544,14 +567,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                             for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
                             tmem_st16(tO + 16 * cc, y);
                         }
+                        tmem_wait_st();
+                        fence_before();
                     }
+                }
+                if (!g.two) {
+                    sm.ref[r] = mx;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&sm.r_full[t]);
                 }
                 const float ref = mx == -INFINITY ? 0.f : -mx * sl2;
                 const f2c sl = pair(sl2, sl2), rf = pair(ref, ref);
                 f2c sums = pair(0.f, 0.f);
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t hi[16], lo[16];
+                    uint32_t hi[16], mid[16], lo[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float p0, p1;
@@ -560,14 +590,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         p1 = ex2f(p1);
                         sums = add_pair(sums, pair(p0, p1));
                         hi[i] = pack_bf16(p0, p1);
-                        if constexpr (F32)
-                            lo[i] = pack_bf16(p0 - __uint_as_float(hi[i] << 16), p1 - __uint_as_float(hi[i] & 0xffff0000u));
+                        if constexpr (F32) {
+                            p0 -= __uint_as_float(hi[i] << 16);
+                            p1 -= __uint_as_float(hi[i] & 0xffff0000u);
+                            mid[i] = pack_bf16(p0, p1);
+                            lo[i] = pack_bf16(p0 - __uint_as_float(mid[i] << 16), p1 - __uint_as_float(mid[i] & 0xffff0000u));
+                        }
                     }
+                    tmem_st16(tS + 16 * cc, hi);
                     if constexpr (F32) {
-                        tmem_st16(tS + 32 * cc, hi);
-                        tmem_st16(tS + 32 * cc + 16, lo);
-                    } else {
-                        tmem_st16(tS + 16 * cc, hi);
+                        tmem_st16(tS + 64 + 16 * cc, mid);
+                        tmem_st16(tS + 128 + 16 * cc, lo);
                     }
                 }
                 tmem_wait_st();
@@ -581,7 +614,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 }
             }
             // ---- the item's (or the cut's) output
-            float l1 = 0.f, f0 = 1.f, f1 = 0.f;
             if (g.n > 0) {
                 ok = ok && bar_wait(&sm.o_full, oc & 1, sm, a.err);
                 ++oc;
@@ -589,21 +621,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 fence_after();
             }
             if (!g.two) {
-                // slot 1's share of the keys joins slot 0's
+                rc += (g.n + t) / 2;      // the other slot's steps
+                pvc += g.n;
+                // both slots' sums, at the last maximum
                 if (t == 1) { sm.m[r] = mx; sm.l[r] = l; }
                 wg_sync(2);
-                if (t == 0) {
-                    const float m1 = sm.m[r];
-                    l1 = sm.l[r];
-                    const float m = fmaxf(mx, m1), ms = m == -INFINITY ? 0.f : m;
-                    f0 = ex2f((mx - ms) * sl2);
-                    f1 = ex2f((m1 - ms) * sl2);
+                if (t == 0 && g.n > 0) {
+                    const float m = sm.ref[r], ms = m == -INFINITY ? 0.f : m;
+                    l = l * ex2f((mx - ms) * sl2) + sm.l[r] * ex2f((sm.m[r] - ms) * sl2);
                     mx = m;
-                    l = l * f0 + l1 * f1;
                 }
             }
             const bool mine = g.two || t == 0;
-            const bool second = !g.two && g.n > 1;     // slot 1 has an output
             TA* dst = (TA*)a.out + (int64_t)(wq.row0 + tok) * a.out_stride + (int64_t)head * HD;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             // The output leaves through the tile's place for Q, whose products are done: a thread puts 32 values of its
@@ -641,7 +670,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const int prow = tile * CT + r;
             float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == g.ca ? 1 : 0)) * C_SLOT;
             if (mine) {
-                const float w0 = g.whole ? f0 * inv : f0, w1 = g.whole ? f1 * inv : f1;
+                const float w0 = g.whole ? inv : 1.f;
 #pragma unroll 1
                 for (int c2 = 0; c2 < 4; c2 += 2) {
                     uint32_t x[2][32];
@@ -657,15 +686,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = l > 0.f ? __uint_as_float(x[e][i]) * w0 : 0.f;
-                        if (second) {
-                            uint32_t y[32];
-                            tmem_ld32(tO1 + 32 * cc, y);
-                            tmem_wait_ld(y);
-                            if (l > 0.f) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(y[i]), w1, v[i]);
-                            }
-                        }
                         if (g.whole) {
                             put(cc, v);
                         } else {

@@ -31,7 +31,8 @@ namespace {
 constexpr int DW = 4;             // warps of a CTA
 constexpr int DU = 64;            // keys of a unit
 constexpr int d_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of an SM (registers)
-constexpr int D_MIN_UNITS = 1;
+constexpr int D_OVER = 0;         // units that an item costs besides its keys
+constexpr int D_MIN_UNITS = D_OVER + 1;
 
 __device__ __forceinline__ uint4 ldg16(const bf16* p, bool ok) {
     uint4 r;
@@ -62,13 +63,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// part `p` of x in bf16 parts (x = part 0 + part 1 + part 2 for 24-bit x; part 3 is zero)
-__device__ __forceinline__ float part_of(float x, int p) {
-    const float h = __bfloat162float(__float2bfloat16_rn(x));
-    const float r1 = x - h;
-    const float m = __bfloat162float(__float2bfloat16_rn(r1));
-    const float l = __bfloat162float(__float2bfloat16_rn(r1 - m));
-    return p == 0 ? h : p == 1 ? m : p == 2 ? l : 0.f;
+// part `p` of two values, packed: bf16 parts with x = part 0 + part 1 + part 2 (24 bits); part 3 is zero
+__device__ __forceinline__ uint32_t part2(float x0, float x1, int p) {
+    const uint32_t h = pack2(x0, x1);
+    x0 -= __uint_as_float(h << 16);
+    x1 -= __uint_as_float(h & 0xffff0000u);
+    const uint32_t m = pack2(x0, x1);
+    const uint32_t l = pack2(x0 - __uint_as_float(m << 16), x1 - __uint_as_float(m & 0xffff0000u));
+    return p < 2 ? (p == 0 ? h : m) : (p == 2 ? l : 0u);
 }
 
 // NT: column tiles of eight; a query row takes one column (bf16 activations) or
@@ -88,9 +90,9 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
     auto units_of = [&](const PagedSeq& q) -> long long {
         if (q.n_new <= 0) return 0;
         const int groups = (q.n_new * c.G + RG - 1) / RG;
-        return (long long)c.nkv * groups * max(1, (q.ctx + DU - 1) / DU);
+        return (long long)c.nkv * groups * (max(1, (q.ctx + DU - 1) / DU) + D_OVER);
     };
-    const PagedRange R = paged_range<DW * 32>(a, grid_max, D_MIN_UNITS, 0, units_of);
+    const PagedRange R = paged_range<DW * 32>(a, grid_max, D_MIN_UNITS, D_OVER, units_of);
     if (R.u0 >= R.u1) return;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in powers of two
     const float slack = 8.f / sl2;
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
 
     int s = R.s;
     PagedSeq q = R.q;
-    int nu = max(1, (q.ctx + DU - 1) / DU), groups = (q.n_new * c.G + RG - 1) / RG;   // units and row groups of a head
+    int nu = max(1, (q.ctx + DU - 1) / DU) + D_OVER, groups = (q.n_new * c.G + RG - 1) / RG;   // units and row groups of a head
     int item = (R.u0 - R.start) / nu;       // head * groups + row group
     int item0 = R.start + item * nu;        // the item's units [item0, item0 + nu)
     auto next_item = [&]() -> bool {
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
         if (++item < c.nkv * groups) return true;
         if (item0 >= R.u1) return false;
         do { q = paged_seq(a, ++s, false); } while (q.n_new <= 0);
-        nu = max(1, (q.ctx + DU - 1) / DU);
+        nu = max(1, (q.ctx + DU - 1) / DU) + D_OVER;
         groups = (q.n_new * c.G + RG - 1) / RG;
         item = 0;
         return true;
@@ -118,7 +120,8 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
     if (u == item0 + nu && !next_item()) return;
     while (paged_cut(R, item0, item0 + nu, &seg_end)) {
         const int h = item / groups, rg = item - h * groups;
-        const int key0 = (u - item0) * DU, key1 = (int)min((long long)q.ctx, (long long)(seg_end - item0) * DU);
+        const int key0 = u == item0 ? 0 : (u - item0 - D_OVER) * DU;
+        const int key1 = (int)min((long long)q.ctx, (long long)(seg_end - item0 - D_OVER) * DU);
         const int rows = min(RG, q.n_new * c.G - rg * RG);
 
         // ---- blocks of 16 keys: lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9
@@ -176,10 +179,10 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
                     const float4 f0 = there ? *(const float4*)(src + j * 32) : z;
                     const float4 f1 = there ? *(const float4*)(src + j * 32 + 4) : z;
                     const int p = g >> 1;
-                    qb[n][2 * j][0] = pack2(part_of(f0.x, p), part_of(f0.y, p));
-                    qb[n][2 * j][1] = pack2(part_of(f0.z, p), part_of(f0.w, p));
-                    qb[n][2 * j + 1][0] = pack2(part_of(f1.x, p), part_of(f1.y, p));
-                    qb[n][2 * j + 1][1] = pack2(part_of(f1.z, p), part_of(f1.w, p));
+                    qb[n][2 * j][0] = part2(f0.x, f0.y, p);
+                    qb[n][2 * j][1] = part2(f0.z, f0.w, p);
+                    qb[n][2 * j + 1][0] = part2(f1.x, f1.y, p);
+                    qb[n][2 * j + 1][1] = part2(f1.z, f1.w, p);
                 } else {
                     const uint4 w = there ? *(const uint4*)(src + j * 32) : make_uint4(0, 0, 0, 0);
                     qb[n][2 * j][0] = w.x; qb[n][2 * j][1] = w.y;
@@ -274,10 +277,9 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
                     const float m = mx[n][i & 1];
                     p[i] = ex2(fmaf(x[n][i], sl2, m == -INFINITY ? 0.f : -m * sl2));
                     l[n][i & 1] += p[i];
-                    if constexpr (F32) p[i] = part_of(p[i], t);
                 }
-                pb[n][0] = transpose8(pack2(p[0], p[1]));
-                pb[n][1] = transpose8(pack2(p[2], p[3]));
+                pb[n][0] = transpose8(F32 ? part2(p[0], p[1], t) : pack2(p[0], p[1]));
+                pb[n][1] = transpose8(F32 ? part2(p[2], p[3], t) : pack2(p[2], p[3]));
             }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {

@@ -2,24 +2,26 @@
 // min-p from one given uniform number a row (definition in q3tts.h).
 //
 // A row belongs to a cluster of up to eight CTAs.  Each reads its slice of the
-// logits once, keeps the quotients l in shared memory, and everything after
-// that happens there; the CTAs exchange maxima, histograms and sums through
-// distributed shared memory.  Kept weights are whole numbers (at most 2^40
-// each), so no result depends on the order of a sum.
+// logits once into shared memory, and everything after that happens there; the
+// CTAs exchange maxima, histograms, lists and sums through distributed shared
+// memory.  Kept weights are whole numbers (at most 2^40 each), so no result
+// depends on the order of a sum.
 //   - k <= 128: the k-th largest of 512 group maxima bounds the k-th largest
 //     value from below; the few values that reach it go to the first CTA, which
-//     does the rest on that list.
-//   - otherwise: one pass replaces l by e = exp(l - max), adds up the exact
-//     weights and (top-p) a histogram of them, 16 bins an octave of e.  The
-//     histogram says in which bins the top-p border lies; a second pass adds up
-//     exactly what lies above them and lists what lies inside, and a radix
-//     selection on the list finds the border (on the whole slices if the list
-//     overflows or the histogram misjudged it).  Ids of a tie at the border are
-//     kept from the lowest on: a second selection, on the ids.
+//     does the rest on that list while the others leave.
+//   - otherwise: one pass replaces the logits by e = exp(l - max), adds up the
+//     exact weights and (top-p) a histogram of them, 64 bins an octave of e.  The
+//     histogram says in which bin the top-p border lies; a second pass adds up
+//     exactly what lies above it and lists what lies inside, and each entry of
+//     the list finds the weight in front of it.  A bin with more entries than a
+//     list holds is searched by radix instead (and, of the ids that tie at the
+//     border, which are kept).  A k above 128 is found the same way, by a
+//     histogram of max - l and a list.
 //   - the draw: every warp has the kept weight of its run of ids, so only one
 //     warp of one CTA scans its run.
-// What bounds it: about 45 instructions a logit (division, exp, weight), not
-// the 2 or 4 bytes read.
+// What bounds it: the meetings of the cluster at small sizes (one row of 2048
+// logits, k 50: 9 us), about 60 instructions a logit at large ones (division,
+// exp, weight, histogram), not the 2 or 4 bytes read.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -241,7 +243,7 @@ template <typename T>
 struct Row {
     GivenSmem& s;
     cg::cluster_group cl;
-    float* e;            // the slice: l, then e
+    float* e;            // the slice: logits, then e
     const T* x;          // the row's logits
     Quotient q;
     int V, C, rank, slice, seg, base;   // base: id of the slice's first entry
@@ -382,12 +384,13 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
              rank * slice, 0.f};
     const int seg = R.seg, base = R.base, w0 = warp * seg;   // the warp's run of the slice
 
-    // ---- quotients into shared memory; the largest, and maxima of groups of C lanes
+    // ---- logits into shared memory; the largest (division is monotone: its quotient is the largest too), and maxima
+    // of groups of C lanes
     float mx = -INFINITY;   // NaN once it has met one
     {
         const T* x = R.x + base;
         const bool vec = ((uintptr_t)x & (4 * sizeof(T) - 1)) == 0;
-#pragma unroll 4
+#pragma unroll 5
         for (int i = w0 + lane * 4; i < w0 + seg; i += 128) {
             float v[4];
             if (vec && base + i + 3 < V) {
@@ -395,14 +398,6 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = base + i + j < V ? lval(x, i + j) : -INFINITY;
-            }
-            const bool quick = R.q.in_range(v[0]) && R.q.in_range(v[1]) && R.q.in_range(v[2]) && R.q.in_range(v[3]);
-            if (quick) {
-                R.q.quick2(v[0], v[1], v[0], v[1]);
-                R.q.quick2(v[2], v[3], v[2], v[3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = R.q(v[j]);
             }
             mx = max_nan(mx, max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])));
             *(float4*)(e + i) = make_float4(v[0], v[1], v[2], v[3]);
@@ -423,8 +418,17 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
     cl.sync();
     uint32_t best = 0;
     from_all(cl, C, &s.best, [&](int, uint32_t b) { best = max(best, b); });
-    const bool bad = best == 0xFFFFFFFFu;
-    const float m = R.m = order_key_inv(best);
+    const float m = R.m = R.q(order_key_inv(best));
+    bool bad = best == 0xFFFFFFFFu || !(m < INFINITY);
+    if (temp == INFINITY) {     // -inf / inf is no number
+        int none = 0;
+        for (int i = w0 + lane; i < w0 + seg; i += 32) none |= base + i < V && e[i] == -INFINITY;
+        none = __syncthreads_or(none);
+        if (tid == 0) s.pick = none;
+        cl.sync();
+        from_all(cl, C, &s.pick, [&](int, int v) { bad |= v != 0; });
+        cl.sync();
+    }
     const bool fails = bad || m == -INFINITY;
     // the largest alone (the lowest id on ties): greedy, or nothing else passes top-p or min-p
     if (fails || temp == 0.f || !(top_p > 0.f) || !(min_p <= 1.f)) {
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         __syncthreads();
         if (!fails)
             for (int i = w0 + lane; i < w0 + seg; i += 32)
-                if (e[i] == m && base + i < V) atomicMin(&s.pick, base + i);
+                if (base + i < V && R.q(e[i]) == m) atomicMin(&s.pick, base + i);
         cl.sync();
         int first = 0x7fffffff;
         if (rank == 0) from_all(cl, C, &s.pick, [&](int, int v) { first = min(first, v); });
@@ -457,13 +461,15 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
     // ---- small k: the list path (its list is the first CTA's alone)
     const bool with_k = k > 0 && k < V;
     if (with_k && k <= SMALL_K) {
-        // the k-th largest group maximum, rounded down to 16 bits of its key: at least k values reach it
+        // the k-th largest group maximum, rounded down to 16 bits of its key: at least k logits reach it.  One step of
+        // 2^-7 lower, and every logit with the same quotient as any of those does too (unless quotients are denormal).
         const uint32_t v = cl.map_shared_rank(s.maxima, 0)[tid];
         uint32_t tk = 0;
 #pragma unroll 1
         for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
             if (__syncthreads_count(v >= (tk | bit)) >= k) tk |= bit;
-        const float tau = tk < 0x00800000u ? -INFINITY : order_key_inv(tk);
+        float tau = tk < 0x00820000u ? -INFINITY : order_key_inv(tk - 0x10000u);
+        if (!(fabsf(R.q(tau)) > 0x1p-100f)) tau = -INFINITY;
         GivenSmem* lead = cl.map_shared_rank(&s, 0);
         for (int i = w0 + lane * 4; i < w0 + seg; i += 128) {
             const float4 v = *(const float4*)(e + i);
@@ -473,7 +479,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
                 for (int j = 0; j < 4; ++j)
                     if (a[j] >= tau && base + i + j < V) {
                         const int n = atomicAdd(&lead->n_list, 1);
-                        if (n < LIST) { lead->lkey[n] = order_key(a[j]); lead->lid[n] = base + i + j; }
+                        if (n < LIST) { lead->lkey[n] = order_key(R.q(a[j])); lead->lid[n] = base + i + j; }
                     }
             }
         }
@@ -560,12 +566,14 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         if (tid == 0) s.n_list = 0;
         __syncthreads();
         for (int i = w0 + lane; i < w0 + seg; i += 32)
-            if (base + i < V) atomicAdd(&s.hist[bin_of(e[i])], 1u);
+            if (base + i < V) atomicAdd(&s.hist[bin_of(R.q(e[i]))], 1u);
         R.locate([](uint32_t v, int) { return (u64)v; }, [&](u64 c) { return c >= (u64)k; }, [] {});
         const int b = s.edge_bin;
         u64 above = s.pick64;
-        for (int i = w0 + lane; i < w0 + seg; i += 32)
-            if (base + i < V && bin_of(e[i]) == b) R.push(order_key(e[i]), base + i, 0.f);
+        for (int i = w0 + lane; i < w0 + seg; i += 32) {
+            const float l = R.q(e[i]);
+            if (base + i < V && bin_of(l) == b) R.push(order_key(l), base + i, 0.f);
+        }
         int own;
         const int n = R.merge(&own);
         if (n >= 0) {
@@ -591,22 +599,30 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         } else {
             uint32_t key = 0;
             R.select([&](auto f) {
-                for (int i = w0 + lane; i < w0 + seg; i += 32)
-                    if (base + i < V && bin_of(e[i]) == b) f(order_key(e[i]), 1ull);
+                for (int i = w0 + lane; i < w0 + seg; i += 32) {
+                    const float l = R.q(e[i]);
+                    if (base + i < V && bin_of(l) == b) f(order_key(l), 1ull);
+                }
             }, [&](u64 c) { return c >= (u64)k; }, 32, &key, &above);
             kth = order_key_inv(key);
         }
         cl.sync();   // lists and histograms have been read
     }
 
-    // ---- e in place of l; weights, and their histogram where top-p needs it
+    // ---- e in place of the logits; weights, and their histogram where top-p needs it
     const bool with_p = top_p < 1.f;
     for (int i = tid; i < BINS; i += GT) s.hist[i] = 0;
     if (tid == 0) s.n_list = 0;
     __syncthreads();
     u64 sum = 0, kept = 0;
     auto to_e = [&](int i, auto use) {
-        const float4 v = *(const float4*)(e + i);
+        float4 v = *(const float4*)(e + i);
+        if (R.q.in_range(v.x) && R.q.in_range(v.y) && R.q.in_range(v.z) && R.q.in_range(v.w)) {
+            R.q.quick2(v.x, v.y, v.x, v.y);
+            R.q.quick2(v.z, v.w, v.z, v.w);
+        } else {
+            v = make_float4(R.q(v.x), R.q(v.y), R.q(v.z), R.q(v.w));
+        }
         float a[4];
         exp_of2(v.x, v.y, m, a[0], a[1]);
         exp_of2(v.z, v.w, m, a[2], a[3]);

@@ -86,6 +86,38 @@ def test_rows_that_fail():
     check(x.cuda(), 0.3, t, 40, 0.9, 0.0)
 
 
+def test_extreme_temperatures_and_logits():
+    """Quotients that are denormal (many logits share one), that underflow to zero, an infinite temperature (uniform,
+    or no number where a logit is -inf), and logits that the quick division does not take."""
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(10, 5000, generator=g)
+    x[1] *= 1e-30
+    x[2] *= 1e-38
+    x[3] *= 1e25
+    x[4] = torch.where(torch.rand(5000, generator=g) < 0.5, x[4] * 1e-25, x[4] * 1e20)
+    x[6, 3000] = float("-inf")
+    x[8] *= 2.0 ** 70
+    t = np.array([1e12, 1e10, 1.0, 1e-5, 3.0, np.inf, np.inf, 3e38, 2.0 ** 60, 2.0 ** -40], np.float32)
+    u = np.linspace(0.05, 0.95, 10, dtype=np.float32)
+    for k, p in ((0, 1.0), (40, 1.0), (200, 0.9), (0, 0.7)):
+        check(x.cuda(), u, t, k, p, 0.0)
+
+
+@pytest.mark.parametrize("vocab", [3000, 40000])
+def test_many_ids_at_the_border(vocab):
+    """Crowded borders: hundreds of equal or nearly equal logits where top-k or top-p cuts, beyond what the lists
+    hold."""
+    g = torch.Generator().manual_seed(vocab)
+    x = torch.randn(6, vocab, generator=g) * 0.01
+    x[1] = torch.randint(0, 3, (vocab,), generator=g).float()
+    x[2] = 2.0
+    x[3, : vocab // 2] = 1.0
+    x[4] = torch.linspace(0, 1e-3, vocab)
+    u = np.linspace(0.01, 0.99, 6, dtype=np.float32)
+    for k, p in ((100, 1.0), (700, 1.0), (0, 0.5), (900, 0.33), (0, 0.999)):
+        check(x.cuda(), u, 1.0, k, p, 0.0)
+
+
 def test_strided_rows_and_graph():
     import speech_lm_decode_gb300 as q3
     wide = torch.randn(16, 5007, device="cuda")

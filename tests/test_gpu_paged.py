@@ -211,6 +211,52 @@ def test_graph_replay_with_new_lengths():
 
 
 @pytest.mark.parametrize("types", TYPES)
+def test_many_row_graph_replay(types):
+    """Chunks captured once and replayed with other splits of the rows between the sequences."""
+    act, kv = TYPES[types]
+    s = make([(90, 700)] * 3, 16, 8, 16, act, kv, seed=12)
+    cache = cache_of(s)
+    cache.attend(s["q"], s["off"], s["ctx"], 200)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = cache.attend(s["q"], s["off"], s["ctx"], 200)
+    for lens in ([(200, 700), (0, 5), (70, 130)], [(1, 1), (128, 128), (141, 699)], [(90, 90), (90, 300), (60, 61)]):
+        off = [0, lens[0][0], lens[0][0] + lens[1][0], sum(q for q, _ in lens)]
+        s["off"].copy_(torch.tensor(off, dtype=torch.int32))
+        s["ctx"].copy_(torch.tensor([c for _, c in lens], dtype=torch.int32))
+        s["q"].normal_()
+        out.fill_(9.0)
+        gr.replay()
+        torch.cuda.synchronize()
+        cache.check()
+        want, bound = attend64({**s, "lens": lens})
+        close(out[:off[-1]], want, bound, str(lens))
+        assert (out[off[-1]:] == 9.0).all()
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("new", [1, 64])
+def test_growing_scores(types, new):
+    """Keys whose scores grow along the sequence, by far more than 2^8 from tile to tile: the reference maximum
+    moves at every step and the earlier share of the output vanishes."""
+    act, kv = TYPES[types]
+    s = make([(new, 1500), (new, 640)], 8, 4, 32, act, kv, seed=6)
+    direction = torch.randn(HD, device="cuda")
+    direction /= direction.norm()
+    for i, (_, ctx) in enumerate(s["lens"]):
+        pages = s["table"][i, :-(-ctx // 32)].long()
+        at = torch.arange(ctx, device="cuda")
+        grow = (at.float() / 40.0)[:, None, None] * direction
+        k = s["k"][pages[at // 32], :, at % 32].float() * 0.3 + grow
+        s["k"][pages[at // 32], :, at % 32] = k.to(kv)
+    s["q"].copy_((direction * 12 + 0.3 * torch.randn_like(s["q"].float())).to(act))
+    got = cache_of(s).attend(s["q"], s["off"], s["ctx"], new)
+    want, bound = attend64(s)
+    close(got, want, bound)
+
+
+@pytest.mark.parametrize("types", TYPES)
 @pytest.mark.parametrize("new", [1, 40])
 def test_bad_pages_positions_and_lengths_are_reported(types, new):
     import speech_lm_decode_gb300 as q3
