@@ -40,7 +40,8 @@ using u64 = unsigned long long;
 constexpr int GT = 512, GW = GT / 32;   // threads, warps of a CTA
 constexpr int GIVEN_MAX_VOCAB = 262144; // whole weights of a row stay below 2^58
 constexpr int MAX_CLUSTER = 8;
-constexpr int LIST = 512;               // entries of the candidate lists
+constexpr int LIST = 512;               // entries of a CTA's list
+constexpr int MERGED = 1024;            // of the lists of a row together
 constexpr int SMALL_K = 128;            // top-k that the list path takes
 constexpr int GROUPS = 512;             // group maxima of a row
 constexpr int BINS = 41 * 64;           // 64 bins an octave: e from 2^-40 to 2
@@ -171,15 +172,27 @@ struct Quotient {
 struct GivenSmem {
     u64 wsum[GW];                // kept weight of each warp's ids
     u64 red[GW + 1];
-    u64 total, above, kept;      // weight of the slice; of it above the bracket; kept
-    uint32_t hist[BINS];         // sums of mantissas by e, or counts by max - l, from the top
-    uint32_t coarse[COARSE];     // of 16 bins each
+    u64 total, above, kept;      // weight of the slice; of it above the bin; kept
+    union {                      // a histogram has been read by all CTAs when its bin's lists are merged
+        struct {
+            uint32_t hist[BINS];     // sums of mantissas by e, or counts by max - l, from the top
+            uint32_t coarse[COARSE]; // of 16 bins each
+        };
+        struct {
+            u64 sw[MERGED];          // the lists of all CTAs: weights, order keys, ids
+            uint32_t skey[MERGED];
+            int sid[MERGED];
+        };
+    };
+    union {                      // a radix selection follows where the lists have not done
+        struct {
+            uint32_t lkey[LIST];     // this CTA's list: order keys, ids, e
+            int lid[LIST];
+            float le[LIST];
+        };
+        uint32_t radix[2][3 * 256];  // passes in turn
+    };
     uint32_t maxima[GROUPS];     // first CTA: group maxima of the row
-    uint32_t radix[2][3 * 256];  // radix passes, in turn
-    uint32_t lkey[LIST], skey[LIST];
-    int lid[LIST], sid[LIST];
-    float le[LIST];
-    u64 sw[LIST];                // weights of the merged list
     unsigned char keep[LIST];
     uint32_t best;               // largest order key of the slice
     int n_list, pick;
@@ -300,7 +313,7 @@ struct Row {
 
     // The bin of the cluster's histograms in which the running sum of weigh(entry, bin) passes the goal (into
     // s.edge_bin, -1: none) and the sum in front of it (s.pick64).  All threads of the cluster call it.
-    // goal(): sets the goal, once the cluster has met.
+    // goal(part): sets the goal, given the threads' parts of the sum of all.
     template <class Weigh, class Reach, class Goal>
     __device__ void locate(Weigh weigh, Reach reach, Goal goal) {
         const int t = threadIdx.x;
@@ -313,9 +326,9 @@ struct Row {
         }
         if (t == 0) { s.pick = -1; s.edge_bin = -1; }
         cl.sync();
-        goal();
         u64 c = 0;
         if (t < COARSE) from_all(cl, C, &s.coarse[t], [&](int, uint32_t v) { c += weigh(v, t * 16); });
+        goal(c);
         u64 incl = cta_scan64(s, c);
         if (t < COARSE && !reach(incl - c) && reach(incl)) { s.pick = t; s.pick64 = incl - c; }
         __syncthreads();
@@ -338,26 +351,34 @@ struct Row {
         if (n < LIST) { s.lkey[n] = key; s.lid[n] = id; s.le[n] = ev; }
     }
     // The lists of all CTAs, by rank, into skey / sid / sw of each; *own: where this CTA's begins.  Returns their
-    // length, or -1 if it is more than LIST.  All threads of the cluster call it.
+    // length, or -1 if one of them overflowed or all are more than MERGED.  All threads of the cluster call it.
     __device__ int merge(int* own) {
         cl.sync();
-        static_assert(LIST <= GT, "a thread copies an entry");
-        int total = 0, from = 0, at = threadIdx.x;
+        int total = 0, n[MAX_CLUSTER];
         *own = 0;
         from_all(cl, C, &s.n_list, [&](int r, int v) {
             if (r < rank) *own += v;
             total += v;
-            if (r < C - 1 && from == r && at >= v) { at -= v; ++from; }
+            n[r] = v;
         });
-        if (total > LIST) return -1;
-        if ((int)threadIdx.x < total) {
+        if (total > MERGED) return -1;
+        bool fits = true;
+#pragma unroll
+        for (int r = 0; r < MAX_CLUSTER; ++r)
+            if (r < C) fits = fits && n[r] <= LIST;
+        if (!fits) return -1;
+        for (int i = threadIdx.x; i < total; i += GT) {
+            int from = 0, at = i;
+#pragma unroll
+            for (int r = 0; r < MAX_CLUSTER - 1; ++r)
+                if (r < C - 1 && from == r && at >= n[r]) { at -= n[r]; ++from; }
             const GivenSmem* o = cl.map_shared_rank(&s, from);
             const uint32_t key = o->lkey[at];
             const int id = o->lid[at];
             const float ev = o->le[at];
-            s.skey[threadIdx.x] = key;
-            s.sid[threadIdx.x] = id;
-            s.sw[threadIdx.x] = weight_of(ev);
+            s.skey[i] = key;
+            s.sid[i] = id;
+            s.sw[i] = weight_of(ev);
         }
         __syncthreads();
         return total;
@@ -365,7 +386,7 @@ struct Row {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, const T* logits, int64_t ld,
+__global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, int n, int ahead, const T* logits, int64_t ld,
                                                              const float* u_, const float* temp_, const int32_t* topk_,
                                                              const float* topp_, const float* minp_, int32_t* ids,
                                                              float* logprob, int* err) {
@@ -402,6 +423,12 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             mx = max_nan(mx, max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])));
             *(float4*)(e + i) = make_float4(v[0], v[1], v[2], v[3]);
         }
+    }
+    // the slice of the row that takes this one's place on the GPU, into L2
+    if (row + ahead < n) {
+        const char* next = (const char*)(R.x + (int64_t)ahead * ld + base);
+        const int bytes = min(slice, V - base) * (int)sizeof(T);
+        for (int i = tid * 128; i < bytes; i += GT * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
     }
     {
         const uint32_t key = mx < INFINITY && temp >= 0.f ? order_key(mx) : 0xFFFFFFFFu;   // all ones: the row fails
@@ -463,11 +490,25 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
     if (with_k && k <= SMALL_K) {
         // the k-th largest group maximum, rounded down to 16 bits of its key: at least k logits reach it.  One step of
         // 2^-7 lower, and every logit with the same quotient as any of those does too (unless quotients are denormal).
-        const uint32_t v = cl.map_shared_rank(s.maxima, 0)[tid];
-        uint32_t tk = 0;
+        uint32_t* mine = s.hist;   // (not yet in use)
+        mine[tid] = cl.map_shared_rank(s.maxima, 0)[tid];
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t v[GROUPS / 32], t = 0;
+#pragma unroll
+            for (int i = 0; i < GROUPS / 32; ++i) v[i] = mine[lane + 32 * i];
 #pragma unroll 1
-        for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
-            if (__syncthreads_count(v >= (tk | bit)) >= k) tk |= bit;
+            for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+                const uint32_t c = t | bit;
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < GROUPS / 32; ++i) n += v[i] >= c;
+                if (__reduce_add_sync(0xffffffffu, n) >= k) t = c;
+            }
+            if (lane == 0) s.pick = (int)t;
+        }
+        __syncthreads();
+        const uint32_t tk = (uint32_t)s.pick;
         float tau = tk < 0x00820000u ? -INFINITY : order_key_inv(tk - 0x10000u);
         if (!(fabsf(R.q(tau)) > 0x1p-100f)) tau = -INFINITY;
         GivenSmem* lead = cl.map_shared_rank(&s, 0);
@@ -567,7 +608,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         __syncthreads();
         for (int i = w0 + lane; i < w0 + seg; i += 32)
             if (base + i < V) atomicAdd(&s.hist[bin_of(R.q(e[i]))], 1u);
-        R.locate([](uint32_t v, int) { return (u64)v; }, [&](u64 c) { return c >= (u64)k; }, [] {});
+        R.locate([](uint32_t v, int) { return (u64)v; }, [&](u64 c) { return c >= (u64)k; }, [](u64) {});
         const int b = s.edge_bin;
         u64 above = s.pick64;
         for (int i = w0 + lane; i < w0 + seg; i += 32) {
@@ -640,7 +681,6 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         for (int i = w0 + lane * 4; i < w0 + seg; i += 128)
             to_e(i, [&](float a) {
                 const uint32_t b = __float_as_uint(a);
-                sum += weight_of(a);
                 // 16 bits of the mantissa: at most 2^15 logits a slice, so 32 bits hold their sum
                 if (b >= BIN0 << 17)
                     atomicAdd(&s.hist[BINS - 1 + BIN0 - (b >> 17)], ((b & 0x7FFFFFu) + 0x800080u) >> 8);
@@ -653,18 +693,13 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
     kept = warp_sum64(kept);
     if (lane == 0) s.wsum[warp] = kept;
     if (with_p) {
-        sum = cta_sum64(s, sum);
-        if (tid == 0) s.total = sum;
         double limit = 0.;
-        // the bin in which the histogram, from the top, passes the limit (in units of 2^-40)
+        // the bin in which the histogram, from the top, passes the limit (in units of 2^-40; nearly exact)
         R.locate([](uint32_t v, int i) {
             const int o = ((BINS - 1 - i) >> 6) - 15;   // of e's exponent
             return o >= 0 ? (u64)v << o : (u64)v >> -o;
-        }, [&](u64 c) { return !((double)c < limit); }, [&] {
-            u64 Z = 0;
-            from_all(cl, C, &s.total, [&](int, u64 v) { Z += v; });
-            limit = __dmul_rn((double)top_p, (double)Z);
-        });
+        }, [&](u64 c) { return !((double)c < limit); },
+        [&](u64 part) { limit = __dmul_rn((double)top_p, (double)cta_sum64(s, part)); });
         // What lies above that bin is added up, what lies in it listed, and each listed entry finds the weight in
         // front of it (attempt 0, on the next bin if the border turns out to lie there); a bin with too many entries is
         // searched by radix (1).  e is monotone in l up to rounding only, so the border has to lie clearly inside the
@@ -677,7 +712,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             lo = attempt == 3 || b0 <= 0 ? 0.f : __uint_as_float((uint32_t)(b0 + BIN0) << 17);
             hi = attempt == 3 ? 2.f : __uint_as_float((uint32_t)(b1 + BIN0) << 17);
             auto inside = [&](float v) { return v >= lo && v < hi; };
-            auto clear = [&](float v) {    // of a border at e = v (exp_of is within 2^-20)
+            auto clear = [&](float v) {    // of a border at e = v (exp_of is within 2^-20); the largest l always is
                 return (lo == 0.f || v > lo * 1.000002f) && (hi > 1.f || v < hi * 0.999998f);
             };
             u64 above = 0;
@@ -685,52 +720,61 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
                 __syncthreads();
                 if (tid == 0) s.n_list = 0;
                 __syncthreads();
+                u64 all = 0;
                 sum = kept = 0;
                 for (int i = w0 + lane * 4; i < w0 + seg; i += 128) {
                     const float4 v = *(const float4*)(e + i);
                     const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        const u64 w = weight_of(a[j]);
+                        all += w;
                         if (a[j] >= hi) {
-                            const u64 w = weight_of(a[j]);
                             sum += w;
                             if (a[j] >= min_p) kept += w;
                         } else if (a[j] >= lo && a[j] > 0.f && attempt == 0) {
-                            R.push(order_key(R.l_of(base + i + j)), base + i + j, a[j]);
+                            R.push(0u, base + i + j, a[j]);   // (its key: below)
                         }
                     }
                 }
                 kept = warp_sum64(kept);
                 if (lane == 0) s.wsum[warp] = kept;
                 sum = cta_sum64(s, sum);
-                if (tid == 0) s.above = sum;
+                all = cta_sum64(s, all);
+                if (tid == 0) { s.above = sum; s.total = all; }
+                if (attempt == 0)
+                    for (int i = tid; i < min(s.n_list, LIST); i += GT) s.lkey[i] = order_key(R.l_of(s.lid[i]));
             }
             int own = 0, n = -1;
             if (attempt == 0) n = R.merge(&own);
             else cl.sync();
             from_all(cl, C, &s.above, [&](int, u64 v) { above += v; });
+            {
+                u64 Z = 0;
+                from_all(cl, C, &s.total, [&](int, u64 v) { Z += v; });
+                limit = __dmul_rn((double)top_p, (double)Z);
+            }
             if (attempt == 0 && n < 0) { attempt = 1; cl.sync(); continue; }
             if (attempt == 0) {
-                // eight threads add up what is in front of an entry of this CTA; the last entry kept is the border
-                const int mine = s.n_list;
+                // a few threads add up what is in front of an entry of this CTA; the last entry kept is the border
+                const int mine = s.n_list, per = mine <= GT / 32 ? 32 : mine <= GT / 16 ? 16 : 8;
                 if (tid == 0) s.pick = 0;     // 1: the border is here, 2: but not clear of the bin's ends
                 __syncthreads();
-                for (int i0 = 0; i0 < mine; i0 += GT / 8) {
-                    const int i = min(i0 + tid / 8, mine - 1), id = s.sid[own + i];
+                for (int i0 = 0; i0 < mine; i0 += GT / per) {
+                    const int i = min(i0 + tid / per, mine - 1), id = s.sid[own + i];
                     const uint32_t a = s.skey[own + i];
                     u64 before = 0;
 #pragma unroll 4
-                    for (int j = tid & 7; j < n; j += 8) {
+                    for (int j = tid & (per - 1); j < n; j += per) {
                         const uint32_t o = s.skey[j];
                         if (o > a || (o == a && s.sid[j] < id)) before += s.sw[j];
                     }
-#pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+                    for (int o = 1; o < per; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
                     before += above;
                     const bool in = (double)before < limit;
-                    if ((tid & 7) == 0) {
+                    if ((tid & (per - 1)) == 0) {
                         s.keep[i] = in;
-                        if (in && !((double)(before + s.sw[own + i]) < limit)) atomicOr(&s.pick, clear(s.le[i]) ? 1 : 2);
+                        if (in && !((double)(before + s.sw[own + i]) < limit)) atomicOr(&s.pick, clear(s.le[i]) || a == order_key(m) ? 1 : 2);
                     }
                 }
                 cl.sync();
@@ -767,7 +811,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
                 each_inside([&](int i) { f(order_key(R.l_of(base + i)), weight_of(e[i])); });
             }, [&](u64 c) { return !((double)c < limit); }, 32, &edge, &above);
             const float eb = exp_of(__fsub_rn(order_key_inv(edge), m));
-            if (found && !clear(eb)) found = false;
+            if (found && !clear(eb) && edge != order_key(m)) found = false;
             if (!found) {
                 cl.sync();
                 ++attempt;
@@ -780,10 +824,10 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             u64 ties = 0;
             each_inside([&](int i) { ties += order_key(R.l_of(base + i)) == edge; });
             ties = cta_sum64(s, ties);
-            if (tid == 0) s.total = ties;
+            if (tid == 0) s.above = ties;
             cl.sync();
             u64 all = 0;
-            from_all(cl, C, &s.total, [&](int, u64 v) { all += v; });
+            from_all(cl, C, &s.above, [&](int, u64 v) { all += v; });
             int cut = V;
             if (n_tie < (long long)all) {
                 uint32_t key = 0;
@@ -833,6 +877,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
         if (r < rank) before += v;
         Z += v;
     });
+    cl.sync();    // from here on a CTA works on its own memory alone
     for (int w = 0; w < warp; ++w) before += s.wsum[w];
     const u64 mine = s.wsum[warp];
     const u64 target = target_of(Z);
@@ -862,7 +907,6 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, c
             if (i - lane * 4 + 128 >= w0 + seg) break;
         }
     }
-    cl.sync();
 }
 
 template <typename T>
@@ -893,7 +937,8 @@ cudaError_t launch_t(int n, int V, const void* logits, int64_t ld, const float* 
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_given_kernel<T>, V, slice, (const T*)logits, ld, u, temp, topk, topp, minp,
+    const int ahead = max(1, 2 * device_sm_count() / C);   // rows that run at once, with two CTAs an SM
+    return cudaLaunchKernelEx(&cfg, sample_given_kernel<T>, V, slice, n, ahead, (const T*)logits, ld, u, temp, topk, topp, minp,
                               ids, logprob, err);
 }
 
