@@ -271,8 +271,9 @@ size_t paged_workspace_bytes() {
 }
 
 cudaError_t launch_paged_attention(const PagedAttn& a, cudaStream_t st) {
-    if (a.kv == Q3_F32) return (int64_t)a.max_q * a.c.G <= 16 ? launch_f32<16>(a, st) : launch_f32<64>(a, st);
-    return paged_decode_takes(a) ? launch_paged_decode(a, st) : launch_paged_chunk(a, st);
+    if (paged_decode_takes(a)) return launch_paged_decode(a, st);
+    if (a.kv == Q3_BF16) return launch_paged_chunk(a, st);
+    return (int64_t)a.max_q * a.c.G <= 16 ? launch_f32<16>(a, st) : launch_f32<64>(a, st);
 }
 
 }  // namespace q3

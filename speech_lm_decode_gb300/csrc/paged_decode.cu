@@ -1,6 +1,6 @@
 // Paged attention for few query rows (single tokens, a handful of tokens of a
-// sequence) over bf16 pages: q3paged_attention's kernel while the new tokens
-// times the q heads of a kv head fit one tile of tensor-core rows.
+// sequence): q3paged_attention's kernel while the new tokens times the q heads
+// of a kv head fit a tile or two of tensor-core columns.
 //
 // Bound by reading K and V once (512 bytes a key and kv head).  A CTA of four
 // warps walks its keys in blocks of 16, a warp to a block; K and V go from
@@ -18,6 +18,8 @@
 // exact), whose scores are added up across lanes; the weights enter the second
 // product as their three parts the same way, so that fp32 needs no further
 // tensor-core work.
+//
+// fp32 pages are multiplied on the CUDA cores, eight lanes a key.
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.h"
@@ -34,7 +36,7 @@ constexpr int d_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of a
 constexpr int D_OVER = 0;         // units that an item costs besides its keys
 constexpr int D_MIN_UNITS = D_OVER + 1;
 
-__device__ __forceinline__ uint4 ldg16(const bf16* p, bool ok) {
+__device__ __forceinline__ uint4 ldg16(const void* p, bool ok) {
     uint4 r;
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
@@ -75,11 +77,11 @@ __device__ __forceinline__ uint32_t part2(float x0, float x1, int p) {
 
 // NT: column tiles of eight; a query row takes one column (bf16 activations) or
 // four (the parts of fp32 ones; columns 8 n + 2 p + e hold part p of row 2 n + e).
-template <typename TA, int NT>
+template <typename TA, typename TK, int NT>
 __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const PagedAttn a, int grid_max) {
     pdl_wait();
     pdl_trigger();
-    constexpr bool F32 = sizeof(TA) == 4;
+    constexpr bool F32 = sizeof(TA) == 4, KV32 = sizeof(TK) == 4;
     constexpr int RG = F32 ? 2 * NT : 8 * NT;   // query rows of an item
     const PagedView& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -124,18 +126,135 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
         const int key1 = (int)min((long long)q.ctx, (long long)(seg_end - item0 - D_OVER) * DU);
         const int rows = min(RG, q.n_new * c.G - rg * RG);
 
-        // ---- blocks of 16 keys: lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9
         const int nb = (key1 - key0 + 15) >> 4;
         const int32_t* table = c.table + (int64_t)s * c.max_pages;
         const int pmask = (1 << c.page_shift) - 1;
         const int64_t head_off = (int64_t)h * c.head_stride;
-        const bf16* kbase = (const bf16*)c.k + head_off + g * c.token_stride + t * 8;
-        const bf16* vbase = (const bf16*)c.v + head_off + 2 * t * c.token_stride + g * 8;
         auto page_at = [&](int b) -> int {   // page of block b; < 0: none
             if (b >= nb) return -1;
             const int pg = __ldg(table + ((key0 + b * 16) >> c.page_shift));
             return (unsigned)pg < (unsigned)c.n_pages ? pg : -1;
         };
+        if constexpr (KV32) {
+            // ---- fp32 pages: eight lanes a key (four of its values out of every 32), four keys a step, the next
+            // step's K and V on their way; each group of eight lanes keeps its own maximum, sum and output
+            const int grp = lane >> 3, sub = lane & 7;
+            const float* kbase = (const float*)c.k + head_off + sub * 4;
+            const float* vbase = (const float*)c.v + head_off + sub * 4;
+            const int steps = warp < nb ? 4 * ((nb - warp + DW - 1) / DW) : 0;
+            uint4 kr[2][4], vr[2][4];
+            int pg = -1, pgn = page_at(warp);
+            bool lost = false;
+            auto load = [&](int buf, int i) {
+                const int b = warp + DW * (i >> 2), key = key0 + b * 16 + (i & 3) * 4 + grp;
+                if ((i & 3) == 0) { pg = pgn; pgn = page_at(b + DW); lost |= pg < 0; }
+                const bool ok = pg >= 0 && key < key1;
+                const int64_t off = (int64_t)max(pg, 0) * c.page_stride + (int64_t)(key & pmask) * c.token_stride;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    kr[buf][j] = ldg16(kbase + off + 32 * j, ok);
+                    vr[buf][j] = ldg16(vbase + off + 32 * j, ok);
+                }
+                return pg >= 0;
+            };
+            bool there[2] = {true, true};
+            if (steps > 0) there[0] = load(0, 0);
+            float qf[RG][16], o[RG][16], mx[RG], l[RG];
+            int lim[RG];
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                const bool row = r < rows;
+                const int rr = rg * RG + r, tok = rr / c.G;
+                const float* src = (const float*)a.q + (int64_t)(q.row0 + (row ? tok : 0)) * a.q_stride +
+                                   (int64_t)(h * c.G + (row ? rr - tok * c.G : 0)) * HD + sub * 4;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 f = row ? *(const float4*)(src + 32 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    qf[r][4 * j] = f.x; qf[r][4 * j + 1] = f.y; qf[r][4 * j + 2] = f.z; qf[r][4 * j + 3] = f.w;
+                }
+                lim[r] = row ? min(q.ctx - q.n_new + tok + 1, key1) : 0;
+                mx[r] = -INFINITY;
+                l[r] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[r][j] = 0.f;
+            }
+            auto compute = [&](int buf, int i) {
+                const int key = key0 + (warp + DW * (i >> 2)) * 16 + (i & 3) * 4 + grp;
+                float x[RG];
+                bool grew = false;
+#pragma unroll
+                for (int r = 0; r < RG; ++r) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v = fmaf(qf[r][4 * j], __uint_as_float(kr[buf][j].x), v);
+                        v = fmaf(qf[r][4 * j + 1], __uint_as_float(kr[buf][j].y), v);
+                        v = fmaf(qf[r][4 * j + 2], __uint_as_float(kr[buf][j].z), v);
+                        v = fmaf(qf[r][4 * j + 3], __uint_as_float(kr[buf][j].w), v);
+                    }
+                    v += __shfl_xor_sync(0xffffffffu, v, 1);
+                    v += __shfl_xor_sync(0xffffffffu, v, 2);
+                    v += __shfl_xor_sync(0xffffffffu, v, 4);
+                    x[r] = there[buf] && key < lim[r] ? v : -INFINITY;
+                    grew |= x[r] > mx[r] + slack;
+                }
+                if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                    for (int r = 0; r < RG; ++r) {
+                        const float m = fmaxf(mx[r], x[r]), f = m == -INFINITY ? 1.f : ex2((mx[r] - m) * sl2);
+                        mx[r] = m;
+                        l[r] *= f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[r][j] *= f;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < RG; ++r) {
+                    const float p = ex2(fmaf(x[r], sl2, mx[r] == -INFINITY ? 0.f : -mx[r] * sl2));
+                    l[r] += p;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        o[r][4 * j] = fmaf(p, __uint_as_float(vr[buf][j].x), o[r][4 * j]);
+                        o[r][4 * j + 1] = fmaf(p, __uint_as_float(vr[buf][j].y), o[r][4 * j + 1]);
+                        o[r][4 * j + 2] = fmaf(p, __uint_as_float(vr[buf][j].z), o[r][4 * j + 2]);
+                        o[r][4 * j + 3] = fmaf(p, __uint_as_float(vr[buf][j].w), o[r][4 * j + 3]);
+                    }
+                }
+            };
+            for (int i = 0; i < steps; i += 2) {      // (a multiple of four)
+                there[1] = load(1, i + 1);
+                compute(0, i);
+                if (i + 2 < steps) there[0] = load(0, i + 2);
+                compute(1, i + 1);
+            }
+            if (lost && lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
+            __syncthreads();   // the previous segment's readers are done
+#pragma unroll
+            for (int r = 0; r < RG; ++r) {
+                float m = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 8));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                const float f = ex2((mx[r] - (m == -INFINITY ? 0.f : m)) * sl2);
+                l[r] *= f;
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    o[r][j] *= f;
+                    o[r][j] += __shfl_xor_sync(0xffffffffu, o[r][j], 8);
+                    o[r][j] += __shfl_xor_sync(0xffffffffu, o[r][j], 16);
+                }
+                if (grp == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *(float4*)&so[warp][r][32 * j + sub * 4] =
+                            make_float4(o[r][4 * j], o[r][4 * j + 1], o[r][4 * j + 2], o[r][4 * j + 3]);
+                }
+                if (lane == 0) { sm_m[warp][r] = m; sm_l[warp][r] = l[r]; }
+            }
+        } else {
+        // ---- bf16 pages: blocks of 16 keys, lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9
+        const bf16* kbase = (const bf16*)c.k + head_off + g * c.token_stride + t * 8;
+        const bf16* vbase = (const bf16*)c.v + head_off + 2 * t * c.token_stride + g * 8;
         uint4 kr[2][4], vr[4][2];
         auto load_k = [&](int b, int pg) {
             const int kb = key0 + b * 16;
@@ -320,6 +439,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
                     *(float2*)&so[warp][8 * n + 2 * t + e][64 * (i >> 2) + 8 * g + 2 * (i & 3)] =
                         make_float2(o[n][i >> 2][i & 3][e], o[n][i >> 2][i & 3][e + 2]);
         }
+        }
         __syncthreads();
         const bool whole = u == item0 && seg_end == item0 + nu;
         const int ca = paged_cut_first(R, item0), cb = paged_cut_last(R, item0 + nu);   // where it is cut
@@ -339,7 +459,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
             for (int w = 0; w < DW; ++w) {
                 const float f = ex2((sm_m[w][r] - ms) * sl2);
                 float v;
-                if constexpr (F32) {
+                if constexpr (F32 && !KV32) {
                     const int col = 8 * (r >> 1) + (r & 1);
                     v = so[w][col][tid] + so[w][col + 2][tid] + so[w][col + 4][tid];
                 } else {
@@ -420,24 +540,25 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
     }
 }
 
-template <typename TA, int NT>
+template <typename TA, typename TK, int NT>
 cudaError_t launch_t(const PagedAttn& a, cudaStream_t st) {
     const int grid = min(device_sm_count(), 160) * d_ctas(NT);
-    return launch_pdl(paged_decode_kernel<TA, NT>, grid, DW * 32, 0, st, a, grid);
+    return launch_pdl(paged_decode_kernel<TA, TK, NT>, grid, DW * 32, 0, st, a, grid);
 }
 
 }  // namespace
 
 size_t paged_decode_ws() { return (size_t)PAGED_MAX_CTAS * 2 * 16 * (HD + 4) * sizeof(float); }
 
-bool paged_decode_takes(const PagedAttn& a) {
-    return a.kv == Q3_BF16 && (int64_t)a.max_q * a.c.G <= (a.act == Q3_BF16 ? 16 : 8);
-}
+// rows of a kv head that one sequence may have: one tile of columns (bf16), two (fp32: the keys are read twice, by
+// neighbours of the same L2)
+bool paged_decode_takes(const PagedAttn& a) { return (int64_t)a.max_q * a.c.G <= (a.act == Q3_BF16 ? 16 : 8); }
 
 cudaError_t launch_paged_decode(const PagedAttn& a, cudaStream_t st) {
     const int rows = a.max_q * a.c.G;
-    if (a.act == Q3_BF16) return rows <= 8 ? launch_t<bf16, 1>(a, st) : launch_t<bf16, 2>(a, st);
-    return rows <= 2 ? launch_t<float, 1>(a, st) : launch_t<float, 2>(a, st);
+    if (a.act == Q3_BF16) return rows <= 8 ? launch_t<bf16, bf16, 1>(a, st) : launch_t<bf16, bf16, 2>(a, st);
+    if (a.kv == Q3_BF16) return rows <= 2 ? launch_t<float, bf16, 1>(a, st) : launch_t<float, bf16, 2>(a, st);
+    return rows <= 2 ? launch_t<float, float, 1>(a, st) : launch_t<float, float, 2>(a, st);
 }
 
 }  // namespace q3
