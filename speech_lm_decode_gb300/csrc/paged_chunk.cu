@@ -62,7 +62,6 @@ struct ChunkSmem {
     uint32_t tmem;
     int dead, last;
     float ref[CT];           // one tile of rows: the maxima that both slots' weights refer to
-    float m[CT], l[CT];      // slot 1's maximum and sum for slot 0
     PagedRange range;        // the softmax warps' walk, kept here to save them the registers
     Walk walk;
     Seg seg;
@@ -624,15 +623,19 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 rc += (g.n + t) / 2;      // the other slot's steps
                 pvc += g.n;
                 // both slots' sums, at the last maximum
-                if (t == 1) { sm.m[r] = mx; sm.l[r] = l; }
+                float* stats = (float*)(qs + (F32 ? 2 : 1) * STAGE);   // [maxima, sums][slot][row], where Q is not needed
+                stats[t * CT + r] = mx;
+                stats[(2 + t) * CT + r] = l;
                 wg_sync(2);
-                if (t == 0 && g.n > 0) {
-                    const float m = sm.ref[r], ms = m == -INFINITY ? 0.f : m;
-                    l = l * ex2f((mx - ms) * sl2) + sm.l[r] * ex2f((sm.m[r] - ms) * sl2);
-                    mx = m;
+                l = 0.f;
+                if (g.n > 0) {
+                    mx = sm.ref[r];
+                    const float ms = mx == -INFINITY ? 0.f : mx;
+                    l = stats[2 * CT + r] * ex2f((stats[r] - ms) * sl2) + stats[3 * CT + r] * ex2f((stats[CT + r] - ms) * sl2);
                 }
             }
-            const bool mine = g.two || t == 0;
+            // blocks of 32 values that this thread puts out: of its own row, or (one tile) half of the row's
+            const int blk0 = g.two ? 0 : 2 * t, blk1 = g.two ? 4 : blk0 + 2;
             TA* dst = (TA*)a.out + (int64_t)(wq.row0 + tok) * a.out_stride + (int64_t)head * HD;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             // The output leaves through the tile's place for Q, whose products are done: a thread puts 32 values of its
@@ -669,10 +672,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             // partials: [32 groups of 4 values][256 rows], then maxima and sums
             const int prow = tile * CT + r;
             float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == g.ca ? 1 : 0)) * C_SLOT;
-            if (mine) {
+            {
                 const float w0 = g.whole ? inv : 1.f;
 #pragma unroll 1
-                for (int c2 = 0; c2 < 4; c2 += 2) {
+                for (int c2 = blk0; c2 < blk1; c2 += 2) {
                     uint32_t x[2][32];
                     if (g.n > 0) {
                         tmem_ld32(tO + 32 * c2, x[0]);
@@ -697,8 +700,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                 }
                 if (g.whole) {
-                    flush(0, 4);
-                } else {
+                    flush(blk0, blk1);
+                } else if (blk0 == 0) {
                     slot[2 * CT * HD + prow] = mx;
                     slot[2 * CT * HD + 2 * CT + prow] = l;
                 }
@@ -714,8 +717,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 }
                 wg_sync(3);
                 if (sm.last) {
-                    // every row by its thread; with one tile of rows, slot 1's thread takes the upper half of the head
-                    const int mrow = tile * CT + r, b0 = g.two ? 0 : 2 * t, b1 = g.two ? 4 : b0 + 2;
+                    const int mrow = tile * CT + r;
                     auto part = [&](int cc) { return parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT; };
                     float m = -INFINITY, sum = 0.f;
 #pragma unroll 1
@@ -738,7 +740,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                     const float ms = m == -INFINITY ? 0.f : m, rs = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
-                    for (int b = b0; b < b1; ++b) {
+                    for (int b = blk0; b < blk1; ++b) {
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.f;
@@ -770,7 +772,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         for (int i = 0; i < 32; ++i) v[i] *= rs;
                         put(b, v);
                     }
-                    flush(b0, b1);
+                    flush(blk0, blk1);
                 }
             }
             wg_sync(1);
