@@ -26,13 +26,15 @@ int paged_fail(int code, const char* fmt, ...) {
 namespace {
 
 // ------------------------------------------------------------------ append
-// Bound by the bytes moved: 12 KB in and out a token (16/8 heads, bf16).  A warp
+// Bound by the bytes moved (18 KB in and out a token with 16/8 heads in bf16)
+// and, below that, by the chain position -> page -> stores of a warp.  A warp
 // takes NL 16-byte loads of one token, all in flight together; a head is 16
 // lanes of 8 bf16 or 32 lanes of 4 fp32 values, so a load brings two heads or
-// one.  The rotation's pair (j, j + 64) lies half a head's lanes apart.
+// one, and the rotation's pair (j, j + 64) lies half a head's lanes apart.
 // With few tokens a warp takes one load, so that the heads of a token run
-// beside each other; with many, eight (prompts of 32 sequences, 9 thousand
-// tokens, bf16: 55 us with 256-byte loads of four heads, see launch).
+// beside each other (256 tokens, fp32: 3.1 us; one: 2.0 us); from 1024 on eight
+// (9374 tokens of 32 prompts, bf16: 42 us, 4.0 TB/s; with 8-byte lanes and four
+// heads a warp 55 us, with four loads 43 us).
 constexpr int APPEND_WARPS = 4;
 
 // 16 bytes of activations as fp32 values
@@ -51,7 +53,7 @@ __device__ __forceinline__ void put(bf16* p, const float (&v)[4]) { *(uint2*)p =
 __device__ __forceinline__ void put(float* p, const float (&v)[4]) { *(float4*)p = make_float4(v[0], v[1], v[2], v[3]); }
 
 template <typename TA, typename TK, int NL>
-__global__ void __launch_bounds__(APPEND_WARPS * 32)
+__global__ void __launch_bounds__(APPEND_WARPS * 32, 8)
 paged_append_kernel(PagedView c, int n_tokens, const TA* qkv, int64_t ldq, const int32_t* __restrict__ tok_seq,
                     const int32_t* __restrict__ tok_pos, const float* __restrict__ qn, const float* __restrict__ kn,
                     float eps, const float2* __restrict__ rope, int rope_rows, TA* q_out, int64_t ldo, int* err) {
@@ -101,7 +103,7 @@ paged_append_kernel(PagedView c, int n_tokens, const TA* qkv, int64_t ldq, const
             for (int j = 0; j < VL; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
             for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = 1.0f / sqrtf(ss / (float)HD + eps);
+            const float r = rsqrtf(fmaf(ss, 1.0f / HD, eps));   // within 2^-22
             if (h < c.nq + c.nkv) {
                 const float4* w = (const float4*)((h < c.nq ? qn : kn) + sub * VL);
 #pragma unroll
