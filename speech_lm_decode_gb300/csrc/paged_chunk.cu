@@ -17,8 +17,11 @@
 // take the tile's even and odd key tiles, with one output and one reference
 // maximum that is handed on from step to step.
 //
-// fp32 activations enter as three bf16 parts of q and of p (24 bits): 6 products
-// for 2.
+// fp32 activations enter as three bf16 parts of q (24 bits: exact) and two of p
+// (17 bits), 5 products for 2.  The parts of p have an output each, as the
+// tensor cores cut the terms of a sum to the bits of its largest one: with one
+// output and three parts of p the error was no smaller (2e-6 to 7e-6 of the
+// result, growing with the context) and the call a fifth slower.
 //
 // Every wait is bounded: one that runs out sets the timeout bit, after which
 // the CTA goes through its remaining steps without waiting or issuing, drains
@@ -236,10 +239,10 @@ __global__ void __launch_bounds__(C_THREADS, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                    const __grid_constant__ PagedAttn a) {
     constexpr bool F32 = sizeof(TA) == 4;
-    constexpr int ST = c_stages(F32), QP = F32 ? 3 : 1, PP = F32 ? 3 : 1;
-    // tensor memory: the slots' scores (and weights over them), then their outputs; fp32 has one output, but weights
-    // of three parts
-    constexpr int SLOT = F32 ? 192 : CT, OUT = 2 * SLOT;
+    constexpr int ST = c_stages(F32), QP = F32 ? 3 : 1, PP = F32 ? 2 : 1;
+    // tensor memory: the slots' scores (the weights over them), then outputs: of the two tiles, or (fp32) of the
+    // weights' two parts
+    constexpr int SLOT = CT, OUT = 2 * SLOT;
     extern __shared__ __align__(1024) unsigned char raw[];
     __shared__ ChunkSmem sm;
     unsigned char* base = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -351,11 +354,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const uint32_t qd = uniform(tile_desc(q0 + (!F32 && g.two ? t : 0) * STAGE, 16)), d = uniform(tmem + t * SLOT);
             if (ok && elect_one()) {
 #pragma unroll
-                for (int p = 0; p < QP; ++p)
+                for (int p = QP - 1; p >= 0; --p)     // the smallest part first: sums are cut to the bits of the largest term
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t off = ((ks >> 2) * (STAGE / 2) + (ks & 3) * 32) >> 4;
-                        umma_ss(d, qd + p * (STAGE >> 4) + off, kd + off, IDESC, (p | ks) != 0);
+                        umma_ss(d, qd + p * (STAGE >> 4) + off, kd + off, IDESC, p != QP - 1 || ks != 0);
                     }
                 commit(&sm.s_full[t]);
             }
@@ -371,8 +374,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 for (int p = 0; p < PP; ++p)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_ts(d, pa + 64 * p + 8 * ks, vd + ks * (2048 >> 4), IDESC_V,
-                                (p | ks) != 0 ? 1u : first);
+                        umma_ts(d + p * CT, pa + 64 * p + 8 * ks, vd + ks * (2048 >> 4), IDESC_V, ks != 0 ? 1u : first);
             }
             __syncwarp();
         };
@@ -559,7 +561,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                             fence_after();
                         }
 #pragma unroll 1
-                        for (int cc = 0; cc < 8; ++cc) {
+                        for (int cc = 0; cc < 8 * PP; ++cc) {
                             uint32_t y[16];
                             tmem_ld16(tO + 16 * cc, y);
 #pragma unroll
@@ -580,7 +582,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 f2c sums = pair(0.f, 0.f);
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t hi[16], mid[16], lo[16];
+                    uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float p0, p1;
@@ -589,18 +591,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         p1 = ex2f(p1);
                         sums = add_pair(sums, pair(p0, p1));
                         hi[i] = pack_bf16(p0, p1);
-                        if constexpr (F32) {
-                            p0 -= __uint_as_float(hi[i] << 16);
-                            p1 -= __uint_as_float(hi[i] & 0xffff0000u);
-                            mid[i] = pack_bf16(p0, p1);
-                            lo[i] = pack_bf16(p0 - __uint_as_float(mid[i] << 16), p1 - __uint_as_float(mid[i] & 0xffff0000u));
-                        }
+                        if constexpr (F32)
+                            lo[i] = pack_bf16(p0 - __uint_as_float(hi[i] << 16), p1 - __uint_as_float(hi[i] & 0xffff0000u));
                     }
                     tmem_st16(tS + 16 * cc, hi);
-                    if constexpr (F32) {
-                        tmem_st16(tS + 64 + 16 * cc, mid);
-                        tmem_st16(tS + 128 + 16 * cc, lo);
-                    }
+                    if constexpr (F32) tmem_st16(tS + 64 + 16 * cc, lo);
                 }
                 tmem_wait_st();
                 fence_before();
@@ -682,6 +677,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         tmem_ld32(tO + 32 * c2 + 32, x[1]);
                         tmem_wait_ld(x[0]);
                         tmem_wait_ld(x[1]);
+                        if constexpr (F32) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t y[32];
+                                tmem_ld32(tO + CT + 32 * (c2 + e), y);
+                                tmem_wait_ld(y);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    x[e][i] = __float_as_uint(__uint_as_float(x[e][i]) + __uint_as_float(y[i]));
+                            }
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
