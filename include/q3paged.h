@@ -101,12 +101,15 @@ size_t q3paged_workspace_bytes(const q3paged_cache* c);
  *   max_q      upper bound of the new tokens of any one sequence (it chooses
  *              the kernel; a sequence with more sets Q3PAGED_ERR_BOUNDS)
  *   scale      factor of the scores, > 0 (1/sqrt(128) for the talker)
- *   out        [n_tokens][nq * 128] activations, row stride out_stride
+ *   out        [n_tokens][nq * 128] activations, row stride out_stride (0:
+ *              packed); may be q itself (with its stride)
  * Token i of sequence s stands at position ctx_len[s] - n_s + i and sees the
  * positions up to its own; one that sees nothing (a negative position) gets
- * zeros.  Rows from q_off[n_seqs] on are left as they are.  Softmax and sums
- * are fp32; with fp32 activations over bf16 pages the products are exact to
- * about 2^-17 of a value.  Values of keys below ctx_len must be finite; what
+ * zeros.  Rows from q_off[n_seqs] on are left as they are, and so are those of
+ * a sequence that is skipped for its offsets.  Softmax and sums are fp32.  bf16
+ * activations: the weights enter the second product as bf16.  fp32 activations
+ * over bf16 pages: q enters with its 24 bits, the weights with 17 (chunks) or
+ * 24 (few rows).  Values of keys below ctx_len must be finite; what
  * pages hold beyond it does not matter.  err may be NULL.  Errors: Q3_ERR_ARG,
  * Q3_ERR_CAPACITY (workspace too small), Q3_ERR_CUDA. */
 int q3paged_attention(const q3paged_cache* c, int n_tokens, int max_q, const void* q, int64_t q_stride,

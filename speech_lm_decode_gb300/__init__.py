@@ -592,7 +592,11 @@ class PagedKV:
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         c = PagedCache()
         c.n_pages, c.n_kv_heads, c.page_size, c.head_dim = k_pages.shape
-        c.page_stride, c.head_stride, c.token_stride = k_pages.stride()[:3]
+        # 0 stands for packed: of an axis of one entry, whatever the tensor says
+        steps = [st if size > 1 else 0 for size, st in zip(k_pages.shape[:3], k_pages.stride())]
+        if any(size > 1 and st < 128 for size, st in zip(k_pages.shape[:3], steps)):
+            raise ValueError("k_pages and v_pages: pages, heads and positions must not share memory")
+        c.page_stride, c.head_stride, c.token_stride = steps
         c.n_q_heads = n_q_heads
         c.kv_dtype = _dtype_code(k_pages)
         c.n_seqs, c.max_pages = page_table.shape
@@ -635,6 +639,8 @@ class PagedKV:
         if not ((n == 3 and shape[1] == heads and shape[2] == 128 and stride[2] == 1 and (heads == 1 or stride[1] == 128))
                 or (n == 2 and shape[1] == width and stride[1] == 1)):
             raise ValueError(f"{name}: rows of {width} contiguous values are expected")
+        if shape[0] > 1 and stride[0] < width:
+            raise ValueError(f"{name}: rows must not share memory")
         return shape[0], (stride[0] if shape[0] > 1 else width)
 
     def _act(self, t):
@@ -671,7 +677,7 @@ class PagedKV:
     def attend(self, q, q_off, ctx_len, max_q: int, scale=128 ** -0.5, out=None):
         """Causal attention of the newest tokens of every sequence: rows q_off[s]..q_off[s+1]-1 of q [n, nq, 128]
         are the last ones of sequence s, which has ctx_len[s] positions (int32 tensors); max_q bounds the new
-        tokens of a sequence.  Returns [n, nq, 128]."""
+        tokens of a sequence.  Returns [n, nq, 128]; `out` may be q itself."""
         from torch import int32
         c = self._act(q)
         n, ld = self._rows(q, "q", self.nq)
@@ -684,7 +690,9 @@ class PagedKV:
         return out
 
     def check(self):
-        """Waits for the work so far and raises where the device met a page, position or length out of range."""
+        """Waits for the device and raises where it met a page, position or length out of range since the last check."""
+        import torch
+        torch.cuda.synchronize(self.device)
         e = int(self.err.item())
         if e:
             self.err.zero_()
@@ -703,6 +711,8 @@ def sample_given(logits, u, temperature, top_k, top_p, min_p, ids=None, logprob=
             (logits.shape[1] <= 1 or logits.stride(1) == 1)):
         raise ValueError("logits: a CUDA tensor [n, vocab] with contiguous rows is expected")
     (n, vocab), dev, f = logits.shape, logits.get_device(), torch.float32
+    if n > 1 and logits.stride(0) < vocab:
+        raise ValueError("logits: rows must not share memory")
     if ids is None:
         ids = torch.empty(n, dtype=torch.int32, device=logits.device)
     if logprob is None:

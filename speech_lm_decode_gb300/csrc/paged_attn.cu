@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
             for (int z = 1; z < 16; z <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], z);
         auto store = [&](int r, const float (&v)[8], float sum) {
             const int tok = tok0 + r / c.G;
-            const float f = sum > 0.f ? 1.f / sum : 0.f;
+            const float f = sum != 0.f ? 1.f / sum : 0.f;   // (NaN stays NaN)
             float* dst = (float*)a.out + (int64_t)(q.row0 + tok) * a.out_stride + (int64_t)(h * c.G + r % c.G) * HD + tx * 4;
             *(float4*)dst = make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
             *(float4*)(dst + 64) = make_float4(v[4] * f, v[5] * f, v[6] * f, v[7] * f);

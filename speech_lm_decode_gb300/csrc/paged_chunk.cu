@@ -325,9 +325,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             }
             if (w.more) walk_step<CT, C_OVER>(w, a, R, tpi);
         }
-        // given up: nothing may still be writing this CTA's shared memory when it leaves
-        if (*(volatile int*)&sm.dead)
-            for (int i = max(0, issued - ST); i < issued; ++i) bar_wait(&sm.full[i % ST], (i / ST) & 1, sm, a.err, false);
+        // nothing may still be writing this CTA's shared memory when it leaves (given up, its last copies are not
+        // waited for elsewhere)
+        for (int i = max(0, issued - ST); i < issued; ++i) bar_wait(&sm.full[i % ST], (i / ST) & 1, sm, a.err, false);
     } else if (warp == 1) {
         // ---------------------------------------------------------- products
         int cnt = 0, pc[2] = {0, 0}, qc = 0;
@@ -476,7 +476,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         const uint4* src = (const uint4*)((const TA*)a.q + (int64_t)(wq.row0 + (there ? rt : 0)) * a.q_stride +
                                                           (int64_t)(g.h * c.G + (there ? row - rg * c.G : 0)) * HD + ch * 8);
 #pragma unroll
-                        for (int j = 0; j < V4; ++j) raw[b][j] = there ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < V4; ++j) raw[b][j] = there ? src[j] : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
@@ -632,7 +632,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             // blocks of 32 values that this thread puts out: of its own row, or (one tile) half of the row's
             const int blk0 = g.two ? 0 : 2 * t, blk1 = g.two ? 4 : blk0 + 2;
             TA* dst = (TA*)a.out + (int64_t)(wq.row0 + tok) * a.out_stride + (int64_t)head * HD;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;   // (NaN stays NaN)
             // The output leaves through the tile's place for Q, whose products are done: a thread puts 32 values of its
             // row, then the warp stores its rows side by side (16-byte pieces at places that depend on the row).
             constexpr int PR = HD * (int)sizeof(TA) / 16, PB = PR / 4;   // pieces of a row, of 32 values
@@ -694,7 +694,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         const int cc = c2 + e;
                         float v[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = l > 0.f ? __uint_as_float(x[e][i]) * w0 : 0.f;
+                        for (int i = 0; i < 32; ++i) v[i] = l != 0.f ? __uint_as_float(x[e][i]) * w0 : 0.f;
                         if (g.whole) {
                             put(cc, v);
                         } else {
@@ -744,7 +744,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                         for (int j = 0; j < 8; ++j)
                             if (c0 + j <= g.cb) sum = fmaf(ex2f((pm[j] - ms) * sl2), pl[j], sum);
                     }
-                    const float ms = m == -INFINITY ? 0.f : m, rs = sum > 0.f ? 1.f / sum : 0.f;
+                    const float ms = m == -INFINITY ? 0.f : m, rs = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll 1
                     for (int b = blk0; b < blk1; ++b) {
                         float v[32];

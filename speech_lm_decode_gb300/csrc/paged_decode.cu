@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
                 sum += f * sm_l[w][r];
             }
             if (whole) {
-                store(r, sum > 0.f ? acc / sum : 0.f);
+                store(r, sum != 0.f ? acc / sum : 0.f);
             } else {
                 slot[r * HD + tid] = acc;
                 if (tid == 0) { slot[RG * HD + r] = m; slot[RG * HD + RG + r] = sum; }
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
                 for (int r = 0; r < rows; ++r) {
                     const float sum = sm_l[0][r];
                     const float v = so[0][r][tid] + so[1][r][tid] + so[2][r][tid] + so[3][r][tid];
-                    store(r, sum > 0.f ? v / sum : 0.f);
+                    store(r, sum != 0.f ? v / sum : 0.f);
                 }
             }
         }

@@ -56,6 +56,18 @@ def test_filters(vocab, dtype):
     check(x.cuda(), rng.random(n).astype(np.float32), t, k, p, mp)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_largest_vocabulary_and_many_rows(dtype):
+    g = torch.Generator().manual_seed(3)
+    x = (torch.randn(5, 262144, generator=g) * 2).to(dtype)
+    u = np.linspace(0.02, 0.98, 5, dtype=np.float32)
+    for k, p in ((0, 0.9), (60, 1.0), (300, 0.8)):
+        check(x.cuda(), u, 0.8, k, p, 0.001)
+    # more rows than the GPU holds at once
+    x = (torch.randn(700, 9001, generator=g) * 2).to(dtype)
+    check(x.cuda(), (np.arange(700) / 700).astype(np.float32), 1.0, np.arange(700) % 200, 0.9, 0.0)
+
+
 @pytest.mark.parametrize("vocab", [300, 5000, 70000])
 def test_ties_and_edges(vocab):
     """Few distinct values (ties at every threshold, ids of the same value kept from the lowest on), uniform
@@ -164,7 +176,7 @@ def test_refusals():
     x = torch.randn(2, 100, device="cuda")
     f = torch.ones(2, device="cuda")
     k = torch.zeros(2, dtype=torch.int32, device="cuda")
-    for bad in (x.half(), x.cpu(), x[0], x.t()):
+    for bad in (x.half(), x.cpu(), x[0], x.t(), x[:1].expand(2, 100)):
         with pytest.raises(ValueError):
             q3.sample_given(bad, f, f, k, f, f)
     with pytest.raises(ValueError):

@@ -85,6 +85,20 @@ def test_strided_rows_and_pages(types, new):
 
 
 @pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("new", [1, 3, 150])
+def test_in_place(types, new):
+    """The outputs over the queries, items cut between CTAs among them."""
+    act, kv = TYPES[types]
+    s = make([(new, 3000), (new, 400), (1, 77)], 16, 4, 16, act, kv, seed=14)
+    cache = cache_of(s)
+    want = cache.attend(s["q"], s["off"], s["ctx"], new)
+    q = s["q"].clone()
+    got = cache.attend(q, s["off"], s["ctx"], new, out=q)
+    cache.check()
+    assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("types", TYPES)
 @pytest.mark.parametrize("n", [1, 37, 3000])
 @pytest.mark.parametrize("norm", [True, False])
 def test_append_matches_64_bits(types, n, norm):
@@ -257,6 +271,29 @@ def test_growing_scores(types, new):
 
 
 @pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 90)], [(3, 700), (2, 90)], [(9, 5000)], [(150, 700), (40, 90)]])
+def test_nan_stays_where_it_belongs(lens, types):
+    """A query, and a key that a later token sees, that are NaN: NaN in their rows and heads, the rest as ever."""
+    act, kv = TYPES[types]
+    s = make(lens, 8, 4, 16, act, kv, seed=30)
+    cache = cache_of(s)
+    n0, ctx = lens[0]
+    s["q"][0, 5, 77] = float("nan")
+    last = ctx - 1                       # the last token alone sees it
+    s["k"][int(s["table"][0, last // 16]), 1, last % 16, 3] = float("nan")
+    got = cache.attend(s["q"], s["off"], s["ctx"], n0)
+    cache.check()
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[0, 5] = True
+    nan[n0 - 1, 2:4] = True
+    assert torch.equal(torch.isnan(got), nan)
+    clean = dict(s, q=torch.nan_to_num(s["q"]), k=s["k"].clone())
+    clean["k"][int(s["table"][0, last // 16]), 1, last % 16, 3] = 0.0
+    want, bound = attend64(clean)
+    close(torch.where(nan, want.to(act), got), want, bound, "the others")
+
+
+@pytest.mark.parametrize("types", TYPES)
 @pytest.mark.parametrize("new", [1, 40])
 def test_bad_pages_positions_and_lengths_are_reported(types, new):
     import speech_lm_decode_gb300 as q3
@@ -365,5 +402,14 @@ def test_refusals():
     f32 = q3.PagedKV(s["k"].float(), s["v"].float(), s["table"], 16)
     with pytest.raises(q3.Q3Error):     # bf16 activations over fp32 pages
         f32.attend(s["q"], s["off"], s["ctx"], 1)
+    # broadcast tensors: their rows, pages or heads are the same memory
+    with pytest.raises(ValueError):
+        cache.attend(s["q"][:1].expand(5, 16, HD), s["off"], s["ctx"], 1)
+    with pytest.raises(ValueError):
+        cache.attend(s["q"], s["off"], s["ctx"], 1, out=torch.empty_like(s["q"][:1]).expand(len(s["q"]) + 1, 16, HD))
+    with pytest.raises(ValueError):
+        q3.PagedKV(s["k"][:1].expand(9, 8, 16, HD), s["v"][:1].expand(9, 8, 16, HD), s["table"], 16)
+    with pytest.raises(ValueError):
+        q3.PagedKV(s["k"][:, :1].expand(-1, 8, 16, HD), s["v"][:, :1].expand(-1, 8, 16, HD), s["table"], 16)
     # nothing to do is no error
     assert cache.attend(s["q"][:0], torch.zeros(2, dtype=torch.int32, device="cuda"), s["ctx"], 1).shape == (0, 16, HD)
