@@ -68,6 +68,53 @@ def test_largest_vocabulary_and_many_rows(dtype):
     check(x.cuda(), (np.arange(700) / 700).astype(np.float32), 1.0, np.arange(700) % 200, 0.9, 0.0)
 
 
+# (rows, vocabulary) past what shared memory holds while all rows run at once: one, two and four CTAs a row
+STREAMED = [(160, 33000), (80, 50001), (40, 90000)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,vocab", STREAMED)
+def test_many_rows_of_large_vocabularies(n, vocab, dtype):
+    g = torch.Generator().manual_seed(n)
+    x = torch.randn(n, vocab, generator=g) * torch.linspace(0.1, 5, n)[:, None]
+    x[:, torch.randint(0, vocab, (vocab // 20,), generator=g)] = float("-inf")
+    rng = np.random.default_rng(vocab)
+    k = rng.choice([0, 0, 1, 50, 400, 5000, vocab, vocab + 5], n)
+    p = rng.choice([1.0, 0.95, 0.95, 0.5, 0.999, 0.0], n)
+    mp = rng.choice([0.0, 0.0, 0.05, 0.5, 1.0], n)
+    t = rng.choice([1.0, 0.7, 1.3, 0.0, 0.05, 8.0], n)
+    check(x.to(dtype).cuda(), rng.random(n).astype(np.float32), t, k, p, mp)
+
+
+@pytest.mark.parametrize("n,vocab", STREAMED)
+def test_many_rows_of_awkward_logits(n, vocab):
+    """What the tests below do to a few rows: ties, crowded borders, extreme quotients, rows that fail, and rows that
+    do not start on 16-byte boundaries."""
+    g = torch.Generator().manual_seed(n + 1)
+    wide = torch.randint(-3, 4, (n, vocab + 7), generator=g).float() * 0.5
+    x = wide[:, 3:3 + vocab]
+    t = np.ones(n, np.float32)
+    x[0::10] = torch.randn(len(x[0::10]), vocab, generator=g) * 0.01
+    x[1::10] = 1.25
+    x[2::10] = torch.linspace(-90, 0, vocab)
+    x[3::10] = torch.linspace(0, 1e-3, vocab)
+    x[4::10] = torch.randn(len(x[4::10]), vocab, generator=g) * 1e25
+    t[4::10] = 1e-5
+    x[5::10] = torch.randn(len(x[5::10]), vocab, generator=g) * 1e-30
+    t[5::10] = 1e10
+    x[6::10] = torch.where(torch.arange(vocab) % 2 == 0, 0.0, -0.0)
+    x[7, 17], x[17, vocab - 1], x[27] = float("nan"), float("inf"), float("-inf")
+    x[8::10, vocab // 2] = 9.0
+    t[9], t[19], t[29] = -1, np.inf, np.nan
+    u = np.linspace(0, 1, n, dtype=np.float32)
+    u[-1] = np.float32(1 - 2.0 ** -24)
+    rng = np.random.default_rng(n)
+    k = rng.choice([0, 0, 0, 7, 150, 900], n)
+    p = rng.choice([1.0, 0.9, 0.6, 0.3, 0.999], n)
+    mp = rng.choice([0.0, 0.0, 0.4], n)
+    check(wide.cuda()[:, 3:3 + vocab], u, t, k, p, mp)
+
+
 @pytest.mark.parametrize("vocab", [300, 5000, 70000])
 def test_ties_and_edges(vocab):
     """Few distinct values (ties at every threshold, ids of the same value kept from the lowest on), uniform
