@@ -225,6 +225,74 @@ def test_graph_replay_with_new_lengths():
 
 
 @pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("most", [1, 3, 40])
+def test_many_sequences(types, most):
+    """More sequences than a CTA has threads, some without new tokens or without any."""
+    act, kv = TYPES[types]
+    g = torch.Generator().manual_seed(most)
+    lens = []
+    for _ in range(1500):
+        new = int(torch.randint(0, most + 1, (1,), generator=g))
+        lens.append((new, int(torch.randint(0, 60, (1,), generator=g))))
+    s = make(lens, 2, 1, 16, act, kv, seed=21)
+    cache = cache_of(s)
+    got = cache.attend(s["q"], s["off"], s["ctx"], most)
+    cache.check()
+    want, bound = attend64(s)
+    close(got, want, bound)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("new", [1, 50])
+def test_sequences_that_share_pages(types, new):
+    act, kv = TYPES[types]
+    s = make([(new, 300), (new, 333), (new, 290)], 8, 2, 16, act, kv, seed=22)
+    s["table"][1, :12] = s["table"][0, :12]
+    s["table"][2, :15] = s["table"][0, :15]
+    cache = cache_of(s)
+    got = cache.attend(s["q"], s["off"], s["ctx"], new)
+    cache.check()
+    want, bound = attend64(s)
+    close(got, want, bound)
+
+
+@pytest.mark.parametrize("types", TYPES)
+def test_two_streams_at_once(types):
+    """Calls of one cache object on two streams, single tokens on one and chunks on the other, beside draws of both
+    kinds: the bits of the same calls alone."""
+    import speech_lm_decode_gb300 as q3
+    act, kv = TYPES[types]
+    s = make([(150, 700), (1, 1200), (40, 333)], 16, 8, 16, act, kv, seed=23)
+    cache = cache_of(s)
+    tokens = torch.randn(3, 16, HD, device="cuda").to(act)
+    off1 = torch.arange(4, dtype=torch.int32, device="cuda")
+    x = torch.randn(160, 30000, device="cuda")
+    f = torch.full((160,), 0.9, device="cuda")
+    zero = torch.zeros(160, device="cuda")
+    k = torch.zeros(160, dtype=torch.int32, device="cuda")
+
+    def chunks():
+        return [cache.attend(s["q"], s["off"], s["ctx"], 150), *q3.sample_given(x, f, f, k, f, zero)]
+
+    def singles():
+        return [cache.attend(tokens, off1, s["ctx"], 1), *q3.sample_given(x[:3], f[:3], f[:3], k[:3] + 20, f[:3], zero[:3])]
+    want_a, want_b = chunks(), singles()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        with torch.cuda.stream(a):
+            got.append((chunks(), want_a))
+        with torch.cuda.stream(b):
+            got.append((singles(), want_b))
+            got.append((singles(), want_b))
+    torch.cuda.synchronize()
+    cache.check()
+    for have, want in got:
+        assert all(torch.equal(h, w) for h, w in zip(have, want))
+
+
+@pytest.mark.parametrize("types", TYPES)
 def test_many_row_graph_replay(types):
     """Chunks captured once and replayed with other splits of the rows between the sequences."""
     act, kv = TYPES[types]
