@@ -6,7 +6,8 @@
 // keys in shared memory: V(t) is on its way (cp.async) while the scores of t
 // are formed, K(t+1) while its outputs are.  A thread forms ROWS/16 x 4 scores
 // and ROWS/16 x 8 outputs, so that a 16-byte shared load serves 8 (ROWS = 64)
-// multiply-adds; K rows are padded by 16 bytes against bank conflicts.  ROWS =
+// multiply-adds; two CTAs fit an SM, as the places in shared memory are mixed
+// against bank conflicts instead of padded.  ROWS =
 // 16 serves a few tokens of many heads.  Bound by the multiply-adds and the
 // shared loads beside them: a prompt of 2048 tokens (16 q, 8 kv heads) 607 us,
 // 28 TFLOP/s.
@@ -23,10 +24,9 @@ namespace {
 constexpr int FT = 256;            // threads
 constexpr int FK = 64;             // keys of a tile and of a unit
 constexpr int F_OVER = 0;          // units that an item costs besides its keys (1 and 2 were slower)
-constexpr int FKS = HD + 4;        // row of K in shared memory, floats
-constexpr int FPS = FK + 4;        // row of the weights
 constexpr int F_CTAS = 2;          // resident CTAs of an SM
-constexpr int f_smem(int rows) { return (rows * HD + FK * FKS + FK * HD + rows * FPS) * 4; }
+constexpr int f_smem(int rows) { return (rows * HD + 2 * FK * HD + rows * FK) * 4; }
+static_assert(F_CTAS * (f_smem(64) + 2048) <= 228 * 1024, "both fit an SM's shared memory");
 constexpr size_t f_slot(int rows) { return (size_t)rows * (HD + 4); }   // outputs, maxima, sums
 
 __device__ __forceinline__ void cp16(float* dst, const float* src, bool ok) {
@@ -48,9 +48,9 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
     constexpr int RT = ROWS / 16;      // rows of a thread
     extern __shared__ __align__(16) float fs[];
     float* Qs = fs;                    // [ROWS][128]
-    float* Ks = Qs + ROWS * HD;        // [64][132]
-    float* Vs = Ks + FK * FKS;         // [64][128]
-    float* Ps = Vs + FK * HD;          // [ROWS][68]
+    float* Ks = Qs + ROWS * HD;        // [64][128], 16-byte pieces of a row in the order piece ^ (row & 7)
+    float* Vs = Ks + FK * HD;          // [64][128]
+    float* Ps = Vs + FK * HD;          // [ROWS][64], the halves of 16 swapped for every other thread row
     __shared__ int s_last;
     const PagedView& c = a.c;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
         const int nt = key1 > key0 ? (key1 - key0 + FK - 1) / FK : 0;
         const int32_t* table = c.table + (int64_t)s * c.max_pages;
         const int pmask = (1 << c.page_shift) - 1;
-        auto load = [&](float* dst, int stride, const void* pool, int t) {
+        auto load = [&](float* dst, int mix, const void* pool, int t) {
 #pragma unroll
             for (int i = 0; i < FK * 32 / FT; ++i) {
                 const int row = (tid + i * FT) >> 5, ch = tid & 31, key = key0 + t * FK + row;
@@ -89,12 +89,12 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
                         if (a.err) atomicOr(a.err, ERRB_BOUNDS);
                     }
                 }
-                cp16(dst + row * stride + ch * 4, src, ok);
+                cp16(dst + row * HD + (ch ^ (row & mix)) * 4, src, ok);
             }
             cp_commit();
         };
         __syncthreads();   // the segment before is done with the buffers
-        if (nt > 0) load(Ks, FKS, c.k, 0);
+        if (nt > 0) load(Ks, 7, c.k, 0);
         for (int i = tid; i < ROWS * 32; i += FT) {
             const int r = i >> 5, tok = tok0 + r / c.G;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
             for (int d = 0; d < 8; ++d) o[i][d] = 0.f;
         }
         for (int t = 0; t < nt; ++t) {
-            load(Vs, HD, c.v, t);
+            load(Vs, 0, c.v, t);
             cp_wait<1>();
             __syncthreads();
             float x[RT][4];
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
 #pragma unroll
                 for (int i = 0; i < RT; ++i) qv[i] = *(const float4*)(Qs + (ty * RT + i) * HD + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) kv[j] = *(const float4*)(Ks + (tx + 16 * j) * FKS + d);
+                for (int j = 0; j < 4; ++j) kv[j] = *(const float4*)(Ks + (tx + 16 * j) * HD + (d ^ (tx & 7) * 4));
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -161,12 +161,12 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
                 for (int j = 0; j < 4; ++j) {
                     const float p = fex2(fmaf(x[i][j], sl2, -ref));
                     l[i] += p;
-                    Ps[(ty * RT + i) * FPS + tx + 16 * j] = p;
+                    Ps[(ty * RT + i) * FK + ((tx + 16 * j) ^ (ty & 1) * 16)] = p;
                 }
             }
             __syncthreads();   // weights are there, K is free
             if (t + 1 < nt) {
-                load(Ks, FKS, c.k, t + 1);
+                load(Ks, 7, c.k, t + 1);
                 cp_wait<1>();
             } else {
                 cp_wait<0>();
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
             for (int k = 0; k < FK; k += 4) {
                 float4 p[RT];
 #pragma unroll
-                for (int i = 0; i < RT; ++i) p[i] = *(const float4*)(Ps + (ty * RT + i) * FPS + k);
+                for (int i = 0; i < RT; ++i) p[i] = *(const float4*)(Ps + (ty * RT + i) * FK + (k ^ (ty & 1) * 16));
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const float4 v0 = *(const float4*)(Vs + (k + kk) * HD + tx * 4);
