@@ -9,8 +9,8 @@
 // multiply-adds; two CTAs fit an SM, as the places in shared memory are mixed
 // against bank conflicts instead of padded.  ROWS =
 // 16 serves a few tokens of many heads.  Bound by the multiply-adds and the
-// shared loads beside them: a prompt of 2048 tokens (16 q, 8 kv heads) 607 us,
-// 28 TFLOP/s.
+// shared loads beside them: a prompt of 2048 tokens (16 q, 8 kv heads) 515 us,
+// 33 TFLOP/s (padded, with one CTA an SM, 604; packed products: the same).
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.h"
