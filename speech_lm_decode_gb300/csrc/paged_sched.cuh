@@ -29,10 +29,10 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedAttn& a, int s, bool re
     PagedSeq q;
     q.row0 = a.q_off[s];
     const int end = a.q_off[s + 1], cap = a.c.max_pages << a.c.page_shift;
-    q.n_new = end - q.row0;
     q.ctx = a.ctx[s];
-    bool bad = false;
-    if (q.row0 < 0 || q.n_new < 0 || end > a.n_tokens || q.n_new > a.max_q) { bad = true; q.n_new = 0; }
+    // (the order matters: the difference is formed of offsets in range only, as that of any two may wrap around)
+    bool bad = q.row0 < 0 || end < q.row0 || end > a.n_tokens || end - q.row0 > a.max_q;
+    q.n_new = bad ? 0 : end - q.row0;
     if (q.n_new > 0 && (q.ctx < 0 || q.ctx > cap)) { bad = true; q.ctx = min(max(q.ctx, 0), cap); }
     if (bad && report && a.err) atomicOr(a.err, ERRB_BOUNDS);
     return q;
