@@ -70,6 +70,7 @@ struct ChunkSmem {
     uint64_t full[5], empty[5], s_full[2], p_full[2], r_full[2], pv_full, q_full, o_full, drain;
     uint32_t tmem;
     int dead, last;
+    int lost;                // the cut's keys have a page out of range among them
     float ref[CT];           // one tile of rows: the maxima that both slots' weights refer to
     PagedRange range;        // the softmax warps' walk, kept here to save them the registers
     Walk walk;
@@ -144,7 +145,9 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// of the softmax warps, or of those and warp 2
 __device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void seg_sync(int id) { asm volatile("bar.sync %0, 288;" ::"r"(id) : "memory"); }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
@@ -308,16 +311,24 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             if (!ok) return;
             issued = cnt;
             const int rows = min(CT, w.q.ctx - kt * CT), nbox = (rows + box - 1) / box;
+            // a box a lane (a page has 16 positions at least); a page out of range is not followed: its box lies past the
+            // last page, where copies read zeros
+            const int key = kt * CT + min(lane, nbox - 1) * box;
+            int page = 0;
+            bool bad = false;
+            if (lane < nbox) {
+                page = c.table[(int64_t)g.s * c.max_pages + (key >> c.page_shift)];
+                bad = (unsigned)page >= (unsigned)c.n_pages;
+            }
+            if (bad) {
+                if (a.err) atomicOr(a.err, ERRB_BOUNDS);
+                page = c.n_pages;
+            }
+            __syncwarp();
             if (lane == 0) bar_expect(&sm.full[st], (unsigned)(nbox * box * HD * 2));
             __syncwarp();
-            for (int i = lane; i < nbox; i += 32) {
-                const int key = kt * CT + i * box;
-                int page = c.table[(int64_t)g.s * c.max_pages + (key >> c.page_shift)];
-                if ((unsigned)page >= (unsigned)c.n_pages) {
-                    if (a.err) atomicOr(a.err, ERRB_BOUNDS);
-                    page = 0;
-                }
-                const uint32_t dst = su32(ring + (size_t)st * STAGE) + i * box * 128;
+            if (lane < nbox) {
+                const uint32_t dst = su32(ring + (size_t)st * STAGE) + lane * box * 128;
                 tma_4d(dst, map, 0, key & pmask, g.h, page, &sm.full[st]);
                 tma_4d(dst + STAGE / 2, map, 64, key & pmask, g.h, page, &sm.full[st]);
             }
@@ -441,6 +452,24 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             commit(&sm.drain);
             bar_wait(&sm.drain, 0, sm, a.err, false);
         }
+    } else if (warp == 2) {
+        // ---------------------------------------------------------- pages out of range among a cut's, beside the query rows
+        for (;;) {
+            seg_sync(1);
+            seg_sync(1);
+            if (!sm.more) break;
+            const Seg& g = sm.seg;
+            const int32_t* row = c.table + (int64_t)g.s * c.max_pages;
+            const int p0 = g.kt0 * CT >> c.page_shift;
+            const int p1 = g.n > 0 ? (min((g.kt0 + g.n) * CT, sm.walk.q.ctx) - 1 >> c.page_shift) + 1 : p0;
+            bool bad = false;
+#pragma unroll 8
+            for (int i = p0 + lane; i < p1; i += 32) bad |= (unsigned)row[i] >= (unsigned)c.n_pages;
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) sm.lost = bad;
+            seg_sync(4);
+            seg_sync(1);
+        }
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -456,9 +485,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         bool ok = true;
         for (;;) {
             // both slots are done with Q and with the tensor memory of the item before
-            wg_sync(1);
+            seg_sync(1);
             if (threadIdx.x == 128) sm.more = walk_seg(sm.walk, sm.range, tpt, tpi, sm.seg);
-            wg_sync(1);
+            seg_sync(1);
             if (!sm.more) break;
             const Seg& g = sm.seg;
             const PagedSeq& wq = sm.walk.q;
@@ -466,7 +495,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const uint32_t tO = tmem + lanes + OUT + tile * CT;
             const int rg = (int)(r * ginv >> 16), tok = g.tok0 + tile * tpt + rg, head = g.h * c.G + r - rg * c.G;
             const bool live = r < tpt * c.G && tok < g.tok0 + g.ntok;
-            const int lim = live ? min(wq.ctx - wq.n_new + tok + 1, wq.ctx) : 0;
+            auto lim = [&] { return live ? min(wq.ctx - wq.n_new + tok + 1, wq.ctx) : 0; };   // keys that the row sees
             float mx = -INFINITY, l = 0.f;
             if (g.n > 0) {
                 // ---- query rows: 16 threads a row, 8 values each, loads of a batch in flight together
@@ -514,6 +543,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 fence_async_smem();
                 bar_arrive(&sm.q_full);
             }
+            seg_sync(4);
+            const int plain = sm.lost ? 0 : lim();     // tiles up to here are taken as they are
             const int n = g.two ? g.n : (g.n + 1 - t) / 2;
             for (int j = 0; j < n; ++j) {
                 const int k0 = (g.kt0 + (g.two ? j : 2 * j + t)) * CT;
@@ -521,13 +552,29 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 ++sc;
                 ok = __all_sync(0xffffffffu, ok);
                 fence_after();
-                const int seen = lim - k0;                         // columns that the row sees
                 uint32_t x[4][32];
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, x[cc]);
 #pragma unroll
                 for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(x[cc]);
-                if (__any_sync(0xffffffffu, seen < CT)) {
+                if (__any_sync(0xffffffffu, plain - k0 < CT)) {
+                    if (sm.lost) {   // keys of pages out of range do not count: their scores become -inf, all are read again
+                        const int key = k0 + 16 * (lane & 7);
+                        const unsigned gone = __ballot_sync(0xffffffffu, key < wq.ctx &&    // bit i: keys 16 i .. 16 i + 15
+                            (unsigned)c.table[(int64_t)g.s * c.max_pages + (key >> c.page_shift)] >= (unsigned)c.n_pages);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[0][i] = 0xff800000u;
+                        uint32_t (&none)[16] = *reinterpret_cast<uint32_t (*)[16]>(&x[0][0]);
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i)
+                            if (gone >> i & 1) tmem_st16(tS + 16 * i, none);
+                        tmem_wait_st();
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, x[cc]);
+#pragma unroll
+                        for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(x[cc]);
+                    }
+                    const int seen = lim() - k0;                   // columns that the row sees
 #pragma unroll
                     for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
@@ -787,7 +834,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     flush(blk0, blk1);
                 }
             }
-            wg_sync(1);
+            seg_sync(1);
             if (threadIdx.x == 128 && sm.walk.more) walk_step<CT, C_OVER>(sm.walk, a, sm.range, tpi);
         }
     }

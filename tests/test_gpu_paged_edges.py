@@ -29,3 +29,77 @@ def test_offsets_whose_difference_wraps_around(new, types):
         assert e.value.code == q3.Q3_ERR_BOUNDS
         close(out[:new], want, bound, str(off))
         assert (out[new:] == 7.0).all(), off
+
+
+def attend_seen(s, gone, scale=HD ** -0.5):
+    """attend64 with keys that do not count: gone[i] has the page indices of sequence i that are out of range."""
+    out, bound = [], []
+    for i, (n_new, ctx) in enumerate(s["lens"]):
+        there = torch.tensor([j for j in range(ctx) if j // s["page"] not in gone[i]], dtype=torch.long, device="cuda")
+        pages = s["table"][i, :-(-ctx // s["page"])].long()
+        pages = torch.where(pages.clamp(0, s["k"].shape[0] - 1) == pages, pages, 0)
+        k, v = (p[pages].transpose(1, 2).reshape(-1, s["nkv"], HD)[there].double() for p in (s["k"], s["v"]))
+        q = s["q"][int(s["off"][i]):int(s["off"][i]) + n_new].double()
+        last = ctx - n_new + torch.arange(n_new, device="cuda")
+        hidden = there[None] > last[:, None]
+        some = ~hidden.all(1)
+        o = torch.zeros(n_new, s["nq"], HD, dtype=torch.float64, device="cuda")
+        b = torch.zeros_like(o)
+        for h in range(s["nq"] if len(there) else 0):
+            kh, vh = k[:, h * s["nkv"] // s["nq"]], v[:, h * s["nkv"] // s["nq"]]
+            p = torch.softmax((q[:, h] @ kh.T * scale).masked_fill(hidden, float("-inf")), -1)
+            p[~some] = 0
+            o[:, h] = p @ vh
+            # as in attend64: the operands' and the sums' errors of a score, twice; parts, exp and sums of the weights
+            e_s = scale * (q[:, h].abs() @ kh.abs().T).masked_fill(hidden, 0).amax(-1) * 2.0 ** -16
+            e_p = 2.0 ** -17 + 2.0 ** -20 + (ctx + 128) * 2.0 ** -24 + (2.0 ** -8 if s["q"].dtype != torch.float32 else 0)
+            b[:, h] = (p @ vh.abs()) * (2 * e_s + e_p)[:, None]
+        out.append(o)
+        bound.append(b + o.abs() * (2.0 ** -24 if s["q"].dtype == torch.float32 else 2.0 ** -8))
+    return torch.cat(out), torch.cat(bound)
+
+
+# (new tokens, positions) of each sequence and the pages of each that are out of range
+GONE = {
+    "single": ([(1, 300), (1, 90)], [{2, 18}, {0}]),
+    "few": ([(3, 700), (2, 40)], [{0, 1, 2, 43}, {1}]),
+    "chunk": ([(40, 700), (17, 333)], [{2, 3, 11, 43}, set(range(8, 16))]),
+    "two-tiles": ([(150, 700), (200, 1100)], [{0, 20}, {5, 6, 7, 40, 68}]),
+    "all-of-one": ([(9, 150), (30, 400)], [set(range(10)), {24}]),
+    "long": ([(20, 9000), (1, 64)], [{0, 7, 100, 562}, {3}]),
+}
+
+
+def check_gone(case, types, page):
+    """Whichever kernel serves the call: such a page's keys are masked, rows that see nothing else are zeros, and no
+    other page is read in its place (page 0 belongs to nobody and holds NaN)."""
+    import speech_lm_decode_gb300 as q3
+    act, kv = TYPES[types]
+    lens, gone = GONE[case]
+    if page == 128:
+        gone = [{j * 16 // page for j in g} for g in gone]
+    s = make(lens, 8, 4, page, act, kv, seed=41)
+    # what page 0 holds moves to a page that no sequence has
+    to = next(i for i in range(s["k"].shape[0]) if not (s["table"] == i).any())
+    if to != 0:
+        s["k"][to], s["v"][to] = s["k"][0].clone(), s["v"][0].clone()
+        s["table"][s["table"] == 0] = to
+        s["k"][0], s["v"][0] = float("nan"), float("nan")
+    bad = [-1, s["k"].shape[0], 2 ** 31 - 1, -2 ** 31]
+    for i, g in enumerate(gone):
+        for n, j in enumerate(sorted(g)):
+            s["table"][i, j] = bad[n % 4]
+    cache = cache_of(s)
+    got = cache.attend(s["q"], s["off"], s["ctx"], max(q for q, _ in lens))
+    with pytest.raises(q3.Q3Error) as e:
+        cache.check()
+    assert e.value.code == q3.Q3_ERR_BOUNDS
+    want, bound = attend_seen(s, gone)
+    close(got, want, bound, case)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("types", ["bf16", "f32"])
+@pytest.mark.parametrize("case", GONE)
+def test_keys_of_pages_out_of_range_do_not_count(case, types, page):
+    check_gone(case, types, page)
