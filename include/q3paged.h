@@ -19,7 +19,8 @@
  *    they can be captured into a CUDA graph and replayed with new lengths,
  *    positions, tables and values in the same arrays.
  *  - What the host cannot see (page ids, positions, lengths) is checked on the
- *    device: an entry out of range is never followed; it sets bit
+ *    device: an entry out of range is never followed (attention: the keys of
+ *    such a page do not count, as if they were masked); it sets bit
  *    Q3PAGED_ERR_BOUNDS of *err, and a device wait that gave up sets
  *    Q3PAGED_ERR_TIMEOUT.  Bits are only ever set; the caller clears them.
  *  - All pointers are device memory, borrowed for the duration of the work.

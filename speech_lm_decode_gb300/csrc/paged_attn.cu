@@ -51,9 +51,10 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
     float* Ks = Qs + ROWS * HD;        // [64][128], 16-byte pieces of a row in the order piece ^ (row & 7)
     float* Vs = Ks + FK * HD;          // [64][128]
     float* Ps = Vs + FK * HD;          // [ROWS][64], the halves of 16 swapped for every other thread row
-    __shared__ int s_last;
+    __shared__ int s_last, s_lost;     // s_lost: a page out of range has been met
     const PagedView& c = a.c;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    if (tid == 0) s_lost = 0;
 
     const int tpi = ROWS / c.G;        // tokens of an item
     const PagedRange R = paged_range<FT>(a, grid_max, F_OVER + 1, F_OVER, [&](const PagedSeq& q) { return c.nkv * seq_units<FK, F_OVER>(q, tpi); });
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
                         src += page * c.page_stride + (int64_t)h * c.head_stride + (int64_t)(key & pmask) * c.token_stride + ch * 4;
                     else {
                         ok = false;
+                        *(volatile int*)&s_lost = 1;
                         if (a.err) atomicOr(a.err, ERRB_BOUNDS);
                     }
                 }
@@ -141,12 +143,18 @@ __global__ void __launch_bounds__(FT, F_CTAS) paged_f32_kernel(const PagedAttn a
                     }
             }
             const int kb = key0 + t * FK + tx;
+            int gone = 0;      // of the four keys: those of pages out of range, which do not count
+            if (*(volatile int*)&s_lost)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (kb + 16 * j < key1 && (unsigned)__ldg(table + ((kb + 16 * j) >> c.page_shift)) >= (unsigned)c.n_pages)
+                        gone |= 1 << j;
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
                 float top = m[i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (kb + 16 * j >= lim[i]) x[i][j] = -INFINITY;
+                    if (kb + 16 * j >= lim[i] || (gone >> j & 1)) x[i][j] = -INFINITY;
                     top = fmaxf(top, x[i][j]);
                 }
 #pragma unroll

@@ -103,3 +103,9 @@ def check_gone(case, types, page):
 @pytest.mark.parametrize("case", GONE)
 def test_keys_of_pages_out_of_range_do_not_count(case, types, page):
     check_gone(case, types, page)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("case", GONE)
+def test_keys_of_fp32_pages_out_of_range_do_not_count(case, page):
+    check_gone(case, "f32kv", page)
