@@ -478,7 +478,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         const int r = (threadIdx.x & 127);                 // this thread's row of a tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + t * SLOT;
-        const float sl2 = a.scale * 1.4426950408889634f, slack = 8.f / sl2;
+        const float sl2 = a.scale * 1.4426950408889634f, slack = fminf(8.f / sl2, 3e38f);   // (finite: -inf stays -inf)
         int* counters = (int*)a.ws;
         float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
         int sc = 0, oc = 0, rc = 0, pvc = 0;   // steps of this slot, items; of the other slot and products (one tile)

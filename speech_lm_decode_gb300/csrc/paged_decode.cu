@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(DW * 32, d_ctas(NT)) paged_decode_kernel(const
     const PagedRange R = paged_range<DW * 32>(a, grid_max, D_MIN_UNITS, D_OVER, units_of);
     if (R.u0 >= R.u1) return;
     const float sl2 = a.scale * 1.4426950408889634f;   // scores in powers of two
-    const float slack = 8.f / sl2;
+    const float slack = fminf(8.f / sl2, 3e38f);       // finite: added to -inf, it has to stay -inf
     int* counters = (int*)a.ws;
     constexpr size_t SLOT = (size_t)RG * (HD + 4);   // outputs, maxima, sums (16-byte rows)
     float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);

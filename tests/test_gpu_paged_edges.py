@@ -109,3 +109,17 @@ def test_keys_of_pages_out_of_range_do_not_count(case, types, page):
 @pytest.mark.parametrize("case", GONE)
 def test_keys_of_fp32_pages_out_of_range_do_not_count(case, page):
     check_gone(case, "f32kv", page)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("new", [1, 3, 40, 150])
+@pytest.mark.parametrize("scale", [1e-38, 1.4e-45, 1e-30])
+def test_scales_next_to_zero(scale, new, types):
+    """Every score is the same then: the outputs are means of the values."""
+    act, kv = TYPES[types]
+    s = make([(new, 700), (new, 40), (1, 300)], 8, 4, 16, act, kv, seed=42)
+    cache = cache_of(s)
+    got = cache.attend(s["q"], s["off"], s["ctx"], new, scale=scale)
+    cache.check()
+    want, bound = attend64(s, scale=scale)
+    close(got, want, bound, str(scale))
