@@ -87,10 +87,11 @@ int q3paged_append(const q3paged_cache* c, int n_tokens, const void* qkv, int64_
                    const int32_t* tok_pos, const float* q_norm, const float* k_norm, float eps, const float* rope_cs,
                    int rope_rows, void* q_out, int64_t q_stride, int32_t* err, void* stream);
 
-/* Bytes of workspace that q3paged_attention wants for this cache's heads
- * (0: invalid cache).  The caller clears its first Q3PAGED_COUNTER_BYTES bytes
- * once; every call leaves it ready for the next.  Calls that may run at the same time (other streams,
- * graphs replayed side by side) need one workspace each. */
+/* Bytes of workspace that q3paged_attention wants: the same for every valid
+ * cache (0: invalid cache).  The caller clears its first Q3PAGED_COUNTER_BYTES
+ * bytes once; every call leaves it ready for the next, which may be for another
+ * cache.  Calls that may run at the same time (other streams, graphs replayed
+ * side by side) need one workspace each. */
 size_t q3paged_workspace_bytes(const q3paged_cache* c);
 
 /* Causal attention of new tokens over the cache, which holds them already:

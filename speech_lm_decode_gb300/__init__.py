@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import weakref
 
 import numpy as np
 
@@ -567,6 +568,10 @@ def _on_stream(device, call):
         _paged_raise(rc)
 
 
+# attention workspaces by (device, stream): calls of one stream follow each other, whichever cache they are for
+_paged_workspaces = weakref.WeakValueDictionary()
+
+
 class PagedKV:
     """A paged key / value cache over tensors that the caller owns (q3paged.h).
 
@@ -574,7 +579,9 @@ class PagedKV:
     strides (a permuted view of [n_pages, page_size, n_kv_heads, 128] serves as well); page_table: int32
     [n_seqs, max_pages].  The tensors may be written between calls (the table as sequences grow); their
     addresses are taken once, here.  Work is queued on the current stream; calls on different streams have
-    a workspace each, and a call that is being captured gets one of its graph's own."""
+    a workspace each (51 MB, which the cache objects used on a stream share and the last of them gives back), and a
+    call that is being captured gets one of its graph's own.  Keep the object as long as graphs that were captured
+    with it are replayed."""
 
     def __init__(self, k_pages, v_pages, page_table, n_q_heads: int):
         import torch
@@ -627,7 +634,11 @@ class PagedKV:
             return ws
         ws = self._ws.get(stream)
         if ws is None:
-            ws = self._ws[stream] = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            ws = _paged_workspaces.get((self._dev, stream))
+            if ws is None:
+                ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=self.device)
+                _paged_workspaces[self._dev, stream] = ws
+            self._ws[stream] = ws
         return ws
 
     def _rows(self, t, name, heads, dtype=None):

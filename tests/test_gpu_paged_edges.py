@@ -123,3 +123,35 @@ def test_scales_next_to_zero(scale, new, types):
     cache.check()
     want, bound = attend64(s, scale=scale)
     close(got, want, bound, str(scale))
+
+
+def test_cache_objects_share_the_workspace_of_a_stream():
+    """28 layers' caches on a stream hold one workspace, another stream's calls another; calls of unlike caches in
+    turn give the bits of each alone; what the last object held is given back."""
+    import gc
+    import speech_lm_decode_gb300 as q3
+    states = [make([(new, 900), (new, 70)], 8, nkv, 16, *TYPES[t], seed=43) for t in TYPES for new, nkv in ((1, 8), (40, 2))]
+    news = [1, 40] * 3
+    alone = []
+    for s, new in zip(states, news):
+        alone.append(cache_of(s).attend(s["q"], s["off"], s["ctx"], new))
+    gc.collect()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    caches = [cache_of(s) for s in states * 5]
+    got = [c.attend(s["q"], s["off"], s["ctx"], new) for _ in range(2) for c, s, new in zip(caches, states * 5, news * 5)]
+    one = caches[0].ws_bytes
+    assert torch.cuda.memory_allocated() - before < 1.5 * one
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got += [c.attend(s["q"], s["off"], s["ctx"], new) for c, s, new in zip(caches, states, news)]
+    assert one < torch.cuda.memory_allocated() - before < 2.5 * one
+    torch.cuda.synchronize()
+    for c in caches:
+        c.check()
+    for i, o in enumerate(got):
+        assert torch.equal(o, alone[i % len(alone)])
+    del c, caches, got, o
+    gc.collect()
+    assert torch.cuda.memory_allocated() - before < one / 2
