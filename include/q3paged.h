@@ -65,6 +65,10 @@ typedef struct {
     void* v_pages;
     const int32_t* page_table;   /* [n_seqs][max_pages]; entries past a sequence's
                                     last page are not read                            */
+    int inject_timeout;     /* test only (0 = off).  Attention of chunks over bf16 pages:
+                               the wait of each CTA for a place for its n-th tile of
+                               keys or values counts as run out: the call ends early
+                               with Q3PAGED_ERR_TIMEOUT, its outputs are not determined */
 } q3paged_cache;
 
 /* Appends n_tokens tokens, in any order:

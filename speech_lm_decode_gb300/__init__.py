@@ -518,7 +518,7 @@ class PagedCache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("n_q_heads", "n_kv_heads", "head_dim", "act_dtype", "kv_dtype",
                                             "page_size", "n_pages", "n_seqs", "max_pages")] + \
               [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride")] + \
-              [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "page_table")]
+              [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "page_table")] + [("inject_timeout", ctypes.c_int)]
 
 
 def _paged_raise(rc):
@@ -581,9 +581,9 @@ class PagedKV:
     addresses are taken once, here.  Work is queued on the current stream; calls on different streams have
     a workspace each (51 MB, which the cache objects used on a stream share and the last of them gives back), and a
     call that is being captured gets one of its graph's own.  Keep the object as long as graphs that were captured
-    with it are replayed."""
+    with it are replayed.  inject_timeout is for tests (q3paged_cache)."""
 
-    def __init__(self, k_pages, v_pages, page_table, n_q_heads: int):
+    def __init__(self, k_pages, v_pages, page_table, n_q_heads: int, inject_timeout: int = 0):
         import torch
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
             if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.shape[3] == 128 and
@@ -604,7 +604,7 @@ class PagedKV:
         if any(size > 1 and st < 128 for size, st in zip(k_pages.shape[:3], steps)):
             raise ValueError("k_pages and v_pages: pages, heads and positions must not share memory")
         c.page_stride, c.head_stride, c.token_stride = steps
-        c.n_q_heads = n_q_heads
+        c.n_q_heads, c.inject_timeout = n_q_heads, inject_timeout
         c.kv_dtype = _dtype_code(k_pages)
         c.n_seqs, c.max_pages = page_table.shape
         c.k_pages, c.v_pages = k_pages.data_ptr(), v_pages.data_ptr()

@@ -182,6 +182,7 @@ int view_of(const q3paged_cache* c, PagedView* v, bool pools) {
         return paged_fail(Q3_ERR_ARG, "page_size must be a power of two in 16..1024");
     if (c->n_pages < 1 || c->n_seqs < 1 || c->max_pages < 1 || (int64_t)c->max_pages * c->page_size > 0x7fffff00)
         return paged_fail(Q3_ERR_ARG, "n_pages, n_seqs and max_pages must be >= 1 (positions below 2^31)");
+    if (c->inject_timeout < 0) return paged_fail(Q3_ERR_ARG, "inject_timeout must be >= 0");
     v->nq = c->n_q_heads;
     v->nkv = c->n_kv_heads;
     v->G = v->nq / v->nkv;
@@ -271,6 +272,7 @@ int q3paged_attention(const q3paged_cache* cache, int n_tokens, int max_q, const
                           paged_workspace_bytes());
     a.act = cache->act_dtype;
     a.kv = cache->kv_dtype;
+    a.inject = cache->inject_timeout;
     a.n_tokens = n_tokens;
     a.max_q = max_q < n_tokens ? max_q : n_tokens;
     a.q = q;

@@ -22,6 +22,7 @@ struct PagedView {
 struct PagedAttn {
     PagedView c;
     int act, kv, n_tokens, max_q;
+    int inject;                  // test only: the tile whose wait counts as run out (q3paged_cache)
     const void* q;
     int64_t q_stride;
     const int32_t *q_off, *ctx;

@@ -31,7 +31,7 @@
 //
 // Every wait is bounded: one that runs out sets the timeout bit, after which
 // the CTA goes through its remaining steps without waiting or issuing, drains
-// its copies, frees its tensor memory and returns.
+// its copies and products, frees its tensor memory and returns.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -96,6 +96,10 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, unsigned parity) {
         : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ void give_up(ChunkSmem& s, int* err) {
+    *(volatile int*)&s.dead = 1;
+    if (err) atomicOr(err, ERRB_TIMEOUT);
+}
 // bounded wait; false once the CTA has given up (heed: not even looked at then)
 __device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, ChunkSmem& s, int* err, bool heed = true) {
     if (bar_try(b, parity)) return true;
@@ -103,8 +107,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, ChunkSmem
     while (!bar_try(b, parity)) {
         if (heed && *(volatile int*)&s.dead) return false;
         if (clock64() - t0 > C_WAIT_LIMIT) {
-            *(volatile int*)&s.dead = 1;
-            if (err) atomicOr(err, ERRB_TIMEOUT);
+            give_up(s, err);
             return false;
         }
     }
@@ -306,6 +309,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         auto load = [&](const CUtensorMap* map, int kt) {
             const int st = cnt % ST;
             if (cnt >= ST) ok = ok && bar_wait(&sm.empty[st], (cnt / ST - 1) & 1, sm, a.err);
+            if (cnt + 1 == a.inject) {
+                give_up(sm, a.err);
+                ok = false;
+            }
             ok = __all_sync(0xffffffffu, ok);
             ++cnt;
             if (!ok) return;
@@ -448,7 +455,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             }
             if (w.more) walk_step<CT, C_OVER>(w, a, R, tpi);
         }
-        if (!ok && elect_one()) {   // products in flight end before the tensor memory goes
+        // products in flight end before the tensor memory goes (they have, unless the softmax warps gave up on them)
+        if (elect_one()) {
             commit(&sm.drain);
             bar_wait(&sm.drain, 0, sm, a.err, false);
         }

@@ -155,3 +155,30 @@ def test_cache_objects_share_the_workspace_of_a_stream():
     del c, caches, got, o
     gc.collect()
     assert torch.cuda.memory_allocated() - before < one / 2
+
+
+@pytest.mark.parametrize("types", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[(150, 3000), (40, 333)], [(40, 900), (17, 64), (1, 500)]])
+def test_a_wait_that_runs_out(lens, types):
+    """Every CTA's wait for room for its n-th tile counts as run out, at the start of an item or inside: the call returns,
+    says so, and leaves counters with which the next call on the workspace gives the bits that it should."""
+    import speech_lm_decode_gb300 as q3
+    act, kv = TYPES[types]
+    s = make(lens, 8, 4, 16, act, kv, seed=44)
+    most = max(q for q, _ in lens)
+    cache = cache_of(s)
+    want = cache.attend(s["q"], s["off"], s["ctx"], most)
+    cache.check()
+    (ws,) = cache._ws.values()
+    for n in list(range(1, 14)) + [20, 33]:
+        broken = q3.PagedKV(s["k"], s["v"], s["table"], n_q_heads=8, inject_timeout=n)
+        broken.attend(s["q"], s["off"], s["ctx"], most)
+        torch.cuda.synchronize()
+        e = int(broken.err.item())
+        assert e in (0, q3.Q3PAGED_ERR_TIMEOUT) and (e or n > 2)     # (a CTA may have fewer tiles than that)
+        assert list(broken._ws.values())[0] is ws
+        assert not ws[:q3.Q3PAGED_COUNTER_BYTES].any()
+        assert torch.equal(cache.attend(s["q"], s["off"], s["ctx"], most), want)
+        cache.check()
+    with pytest.raises(q3.Q3Error):
+        q3.PagedKV(s["k"], s["v"], s["table"], n_q_heads=8, inject_timeout=-1)

@@ -73,3 +73,11 @@ def test_arguments_that_are_refused():
                dict(t=None), dict(k=None), dict(p=None), dict(mp=None), dict(ids=None), dict(ld=9)):
         assert draw(**kw) == ERR_ARG, kw
     assert draw(n=0) == 0
+
+
+def test_an_injected_timeout_is_not_negative():
+    import speech_lm_decode_gb300 as q3
+    L = q3.lib()
+    assert L.q3paged_workspace_bytes(ctypes.byref(cache(q3, inject_timeout=3))) > 0
+    assert L.q3paged_workspace_bytes(ctypes.byref(cache(q3, inject_timeout=-1))) == 0
+    assert b"inject_timeout" in L.q3paged_last_error()
