@@ -445,7 +445,8 @@ struct Row {
     }
 
     // The bin of the cluster's histograms in which the running sum of weigh(entry, bin) passes the goal (into
-    // s.edge_bin, -1: none) and the sum in front of it (s.pick64).  All threads of the cluster call it.
+    // s.edge_bin, -1: none) and the sum in front of it (s.pick64).  All threads of the cluster call it; its CTAs have
+    // to get the same, as what they do next, and how often they meet, goes by it.
     // goal(): sets the goal, once the CTAs have met.
     template <class Weigh, class Reach, class Goal>
     __device__ void locate(Weigh weigh, Reach reach, Goal goal) {
@@ -457,13 +458,14 @@ struct Row {
             for (int i = 0; i < 16; ++i) c += s.hist[t * 16 + ((i + t) & 15)];
             s.coarse[t] = c;
         }
-        if (t == 0) { s.pick = -1; s.edge_bin = -1; }
+        if (t == 0) { s.pick = -1; s.edge_bin = -1; s.pick64 = 0; }
         cl.sync();
         u64 c = 0;
         if (t < COARSE) from_all(cl, C, &s.coarse[t], [&](int, uint32_t v) { c += weigh(v, t * 16); });
         goal();
         u64 incl = cta_scan64(s, c);
         if (t < COARSE && !reach(incl - c) && reach(incl)) { s.pick = t; s.pick64 = incl - c; }
+        if (t == COARSE - 1 && !reach(incl)) s.pick64 = incl;   // none: all of it lies in front, on every CTA alike
         __syncthreads();
         if (s.pick >= 0 && t < 32) {
             const int b = s.pick * 16 + (t & 15);
