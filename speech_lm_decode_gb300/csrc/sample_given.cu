@@ -114,25 +114,29 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+// Products of exp_of2: with -0 as an addend that the compiler does not know (a kernel argument).  It fuses packed
+// products and the sums that they enter, rounding modes or not, which it never does with scalar ones; an fma stays.
+__device__ __forceinline__ f2 product2(f2 a, f2 b, f2 zeros) { return fma2(a, b, zeros); }
 // exp_of of the two l - m.  Where that is below -86, exp_of is zero and this is
 // not, but small enough (2^-124) for a weight of zero, which is all that counts.
-__device__ __forceinline__ f2 exp_of2(f2 l, f2 minus_m) {
+__device__ __forceinline__ f2 exp_of2(f2 l, f2 minus_m, f2 zeros) {
     float d0, d1;
     unpk(add2(l, minus_m), d0, d1);
     const f2 c = pk(fmaxf(d0, -87.f), fmaxf(d1, -87.f));
-    const f2 s = add2(mul2(c, pk(kInvLn2, kInvLn2)), pk(12582912.0f, 12582912.0f));
+    const f2 s = add2(product2(c, pk(kInvLn2, kInvLn2), zeros), pk(12582912.0f, 12582912.0f));
     const f2 n = add2(s, pk(-12582912.0f, -12582912.0f));
-    const f2 r = add2(add2(c, mul2(n, pk(-kLn2Hi, -kLn2Hi))), mul2(n, pk(-kLn2Lo, -kLn2Lo)));
+    // (n kLn2Hi is exact, kLn2Hi having 15 bits)
+    const f2 r = add2(fma2(n, pk(-kLn2Hi, -kLn2Hi), c), product2(n, pk(-kLn2Lo, -kLn2Lo), zeros));
     auto both = [](float v) { return pk(v, v); };
     f2 p = both(1.0f / 40320.0f);
-    p = add2(both(1.0f / 5040.0f), mul2(r, p));
-    p = add2(both(1.0f / 720.0f), mul2(r, p));
-    p = add2(both(1.0f / 120.0f), mul2(r, p));
-    p = add2(both(1.0f / 24.0f), mul2(r, p));
-    p = add2(both(1.0f / 6.0f), mul2(r, p));
-    p = add2(both(0.5f), mul2(r, p));
-    p = add2(both(1.0f), mul2(r, p));
-    p = add2(both(1.0f), mul2(r, p));
+    p = add2(both(1.0f / 5040.0f), product2(r, p, zeros));
+    p = add2(both(1.0f / 720.0f), product2(r, p, zeros));
+    p = add2(both(1.0f / 120.0f), product2(r, p, zeros));
+    p = add2(both(1.0f / 24.0f), product2(r, p, zeros));
+    p = add2(both(1.0f / 6.0f), product2(r, p, zeros));
+    p = add2(both(0.5f), product2(r, p, zeros));
+    p = add2(both(1.0f), product2(r, p, zeros));
+    p = add2(both(1.0f), product2(r, p, zeros));
     float p0, p1, s0, s1;
     unpk(p, p0, p1);
     unpk(s, s0, s1);
@@ -320,6 +324,7 @@ struct Row {
     bool vec;            // the slice is aligned for loads of four
     bool quick;          // quotient2 serves the row, with (qt, qy); else its quotients are formed one by one in front of it
     float qt, qy;
+    f2 zeros;            // two of -0 (product2)
 
     __device__ float l_of(int id) const { return q(lval(x, id)); }
     // four logits from the row; -inf behind its end
@@ -370,8 +375,8 @@ struct Row {
     // e of four logits (quotients where quick is not set)
     __device__ __forceinline__ void e_of(const float4& v, float (&a)[4]) const {
         const f2 l0 = quotient2(pk(v.x, v.y), qt, qy), l1 = quotient2(pk(v.z, v.w), qt, qy);
-        unpk(exp_of2(l0, pk(-m, -m)), a[0], a[1]);
-        unpk(exp_of2(l1, pk(-m, -m)), a[2], a[3]);
+        unpk(exp_of2(l0, pk(-m, -m), zeros), a[0], a[1]);
+        unpk(exp_of2(l1, pk(-m, -m), zeros), a[2], a[3]);
         if (kth > -INFINITY) {
             float l[4];
             unpk(l0, l[0], l[1]);
@@ -524,7 +529,7 @@ template <typename T, bool HELD>
 __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, int n, int ahead, const T* logits, int64_t ld,
                                                              const float* u_, const float* temp_, const int32_t* topk_,
                                                              const float* topp_, const float* minp_, int32_t* ids,
-                                                             float* logprob, int* err) {
+                                                             float* logprob, int* err, f2 zeros) {
     pdl_wait();
     pdl_trigger();
     extern __shared__ __align__(16) float e[];
@@ -538,7 +543,7 @@ __global__ void __launch_bounds__(GT, 2) sample_given_kernel(int V, int slice, i
     const int k = topk_[row];
     Merged& M = HELD ? s.lists : *reinterpret_cast<Merged*>(e);
     Row<T, HELD> R{s, cl, e, M, logits + row * ld, Quotient(temp > 0.f ? temp : 1.f), V, C, rank, slice, slice / GW,
-                   rank * slice, 0.f, -INFINITY, false, true, 1.f, 1.f};
+                   rank * slice, 0.f, -INFINITY, false, true, 1.f, 1.f, zeros};
     R.vec = ((uintptr_t)(R.x + R.base) & (4 * sizeof(T) - 1)) == 0;
     const int seg = R.seg, base = R.base, w0 = warp * seg;   // the warp's run of the slice
 
@@ -1146,7 +1151,7 @@ cudaError_t launch_t(int C, int slice, int V, int n, const void* logits, int64_t
     cfg.numAttrs = 2;
     const int ahead = max(1, 2 * device_sm_count() / C);   // rows that run at once, with two CTAs an SM
     return cudaLaunchKernelEx(&cfg, sample_given_kernel<T, HELD>, V, slice, n, ahead, (const T*)logits, ld, u, temp, topk,
-                              topp, minp, ids, logprob, err);
+                              topp, minp, ids, logprob, err, (f2)0x8000000080000000ull);
 }
 
 }  // namespace

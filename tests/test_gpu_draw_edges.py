@@ -29,3 +29,39 @@ def test_histograms_that_fall_short_of_the_limit(n, vocab, dtype):
     u = rng.random(n).astype(np.float32)
     u[::3] = 1 - 2.0 ** -24
     check(torch.from_numpy(x).to(dtype).cuda(), u, 1.0, 0, p, 0.0)
+
+
+def crowds(rows, vocab, dtype, seed):
+    """Rows of two values, the smaller one where top-p cuts, with as many of the larger as bring the border nearest to a
+    step between two ids: it comes out one id off where the weight of the smaller value is a step of fp32 off."""
+    rng = np.random.default_rng(seed)
+    x, p = np.empty((rows, vocab), np.float32), np.empty(rows, np.float32)
+    one = 1 << 40
+    near = []
+    for i in range(rows):
+        d = np.float32(torch.tensor(-rng.uniform(1.0, 2.3)).to(dtype).float())
+        e = float(spec_exp(np.array([d], np.float32))[0])
+        w = int(np.floor(np.ldexp(e, 40)))
+        best = (1.0, 0, 0)
+        top = np.arange(int(0.2 * e * vocab), int(0.4 * e * vocab), dtype=np.int64)
+        for a in range(28, 44):
+            # top-p a / 64 cuts at a / 64 of the whole weight: top + kept w, with how far that is from whole ids
+            rest = (a * ((vocab - top) * w + top * one) - 64 * top * one) % (64 * w)
+            off = np.minimum(rest, 64 * w - rest) / (64 * w)
+            # against what a step of e, 2^-24 of it at least, moves the border by
+            off = off / ((1 - a / 64) * top / e * 2.0 ** -24)
+            best = min(best, (off.min(), a, int(top[off.argmin()])))
+        near.append(best[0])
+        p[i] = best[1] / 64
+        x[i] = d
+        x[i, rng.choice(vocab, best[2], replace=False)] = 0
+    assert np.median(near) < 0.5
+    return torch.from_numpy(x).to(dtype), rng.random(rows).astype(np.float32), p
+
+
+# in shared memory, by a cluster and by one CTA; read again from L2, by one and by two CTAs
+@pytest.mark.parametrize("rows,vocab", [(30, 40000), (150, 15000), (160, 60000), (80, 60000)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_borders_within_a_step_of_a_weight(rows, vocab, dtype):
+    x, u, p = crowds(rows, vocab, dtype, vocab)
+    check(x.cuda(), u, 1.0, 0, p, 0.0)
