@@ -112,10 +112,11 @@ size_t q3paged_workspace_bytes(const q3paged_cache* c);
  * Token i of sequence s stands at position ctx_len[s] - n_s + i and sees the
  * positions up to its own; one that sees nothing (a negative position) gets
  * zeros.  Rows from q_off[n_seqs] on are left as they are, and so are those of
- * a sequence that is skipped for its offsets.  Softmax and sums are fp32.  bf16
- * activations: the weights enter the second product as bf16.  fp32 activations
- * over bf16 pages: q enters with its 24 bits, the weights with 17 (chunks) or
- * 24 (few rows).  Values of keys below ctx_len must be finite; what
+ * a sequence that is skipped for its offsets.  Softmax and sums are fp32, of
+ * scaled scores below 2^127.  bf16 activations: the weights enter the second
+ * product with 8 bits (chunks) or 17 (few rows: new tokens times the q heads of
+ * a kv head up to 16).  fp32 activations over bf16 pages: q enters with its 24
+ * bits, the weights with 17 (chunks) or 24 (few rows: up to 8).  Values of keys below ctx_len must be finite; what
  * pages hold beyond it does not matter.  err may be NULL.  Errors: Q3_ERR_ARG,
  * Q3_ERR_CAPACITY (workspace too small), Q3_ERR_CUDA. */
 int q3paged_attention(const q3paged_cache* c, int n_tokens, int max_q, const void* q, int64_t q_stride,

@@ -17,6 +17,10 @@
 // take the tile's even and odd key tiles, with one output and one reference
 // maximum that is handed on from step to step.
 //
+// bf16 activations: the weights enter the second product rounded to bf16 (their
+// sum is that of the fp32 ones), which adds 1.6e-3 of the result to the 1.7e-3
+// of the output's own rounding; a second part would be half as many products again.
+//
 // fp32 activations enter as three bf16 parts of q (24 bits: exact) and two of p
 // (17 bits), 5 products for 2.  The parts of p have an output each, as the
 // tensor cores cut the terms of a sum to the bits of its largest one: with one

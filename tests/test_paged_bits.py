@@ -168,3 +168,47 @@ def test_a_prompt_in_one_pass_and_in_chunks(kv):
         # against each other: both within fp32 sums of at most 60 terms and the weights' 17 bits
         diff, size = (parts.double() - whole.double()).square().mean().sqrt(), want.square().mean().sqrt()
         assert diff <= 2 * (2.0 ** -17 + 60 * U) * size, (step, float(diff / size))
+
+
+def between(want, bound):
+    """The bf16 values that a result within `bound` of want (relative) can round to: the least and the largest."""
+    return tuple((want * (1 + s * bound)).float().to(torch.bfloat16).double() for s in (-1, 1))
+
+
+BF16_LENS = [(LENS, 4), (LENS, 1), ([(5, 8), (3, 8), (5, 5)], 2)]
+
+
+@pytest.mark.parametrize("lens,group", BF16_LENS)
+def test_weights_in_bf16_pass_the_bound(lens, group):
+    q, k, v = inputs("weights", lens, group, torch.bfloat16)
+    q = q.to(torch.bfloat16).float()
+    want, size, spread = attend(q, k, v, lens, group)
+    lo, hi = between(want, relative_bound(size, spread, lens, 2.0 ** -17))
+    for parts, inside in ((1, False), (2, True)):
+        got = attend(q, k, v, lens, group, p_parts=parts)[0].float().to(torch.bfloat16).double()
+        assert bool(((got >= lo) & (got <= hi)).all()) is inside
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,group", BF16_LENS)
+def test_few_rows_of_bf16_activations_round_once(lens, group):
+    """Their weights keep 17 bits, so that an output is what the fp32 result rounds to."""
+    import speech_lm_decode_gb300 as q3
+    q, ks, vs = inputs("weights", lens, group, torch.bfloat16)
+    q = q.to(torch.bfloat16)
+    pages = len(lens)
+    k = torch.zeros(pages, NKV, PAGE, HD, dtype=torch.bfloat16)
+    v = k.clone()
+    for i, (_, n) in enumerate(lens):
+        k[i, :, :n], v[i, :, :n] = ks[i].transpose(0, 1), vs[i].transpose(0, 1)
+    off = [0]
+    for new, _ in lens:
+        off.append(off[-1] + new)
+    cache = q3.PagedKV(k.cuda(), v.cuda(), torch.arange(pages, dtype=torch.int32)[:, None].cuda(), n_q_heads=NKV * group)
+    got = cache.attend(q.cuda(), torch.tensor(off, dtype=torch.int32).cuda(),
+                       torch.tensor([n for _, n in lens], dtype=torch.int32).cuda(), max(n for n, _ in lens),
+                       scale=1.0).cpu().double()
+    cache.check()
+    want, size, spread = attend(q.float(), ks, vs, lens, group)
+    lo, hi = between(want, relative_bound(size, spread, lens, 2.0 ** -17))
+    assert ((got >= lo) & (got <= hi)).all()
