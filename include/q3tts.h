@@ -327,8 +327,9 @@ int q3tts_sample_logits_noalloc(int n, int vocab, const float* logits, int talke
  *   temperature     [n] f32: > 0, or 0: the largest l (the lowest id on ties)
  *   top_k           [n] <= 0: off
  *   top_p           [n] >= 1: off; min_p [n] <= 0: off
- *   ids_out         [n]; -1 where the logits hold NaN, +inf or nothing finite,
- *                   or the temperature is negative or NaN
+ *   ids_out         [n]; -1 where the logits or their quotients hold NaN (-inf
+ *                   over an infinite temperature too), +inf (overflow too) or
+ *                   nothing finite, or the temperature is negative or NaN
  *   logprob_out     [n] f32 or NULL: log of the drawn id's share of the kept
  *                   weight (0 for temperature 0, NaN where the id is -1)
  *   err             or NULL: bit 1 (value 1) is set where an id is -1

@@ -1,7 +1,8 @@
 // Paged attention (q3paged.h): the choice of kernel, and the one for fp32 pages.
 //
-// fp32 keys and values have no tensor-core form that keeps their 24 bits in
-// fewer than six products, so this kernel multiplies on the CUDA cores.  A CTA
+// fp32 keys and values would take six products of bf16 parts on the tensor cores
+// (a tenth of this kernel's time, with the parts formed as K and V are brought in:
+// not built), so this kernel multiplies on the CUDA cores.  A CTA
 // of 256 threads takes ROWS query rows of one kv head and walks tiles of 64
 // keys in shared memory: V(t) is on its way (cp.async) while the scores of t
 // are formed, K(t+1) while its outputs are.  A thread forms ROWS/16 x 4 scores
@@ -9,7 +10,7 @@
 // multiply-adds; two CTAs fit an SM, as the places in shared memory are mixed
 // against bank conflicts instead of padded.  ROWS =
 // 16 serves a few tokens of many heads.  Bound by the multiply-adds and the
-// shared loads beside them: a prompt of 2048 tokens (16 q, 8 kv heads) 515 us,
+// shared loads beside them: a prompt of 2048 tokens (16 q, 8 kv heads) 519 us,
 // 33 TFLOP/s (padded, with one CTA an SM, 604; packed products: the same).
 #include "common.cuh"
 #include "kernels.h"

@@ -8,6 +8,8 @@
 //               per page and 64 values of the head, 128-byte swizzle);
 //   warp 1      issues S = Q K^T and O += P V (tcgen05.mma, M = N = 128); P is
 //               the A operand in tensor memory, V the transposed B operand;
+//   warp 2      looks for page ids out of range among a cut's: their keys get -inf
+//               as their score (the copies read zeros past the last page);
 //   warps 4-7   softmax of slot 0, warps 8-11 of slot 1: a thread owns a row,
 //               reads its 128 scores from tensor memory, keeps the running
 //               maximum and sum, and writes P back over the scores.
@@ -27,11 +29,11 @@
 // output and three parts of p the error was no smaller (2e-6 to 7e-6 of the
 // result, growing with the context) and the call a fifth slower.
 //
-// Measured (16 q and 8 kv heads): 4096 tokens over 12288, bf16, 351 us = 1.37
+// Measured (16 q and 8 kv heads): 4096 tokens over 12288, bf16, 355 us = 1.36
 // PFLOP/s (72 % of the measured rate; what is left is a slot's softmax between
-// two of its products), fp32 785 us; 24 prompts of 1..512 over 0..255, fp32, 82
+// two of its products), fp32 782 us; 24 prompts of 1..512 over 0..255, fp32, 85
 // us, five items a CTA of two or three steps, of which loading the query rows
-// and the output are the larger part; 64 tokens over 32k, bf16, 55 us.
+// and the output are the larger part; 64 tokens over 32k, bf16, 53 us.
 //
 // Every wait is bounded: one that runs out sets the timeout bit, after which
 // the CTA goes through its remaining steps without waiting or issuing, drains

@@ -25,10 +25,12 @@
 // fp32 pages are multiplied on the CUDA cores, eight lanes a key.
 //
 // Measured (16 q and 8 kv heads): 256 tokens over 1025..1280 positions, bf16,
-// 1.2 GB in 180 us (98 % of the copy rate), fp32 pages 2.4 GB in 343 us; three
-// tokens over 30000..65537 (32 and 4 heads) 55 us for 42 us of reading, the
+// 1.2 GB in 180 us (98 % of the copy rate), fp32 pages 2.4 GB in 345 us; three
+// tokens over 30000..65537 (32 and 4 heads) 56 us for 42 us of reading, the
 // rest being the join of what 456 CTAs hold of 12 items; 32 fp32 tokens over
-// 65..768, 18 us, and one over 228, 8 us, are latencies.
+// 65..768, 17 us, and one over 228, 8 us, are latencies.  Five to eight rows of
+// fp32 activations are two groups that each read the keys (four tokens of 64
+// sequences over 2000: 183 us, bf16 86).
 #include "common.cuh"
 #include "kernels.h"
 #include "paged.h"

@@ -5,8 +5,9 @@
 // once with all rows.  Where a CTA's slice fits (HELD) it is read once into
 // shared memory and everything after that happens there; else each pass reads
 // the row again, from L2 mostly, and forms e again.  Against clusters of eight
-// that hold every slice, 256 rows of 151936 bf16 logits take 180 us instead of
-// 309: the meetings of a cluster cost more than the passes over L2.  The CTAs of
+// that hold every slice, 256 rows of 151936 bf16 logits took 180 us instead of
+// 309 (213 since the products of e are rounded by themselves again): the meetings
+// of a cluster cost more than the passes over L2.  The CTAs of
 // a row exchange maxima, histograms, lists and sums through distributed shared
 // memory.  Kept weights are whole numbers (at most 2^40 each), so no result
 // depends on the order of a sum.
@@ -25,10 +26,10 @@
 //     run is scanned.
 // What bounds it: the meetings of a row's CTAs and the latency of each step at
 // small sizes (one row of 2048 logits, k 50: 10 us; 32 rows of 151936, k 50: 19
-// us); at large ones about 78 instructions a logit (reading 8, quotient, exp and
-// weights 24 in each of two passes, histogram 9, border 10), half of the time
-// in the packed fp32 operations, and the 48 SMs of 152 that have one row of
-// 256 where the others have two.
+// us); at large ones about 87 instructions a logit (reading 8, quotient, exp and
+// weights 29 in each of two passes, histogram 9, border 10), more than half of
+// the time in the packed fp32 operations, and the 48 SMs of 152 that have one row
+// of 256 where the others have two.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
