@@ -339,6 +339,49 @@ int q3tts_sample_given(int n, int vocab, const void* logits, int dtype, int64_t 
                        const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                        int32_t* ids_out, float* logprob_out, int32_t* err, void* stream);
 
+/* Penalties for repeated tokens, biases and grammar masks on logits, in front of
+ * q3tts_sample_given: everything on the device, nothing synchronised, so the call
+ * can be captured into a graph.  Logit x of id i in row r becomes, in fp32 and
+ * rounded once at the end:
+ *   i among the row's history:               x < 0 ? x * repetition : x / repetition
+ *   i in its generated part, c > 0 times:    x - (presence + frequency * c)
+ *   i among the row's biases:                x + the sum of its biases, in their order
+ *   bit i of the row's mask is 0:            -inf
+ *   n, vocab        rows (0..65535), entries of a row (1..262144)
+ *   logits          [n][vocab] f32 or bf16 (dtype), row stride logits_stride
+ *                   elements (0: packed)
+ *   history         [n][history_cap] int32 ids, row stride history_stride (0:
+ *                   packed), or NULL: none.  Row r holds n_history[r] of them, the
+ *                   first n_prompt[r] its prompt (n_prompt NULL: 0; cut to
+ *                   0..n_history[r]), the others generated.  An id < 0 is padding
+ *   repetition, presence, frequency
+ *                   [n] f32, each or NULL: 1, 0, 0
+ *   bias_off        [n + 1]: entries bias_off[r] .. bias_off[r+1]-1 of bias_ids and
+ *                   bias (n_bias entries) are row r's; starts at 0, does not
+ *                   decrease; all three NULL: none
+ *   mask            [n_masks][ceil(vocab / 32)] words, row stride mask_stride words
+ *                   (0: packed), bit i % 32 of word i / 32 set: id i may be drawn;
+ *                   or NULL: none
+ *   mask_row        [n] mask of each row, -1: none; NULL: row r takes mask r
+ *                   (n_masks >= n)
+ *   out             [n][vocab] in the logits' type, row stride out_stride (0:
+ *                   packed); may be the logits themselves (with their stride):
+ *                   then only what changes is written.  It shares no memory with
+ *                   them otherwise
+ *   err             or NULL: bit Q3PAGED_ERR_BOUNDS (2) is set for what is out of
+ *                   range: an id of a history or a bias >= vocab, a bias id < 0
+ *                   (skipped), n_history outside 0..history_cap (cut to it), a
+ *                   row's bias offsets (it has none), mask_row outside
+ *                   -1..n_masks-1 (nothing may be drawn: the row becomes -inf)
+ * All arrays are device memory of the current device and only read, but for out.
+ * Errors: Q3_ERR_ARG, Q3_ERR_CUDA (q3paged_last_error() has the reason). */
+int q3tts_process_logits(int n, int vocab, const void* logits, int dtype, int64_t logits_stride,
+                         const int32_t* history, int history_cap, int64_t history_stride, const int32_t* n_history,
+                         const int32_t* n_prompt, const float* repetition, const float* presence,
+                         const float* frequency, int n_bias, const int32_t* bias_off, const int32_t* bias_ids,
+                         const float* bias, int n_masks, const uint32_t* mask, int64_t mask_stride,
+                         const int32_t* mask_row, void* out, int64_t out_stride, int32_t* err, void* stream);
+
 /* Number of kernel launches one talker step of the current batch makes (the
  * kernel nodes of the step's CUDA graph, which this call records if needed).
  * Errors: Q3_ERR_STATE (no prefill), Q3_ERR_CUDA. */

@@ -24,7 +24,7 @@ PATH_NAMES = {Q3_PATH_GRAPH: "graph", Q3_PATH_FRAME: "frame", Q3_PATH_CLUSTER: "
 
 EXPORTS = ("q3tts_workspace_bytes", "q3tts_create", "q3tts_prefill", "q3tts_step_frames", "q3tts_set_capture",
            "q3tts_sample_logits", "q3tts_sample_logits_noalloc", "q3tts_step_kernel_count", "q3tts_step_path",
-           "q3tts_text_embed", "q3tts_sample_given", "q3tts_last_error", "q3tts_destroy")
+           "q3tts_text_embed", "q3tts_sample_given", "q3tts_process_logits", "q3tts_last_error", "q3tts_destroy")
 
 
 class Q3Error(RuntimeError):
@@ -94,6 +94,13 @@ def lib():
         L.q3tts_sample_logits_noalloc.argtypes = [i32, i32, vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp]
         i64, f32 = ctypes.c_int64, ctypes.c_float
         L.q3tts_sample_given.argtypes = [i32, i32, vp, i32, i64] + [vp] * 9
+        L.q3tts_process_logits.argtypes = [i32, i32, vp, i32, i64, vp, i32, i64] + [vp] * 5 + [i32, vp, vp, vp, i32, vp,
+                                                                                              i64, vp, vp, i64, vp, vp]
+        L.q3paged8_append.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, vp, f32, vp, i32, vp, i64, vp, vp]
+        L.q3paged8_workspace_bytes.restype = ctypes.c_size_t
+        L.q3paged8_workspace_bytes.argtypes = [vp]
+        L.q3paged8_attention.argtypes = [vp, i32, i32, vp, i64, vp, vp, f32, vp, i64, vp, ctypes.c_size_t, vp, vp]
+        L.q3paged8_read.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp]
         L.q3paged_append.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, f32, vp, i32, vp, i64, vp, vp]
         L.q3paged_workspace_bytes.restype = ctypes.c_size_t
         L.q3paged_workspace_bytes.argtypes = [vp]
@@ -584,6 +591,13 @@ class PagedKV:
     with it are replayed.  inject_timeout is for tests (q3paged_cache)."""
 
     def __init__(self, k_pages, v_pages, page_table, n_q_heads: int, inject_timeout: int = 0):
+        self._pools(k_pages, v_pages)
+        c = self._describe(k_pages, v_pages, page_table, n_q_heads, inject_timeout)
+        c.kv_dtype = _dtype_code(k_pages)
+        self._ready(c, lambda c, act: setattr(c, "act_dtype", act), lib().q3paged_workspace_bytes)
+
+    @staticmethod
+    def _pools(k_pages, v_pages):
         import torch
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
             if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and t.shape[3] == 128 and
@@ -593,6 +607,10 @@ class PagedKV:
         if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
                 or k_pages.device != v_pages.device:
             raise ValueError("k_pages and v_pages must agree in type, shape, strides and device")
+
+    def _describe(self, k_pages, v_pages, page_table, n_q_heads, inject_timeout):
+        """The cache's description, but for its types."""
+        import torch
         if not (isinstance(page_table, torch.Tensor) and page_table.dim() == 2):
             raise ValueError("page_table: an int32 tensor [n_seqs, max_pages] is expected")
         self.device, self._dev = k_pages.device, k_pages.get_device()
@@ -605,20 +623,23 @@ class PagedKV:
             raise ValueError("k_pages and v_pages: pages, heads and positions must not share memory")
         c.page_stride, c.head_stride, c.token_stride = steps
         c.n_q_heads, c.inject_timeout = n_q_heads, inject_timeout
-        c.kv_dtype = _dtype_code(k_pages)
         c.n_seqs, c.max_pages = page_table.shape
         c.k_pages, c.v_pages = k_pages.data_ptr(), v_pages.data_ptr()
         c.page_table = _need(page_table, "page_table", torch.int32, page_table.shape, self._dev)
         self.nq, self.nkv = n_q_heads, c.n_kv_heads
         self._q_off_shape, self._ctx_shape = (c.n_seqs + 1,), (c.n_seqs,)
-        # one description for each type of activations
+        return c
+
+    def _ready(self, c, set_act, workspace_bytes):
+        """One description for each type of activations, the workspace's size and the error word."""
+        import torch
         self._c = {}
         for act in (Q3_F32, Q3_BF16):
-            d = PagedCache.from_buffer_copy(c)
-            d.act_dtype = act
+            d = type(c).from_buffer_copy(c)
+            set_act(d, act)
             self._c[torch.float32 if act == Q3_F32 else torch.bfloat16] = (d, ctypes.addressof(d))
         self._lib = lib()
-        self.ws_bytes = self._lib.q3paged_workspace_bytes(self._c[torch.float32][1])
+        self.ws_bytes = workspace_bytes(self._c[torch.float32][1])
         if self.ws_bytes == 0:
             _paged_raise(Q3_ERR_ARG)
         self._ws = {}
@@ -712,6 +733,97 @@ class PagedKV:
                           "a page, position or length is out of range")
 
 
+# ---------------------------------------------------------------- paged cache in 8 bits (q3paged8.h)
+PAGED8_EXPORTS = ("q3paged8_append", "q3paged8_workspace_bytes", "q3paged8_attention", "q3paged8_read")
+Q3_E4M3 = 2
+
+
+class Paged8Cache(ctypes.Structure):
+    _fields_ = [("cache", PagedCache), ("scale_block", ctypes.c_int), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class PagedKV8(PagedKV):
+    """A paged key / value cache in 8 bits over tensors that the caller owns (q3paged8.h).
+
+    k_pages, v_pages: float8_e4m3fn CUDA tensors [n_pages, n_kv_heads, page_size, 128] as PagedKV takes them; k_scale,
+    v_scale: contiguous [n_pages, n_kv_heads, page_size // block], float8_e8m0fnu (or their bytes as uint8), a
+    power-of-two scale for each block of 16 or more positions of a head.  Nothing of it has to be cleared before its
+    first use.  append, attend and read are queued on the current stream, with the workspaces and the rules of
+    PagedKV."""
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale, page_table, n_q_heads: int, inject_timeout: int = 0):
+        import torch
+        self._pools(k_pages, v_pages)
+        if k_pages.dtype is not torch.float8_e4m3fn:
+            raise ValueError("k_pages and v_pages: float8_e4m3fn tensors are expected")
+        c = Paged8Cache()
+        c.cache = self._describe(k_pages, v_pages, page_table, n_q_heads, inject_timeout)
+        c.cache.kv_dtype = Q3_E4M3
+        n, heads, page, _ = k_pages.shape
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if not (isinstance(t, torch.Tensor) and t.dtype in (torch.float8_e8m0fnu, torch.uint8) and t.dim() == 3 and
+                    t.shape[:2] == (n, heads) and 0 < t.shape[2] <= page and page % t.shape[2] == 0 and
+                    t.shape == k_scale.shape and t.get_device() == self._dev and t.is_contiguous()):
+                raise ValueError(f"{name}: a contiguous float8_e8m0fnu tensor [n_pages, n_kv_heads, page_size // block] "
+                                 f"on {self.device} is expected")
+        self.k_scale, self.v_scale = k_scale, v_scale
+        c.scale_block = page // k_scale.shape[2]
+        c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        self._ready(c, lambda c, act: setattr(c.cache, "act_dtype", act), lib().q3paged8_workspace_bytes)
+
+    def append(self, qkv, q_off, ctx_len, max_q: int, rope, q_norm=None, k_norm=None, eps=1e-6, out=None):
+        """Norms and turns the q and k heads of qkv [n, (nq + 2 nkv) * 128], whose rows q_off[s]..q_off[s+1]-1 are the
+        newest tokens of sequence s with ctx_len[s] positions (int32 tensors; max_q bounds the new tokens of a
+        sequence), stores keys and values as codes and returns the queries [n, nq, 128].  rope: float32 [rows, 64, 2],
+        cosine and sine of each pair at each position."""
+        from torch import float32, int32
+        c = self._act(qkv)
+        n, ld = self._rows(qkv, "qkv", self.nq + 2 * self.nkv)
+        out, ldo = self._out(out, n, qkv)
+        dev, rows = self._dev, rope.shape[0]
+        _on_stream(dev, lambda stream: self._lib.q3paged8_append(
+            c, n, max_q, qkv.data_ptr(), ld, _need(q_off, "q_off", int32, self._q_off_shape, dev),
+            _need(ctx_len, "ctx_len", int32, self._ctx_shape, dev),
+            None if q_norm is None else _need(q_norm, "q_norm", float32, (128,), dev),
+            None if k_norm is None else _need(k_norm, "k_norm", float32, (128,), dev), eps,
+            _need(rope, "rope", float32, (rows, 64, 2), dev), rows, out.data_ptr(), ldo, self._err, stream))
+        return out
+
+    def attend(self, q, q_off, ctx_len, max_q: int, scale=128 ** -0.5, out=None):
+        """Causal attention of the newest tokens of every sequence over the cache: PagedKV.attend's arguments."""
+        from torch import int32
+        c = self._act(q)
+        n, ld = self._rows(q, "q", self.nq)
+        out, ldo = self._out(out, n, q)
+        off = _need(q_off, "q_off", int32, self._q_off_shape, self._dev)
+        ctx = _need(ctx_len, "ctx_len", int32, self._ctx_shape, self._dev)
+        _on_stream(self._dev, lambda stream: self._lib.q3paged8_attention(
+            c, n, max_q, q.data_ptr(), ld, off, ctx, scale, out.data_ptr(), ldo, self._workspace(stream).data_ptr(),
+            self.ws_bytes, self._err, stream))
+        return out
+
+    def read(self, pages, dtype=None, k_out=None, v_out=None):
+        """The values that pages (int32 [n], any order) stand for: (k, v), each [n, n_kv_heads, page_size, 128] in
+        dtype (bfloat16 or float32; default bfloat16, or that of an output given)."""
+        import torch
+        n, dev = pages.shape[0], self._dev
+        if dtype is None:
+            dtype = next((t.dtype for t in (k_out, v_out) if t is not None), torch.bfloat16)
+        shape = (n,) + tuple(self.k_pages.shape[1:])
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=self.device)
+            _need(t, name, dtype, shape, dev)
+            outs.append(t)
+        code = _dtype_code(outs[0])
+        _on_stream(dev, lambda stream: self._lib.q3paged8_read(
+            self._c[torch.float32][1], n, _need(pages, "pages", torch.int32, (n,), dev), code, outs[0].data_ptr(),
+            outs[1].data_ptr(), self._err, stream))
+        return tuple(outs)
+
+
 def sample_given(logits, u, temperature, top_k, top_p, min_p, ids=None, logprob=None, err=None):
     """Draws one id for each row of logits ([n, vocab], float32 or bfloat16) from the given uniform numbers u,
     everything on the GPU and queued on the current stream: u, temperature, top_p, min_p float32 [n], top_k
@@ -737,3 +849,56 @@ def sample_given(logits, u, temperature, top_k, top_p, min_p, ids=None, logprob=
     _on_stream(dev, lambda stream: lib().q3tts_sample_given(
         n, vocab, logits.data_ptr(), _dtype_code(logits), logits.stride(0) if n > 1 else vocab, *args, stream))
     return ids, logprob
+
+
+def _rows2d(t, name, n, width, dtypes, dev):
+    """A 2-D CUDA tensor [n, width] with contiguous rows that do not share memory: its row stride."""
+    if t.dim() != 2 or t.dtype not in dtypes or t.get_device() != dev or t.shape[0] != n or \
+            (width is not None and t.shape[1] != width) or (t.shape[1] > 1 and t.stride(1) != 1) or \
+            (n > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: [{n}, {'any' if width is None else width}] with contiguous rows, "
+                         f"{' or '.join(str(d) for d in dtypes)}, on cuda:{dev} is expected")
+    return t.stride(0) if n > 1 else t.shape[1]
+
+
+def process_logits(logits, history=None, n_history=None, n_prompt=None, repetition=None, presence=None, frequency=None,
+                   bias_off=None, bias_ids=None, bias=None, mask=None, mask_row=None, out=None, err=None):
+    """Penalties for repeated tokens, biases and grammar masks on logits ([n, vocab], float32 or bfloat16), in front of
+    sample_given; everything on the GPU and queued on the current stream (q3tts_process_logits in q3tts.h has the
+    definition).  history: int32 [n, cap], the ids of each row's tokens, of which n_history (int32 [n]) count and the
+    first n_prompt (int32 [n]) are its prompt; repetition, presence, frequency: float32 [n]; bias_off: int32 [n + 1],
+    bias_ids (int32) and bias (float32): lists of all rows one after the other; mask: int32 [masks, ceil(vocab / 32)],
+    a bit for each id that may be drawn; mask_row: int32 [n], the mask of each row or -1.  Returns out ([n, vocab] of
+    the logits' type), which may be the logits themselves.  err: int32 [1] or None."""
+    import torch
+    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2):
+        raise ValueError("logits: a CUDA tensor [n, vocab] with contiguous rows is expected")
+    (n, vocab), dev, f, i32 = logits.shape, logits.get_device(), torch.float32, torch.int32
+    code = _dtype_code(logits)
+    ld = _rows2d(logits, "logits", n, vocab, (logits.dtype,), dev)
+    if out is None:
+        out = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
+    ldo = _rows2d(out, "out", n, vocab, (logits.dtype,), dev)
+
+    def row(t, name, dtype, size=n):
+        return None if t is None else _need(t, name, dtype, (size,), dev)
+    cap, ldh, n_bias, n_masks, ldm = 0, 0, 0, 0, 0
+    if history is not None:
+        ldh, cap = _rows2d(history, "history", n, None, (i32,), dev), history.shape[1]
+        if cap == 0:
+            history = n_history = n_prompt = None
+    if bias_ids is not None:
+        n_bias = bias_ids.shape[0]
+        if n_bias == 0:
+            bias_off = bias_ids = bias = None
+    if mask is not None:
+        n_masks = mask.shape[0]
+        ldm = _rows2d(mask, "mask", n_masks, (vocab + 31) // 32, (i32,), dev)
+    args = (row(n_history, "n_history", i32), row(n_prompt, "n_prompt", i32), row(repetition, "repetition", f),
+            row(presence, "presence", f), row(frequency, "frequency", f), n_bias, row(bias_off, "bias_off", i32, n + 1),
+            row(bias_ids, "bias_ids", i32, n_bias), row(bias, "bias", f, n_bias), n_masks,
+            None if mask is None else mask.data_ptr(), ldm, row(mask_row, "mask_row", i32), out.data_ptr(), ldo,
+            row(err, "err", i32, 1))
+    _on_stream(dev, lambda stream: lib().q3tts_process_logits(
+        n, vocab, logits.data_ptr(), code, ld, None if history is None else history.data_ptr(), cap, ldh, *args, stream))
+    return out

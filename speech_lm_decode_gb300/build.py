@@ -11,7 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libq3tts.so")
 SOURCES = ["linear.cu", "gemm_tc.cu", "attention.cu", "sampler.cu", "loop.cu", "persist.cu", "cluster_step.cu", "q3tts.cu",
-           "noalloc.cu", "codec.cu", "paged.cu", "paged_attn.cu", "paged_decode.cu", "paged_chunk.cu", "sample_given.cu"]
+           "noalloc.cu", "codec.cu", "paged.cu", "paged_attn.cu", "paged_decode.cu", "paged_chunk.cu", "sample_given.cu",
+           "paged8.cu", "paged8_attn.cu", "process_logits.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -34,7 +35,7 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    headers += [os.path.join(ROOT, "include", f) for f in ("q3tts.h", "q3codec.h", "q3paged.h")]
+    headers += [os.path.join(ROOT, "include", f) for f in ("q3tts.h", "q3codec.h", "q3paged.h", "q3paged8.h")]
     procs, objs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -167,8 +167,9 @@ namespace {
 int esize(int dtype) { return dtype == Q3_BF16 ? 2 : 4; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// the cache as kernels see it; pools: the page pointers and strides are checked too
-int view_of(const q3paged_cache* c, PagedView* v, bool pools) {
+}  // namespace
+
+int paged_view(const q3paged_cache* c, PagedView* v, bool pools) {
     if (!c) return paged_fail(Q3_ERR_ARG, "cache is NULL");
     if (c->head_dim != HD) return paged_fail(Q3_ERR_ARG, "head_dim must be 128");
     if (c->n_kv_heads < 1 || c->n_kv_heads > 256 || c->n_q_heads < c->n_kv_heads || c->n_q_heads % c->n_kv_heads ||
@@ -207,8 +208,7 @@ int view_of(const q3paged_cache* c, PagedView* v, bool pools) {
     return Q3_OK;
 }
 
-// rows of activations: pointer, stride (0: packed) and alignment
-int rows_ok(const char* what, const void* p, int64_t* stride, int width, int dtype) {
+int paged_rows(const char* what, const void* p, int64_t* stride, int width, int dtype) {
     if (!p) return paged_fail(Q3_ERR_ARG, "%s is NULL", what);
     if (*stride == 0) *stride = width;
     if (*stride < width || *stride * esize(dtype) % 16 || !aligned16(p))
@@ -216,7 +216,35 @@ int rows_ok(const char* what, const void* p, int64_t* stride, int width, int dty
     return Q3_OK;
 }
 
-}  // namespace
+int paged_attn_args(PagedAttn* a, const q3paged_cache* cache, int n_tokens, int max_q, const void* q, int64_t q_stride,
+                    const int32_t* q_off, const int32_t* ctx_len, float scale, void* out, int64_t out_stride,
+                    void* workspace, size_t workspace_bytes, int32_t* err) {
+    int r;
+    if ((r = paged_rows("q", q, &q_stride, a->c.nq * HD, cache->act_dtype))) return r;
+    if ((r = paged_rows("out", out, &out_stride, a->c.nq * HD, cache->act_dtype))) return r;
+    if (!q_off || !ctx_len) return paged_fail(Q3_ERR_ARG, "NULL q_off or ctx_len");
+    if (!(scale > 0.f) || std::isinf(scale)) return paged_fail(Q3_ERR_ARG, "scale must be finite and > 0");
+    if (!workspace || ((uintptr_t)workspace & 255)) return paged_fail(Q3_ERR_ARG, "workspace must be 256-byte aligned");
+    if (workspace_bytes < paged_workspace_bytes())
+        return paged_fail(Q3_ERR_CAPACITY, "workspace of %zu bytes: %zu are needed", workspace_bytes,
+                          paged_workspace_bytes());
+    a->act = cache->act_dtype;
+    a->kv = cache->kv_dtype;
+    a->inject = cache->inject_timeout;
+    a->n_tokens = n_tokens;
+    a->max_q = max_q < n_tokens ? max_q : n_tokens;
+    a->q = q;
+    a->q_stride = q_stride;
+    a->q_off = q_off;
+    a->ctx = ctx_len;
+    a->scale = scale;
+    a->out = out;
+    a->out_stride = out_stride;
+    a->ws = workspace;
+    a->err = err;
+    return Q3_OK;
+}
+
 }  // namespace q3
 
 using namespace q3;
@@ -229,12 +257,12 @@ int q3paged_append(const q3paged_cache* cache, int n_tokens, const void* qkv, in
                    const int32_t* tok_seq, const int32_t* tok_pos, const float* q_norm, const float* k_norm, float eps,
                    const float* rope_cs, int rope_rows, void* q_out, int64_t q_stride, int32_t* err, void* stream) {
     PagedView v;
-    int r = view_of(cache, &v, true);
+    int r = paged_view(cache, &v, true);
     if (r) return r;
     if (n_tokens < 0) return paged_fail(Q3_ERR_ARG, "negative n_tokens");
     if (n_tokens == 0) return Q3_OK;
-    if ((r = rows_ok("qkv", qkv, &qkv_stride, (v.nq + 2 * v.nkv) * HD, cache->act_dtype))) return r;
-    if ((r = rows_ok("q_out", q_out, &q_stride, v.nq * HD, cache->act_dtype))) return r;
+    if ((r = paged_rows("qkv", qkv, &qkv_stride, (v.nq + 2 * v.nkv) * HD, cache->act_dtype))) return r;
+    if ((r = paged_rows("q_out", q_out, &q_stride, v.nq * HD, cache->act_dtype))) return r;
     if (!tok_seq || !tok_pos || !rope_cs) return paged_fail(Q3_ERR_ARG, "NULL tok_seq, tok_pos or rope_cs");
     if (!q_norm != !k_norm) return paged_fail(Q3_ERR_ARG, "q_norm and k_norm: both or neither");
     if (!aligned16(rope_cs) || !aligned16(q_norm) || !aligned16(k_norm))
@@ -250,7 +278,7 @@ int q3paged_append(const q3paged_cache* cache, int n_tokens, const void* qkv, in
 
 size_t q3paged_workspace_bytes(const q3paged_cache* cache) {
     PagedView v;
-    if (view_of(cache, &v, false)) return 0;
+    if (paged_view(cache, &v, false)) return 0;
     return paged_workspace_bytes();
 }
 
@@ -258,32 +286,13 @@ int q3paged_attention(const q3paged_cache* cache, int n_tokens, int max_q, const
                       const int32_t* q_off, const int32_t* ctx_len, float scale, void* out, int64_t out_stride,
                       void* workspace, size_t workspace_bytes, int32_t* err, void* stream) {
     PagedAttn a{};
-    int r = view_of(cache, &a.c, true);
+    int r = paged_view(cache, &a.c, true);
     if (r) return r;
     if (n_tokens < 0 || max_q < 0) return paged_fail(Q3_ERR_ARG, "negative n_tokens or max_q");
     if (n_tokens == 0 || max_q == 0) return Q3_OK;
-    if ((r = rows_ok("q", q, &q_stride, a.c.nq * HD, cache->act_dtype))) return r;
-    if ((r = rows_ok("out", out, &out_stride, a.c.nq * HD, cache->act_dtype))) return r;
-    if (!q_off || !ctx_len) return paged_fail(Q3_ERR_ARG, "NULL q_off or ctx_len");
-    if (!(scale > 0.f) || std::isinf(scale)) return paged_fail(Q3_ERR_ARG, "scale must be finite and > 0");
-    if (!workspace || ((uintptr_t)workspace & 255)) return paged_fail(Q3_ERR_ARG, "workspace must be 256-byte aligned");
-    if (workspace_bytes < paged_workspace_bytes())
-        return paged_fail(Q3_ERR_CAPACITY, "workspace of %zu bytes: %zu are needed", workspace_bytes,
-                          paged_workspace_bytes());
-    a.act = cache->act_dtype;
-    a.kv = cache->kv_dtype;
-    a.inject = cache->inject_timeout;
-    a.n_tokens = n_tokens;
-    a.max_q = max_q < n_tokens ? max_q : n_tokens;
-    a.q = q;
-    a.q_stride = q_stride;
-    a.q_off = q_off;
-    a.ctx = ctx_len;
-    a.scale = scale;
-    a.out = out;
-    a.out_stride = out_stride;
-    a.ws = workspace;
-    a.err = err;
+    if ((r = paged_attn_args(&a, cache, n_tokens, max_q, q, q_stride, q_off, ctx_len, scale, out, out_stride, workspace,
+                             workspace_bytes, err)))
+        return r;
     const cudaError_t e = launch_paged_attention(a, (cudaStream_t)stream);
     if (e != cudaSuccess) return paged_fail(Q3_ERR_CUDA, "attention: %s", cudaGetErrorString(e));
     return Q3_OK;

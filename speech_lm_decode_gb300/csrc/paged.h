@@ -49,6 +49,15 @@ size_t paged_decode_ws();
 cudaError_t launch_paged_chunk(const PagedAttn& a, cudaStream_t st);
 size_t paged_chunk_ws();
 
+// argument checks (paged.cu).  The cache as kernels see it; pools: the page pointers and strides are checked too.
+int paged_view(const q3paged_cache* c, PagedView* v, bool pools);
+// rows of activations: pointer, stride (0: packed) and alignment
+int paged_rows(const char* what, const void* p, int64_t* stride, int width, int dtype);
+// an attention call's other arguments into a, whose view is there already
+int paged_attn_args(PagedAttn* a, const q3paged_cache* cache, int n_tokens, int max_q, const void* q, int64_t q_stride,
+                    const int32_t* q_off, const int32_t* ctx_len, float scale, void* out, int64_t out_stride,
+                    void* workspace, size_t workspace_bytes, int32_t* err);
+
 // text of the calling thread's last error (q3paged_last_error)
 int paged_fail(int code, const char* fmt, ...);
 

@@ -1,0 +1,57 @@
+// Shared by the operators over a paged cache of 8-bit codes (q3paged8.h).
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "paged.h"
+#include "q3paged8.h"
+
+namespace q3 {
+
+// PagedView's strides are in codes (bytes); scales: [page][kv head][block]
+struct Paged8Attn : PagedAttn {
+    int block_shift;             // positions of a block: 1 << block_shift
+    const uint8_t *ks, *vs;
+};
+
+struct Paged8Append {
+    PagedView c;
+    int block_shift;
+    uint8_t *ks, *vs;
+    int n_tokens, max_q;
+    const void* qkv;
+    int64_t ldq;
+    const int32_t *q_off, *ctx;
+    const float *qn, *kn;
+    float eps;
+    const float2* rope;
+    int rope_rows;
+    void* q_out;
+    int64_t ldo;
+    int* err;
+};
+
+cudaError_t launch_paged8_attention(const Paged8Attn& a, cudaStream_t st);
+
+constexpr int E8_MIN = 127 - 100, E8_MAX = 127 + 119;   // scales that append writes
+
+// 2^(b - 127); 255: NaN
+__device__ __forceinline__ float e8m0(uint32_t b) {
+    return __uint_as_float(b == 255 ? 0x7fffffffu : b == 0 ? 0x00400000u : b << 23);
+}
+// two codes as f16 values (exact), the lower byte first
+__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
+    return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+__device__ __forceinline__ float2 float2_of(uint32_t codes) {
+    const uint32_t h = half2_of(codes);
+    return __half22float2(*(const __half2*)&h);
+}
+// two values as codes, the first in the lower byte: nearest, ties to even, at most 448 (NaN stays, infinities do not)
+__device__ __forceinline__ uint32_t codes_of(float a, float b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+}  // namespace q3
