@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(128) paged8_row_kernel(const Paged8Attn a) {
 }  // namespace
 
 cudaError_t launch_paged8_attention(const Paged8Attn& a, cudaStream_t st) {
+    if (paged8_decode_takes(a)) return launch_paged8_decode(a, st);
     const dim3 grid((unsigned)min((int64_t)a.max_q * a.c.nq / 4 + 1, (int64_t)1024), a.c.n_seqs);
     return a.act == Q3_BF16 ? launch_pdl(paged8_row_kernel<bf16>, grid, 128, 0, st, a)
                             : launch_pdl(paged8_row_kernel<float>, grid, 128, 0, st, a);

@@ -1,0 +1,465 @@
+// Paged attention over 8-bit codes for few query rows (single tokens, a handful
+// of tokens of a sequence): q3paged8_attention's kernel while the new tokens
+// times the q heads of a kv head fit a tile or two of tensor-core columns.
+//
+// Bound by reading K and V once (256 bytes a key and kv head).  As over bf16
+// pages (paged_decode.cu), a CTA of four warps walks its keys in blocks of 16, a
+// warp to a block, K and V go from global memory straight into the fragments of
+// mma.m16n8k16, scores are K q^T and outputs V^T p^T.  Codes become f16 on the
+// way, which holds each exactly: a lane's 16 bytes of a K row are four k-steps of
+// its A fragment with the head dimension of K and q permuted alike, its 16 bytes
+// of two V rows, bytes interleaved, fragments of two output values at a time.
+//
+// Scales stay out of the tensor cores, so that they may be any: the 16 keys of a
+// block have one scale, the keys' multiplies the scores, and the values' the
+// block's output as it is added to the sum, in fp32.  q enters relative to the
+// power of two above its row's largest value, the weights relative to 2^-7 of the
+// running maximum (f16 then holds a weight of 2^-21 of it with all its bits, and
+// as the maximum moves only when a score passes it by 2^8, none passes 2^15).
+//
+// bf16 activations are exact in one f16 part, their weights take one (11 bits;
+// the output's rounding keeps 8).  fp32 activations take two columns a row, f16
+// parts of 22 bits together, and so do their weights.
+#include "common.cuh"
+#include "kernels.h"
+#include "paged8.h"
+#include "paged_sched.cuh"
+#include "pdl.cuh"
+
+namespace q3 {
+
+namespace {
+
+constexpr int DW = 4;             // warps of a CTA
+constexpr int DU = 64;            // keys of a unit
+constexpr int d8_ctas(int nt) { return nt == 1 ? 4 : 3; }   // resident CTAs of an SM (registers)
+constexpr float P_SHIFT = 7.f;    // weights are 2^7 times exp2 of score - maximum
+
+__device__ __forceinline__ uint4 ldg16(const void* p, bool ok) {
+    uint4 r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+        "mov.b32 %3, 0;\n\t@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"((int)ok));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *(const uint32_t*)&v;
+}
+// what the f16 part h of two values leaves of them, as f16
+__device__ __forceinline__ uint32_t rest2(float x0, float x1, uint32_t h) {
+    const float2 f = __half22float2(*(const __half2*)&h);
+    return half2_bits(x0 - f.x, x1 - f.y);
+}
+// transposes an 8 x 8 matrix of 16-bit values (lane (g, t): row g, columns 2t and 2t+1)
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// NT: column tiles of eight; a query row takes one column (bf16 activations) or two (fp32: columns 8 n + r and
+// 8 n + 4 + r hold the parts of row 4 n + r).
+template <typename TA, int NT>
+__global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(const Paged8Attn a, int grid_max) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr bool F32 = sizeof(TA) == 4;
+    constexpr int RG = F32 ? 4 * NT : 8 * NT;   // query rows of an item
+    const PagedView& c = a.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    constexpr int SO = DW * 8 * NT * (HD + 4), WT = 160 * d8_ctas(NT) * RG;
+    __shared__ __align__(16) float so_all[SO > WT ? SO : WT];   // outputs; the weights of an item's parts
+    float (*so)[8 * NT][HD + 4] = (float (*)[8 * NT][HD + 4])so_all;
+    __shared__ float sm_m[DW][RG], sm_l[DW][RG];
+    __shared__ int s_last;
+
+    auto units_of = [&](const PagedSeq& q) -> long long {
+        if (q.n_new <= 0) return 0;
+        const int groups = (q.n_new * c.G + RG - 1) / RG;
+        return (long long)c.nkv * groups * max(1, (q.ctx + DU - 1) / DU);
+    };
+    const PagedRange R = paged_range<DW * 32>(a, grid_max, 1, 0, units_of);
+    if (R.u0 >= R.u1) return;
+    const float sl2 = a.scale * 1.4426950408889634f;   // scores in powers of two
+    int* counters = (int*)a.ws;
+    constexpr size_t SLOT = (size_t)RG * (HD + 4);   // outputs, maxima, sums (16-byte rows)
+    float* parts = (float*)((char*)a.ws + PAGED_COUNTER_BYTES);
+
+    int s = R.s;
+    PagedSeq q = R.q;
+    int nu = max(1, (q.ctx + DU - 1) / DU), groups = (q.n_new * c.G + RG - 1) / RG;   // units and row groups of a head
+    int item = (R.u0 - R.start) / nu;       // head * groups + row group
+    int item0 = R.start + item * nu;        // the item's units [item0, item0 + nu)
+    auto next_item = [&]() -> bool {
+        item0 += nu;
+        if (++item < c.nkv * groups) return true;
+        if (item0 >= R.u1) return false;
+        do { q = paged_seq(a, ++s, false); } while (q.n_new <= 0);
+        nu = max(1, (q.ctx + DU - 1) / DU);
+        groups = (q.n_new * c.G + RG - 1) / RG;
+        item = 0;
+        return true;
+    };
+    int u = paged_begin(R, item0, item0 + nu), seg_end;
+    if (u == item0 + nu && !next_item()) return;
+    while (paged_cut(R, item0, item0 + nu, &seg_end)) {
+        const int h = item / groups, rg = item - h * groups;
+        const int key0 = (u - item0) * DU;
+        const int key1 = (int)min((long long)q.ctx, (long long)(seg_end - item0) * DU);
+        const int rows = min(RG, q.n_new * c.G - rg * RG);
+
+        const int nb = (key1 - key0 + 15) >> 4;
+        const int32_t* table = c.table + (int64_t)s * c.max_pages;
+        const int pmask = (1 << c.page_shift) - 1;
+        const int64_t head_off = (int64_t)h * c.head_stride;
+        auto page_at = [&](int b) -> int {   // page of block b; < 0: none
+            if (b >= nb) return -1;
+            const int pg = __ldg(table + ((key0 + b * 16) >> c.page_shift));
+            return (unsigned)pg < (unsigned)c.n_pages ? pg : -1;
+        };
+        // blocks of 16 keys: lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9
+        const uint8_t* kbase = (const uint8_t*)c.k + head_off + g * c.token_stride + t * 16;
+        const uint8_t* vbase = (const uint8_t*)c.v + head_off + 2 * t * c.token_stride + g * 16;
+        uint4 kr[2][2], vr[4];
+        uint32_t ks = 0, vs = 0;
+        auto scale_at = [&](const uint8_t* sc, int kb, int pg) -> uint32_t {
+            return sc[(((int64_t)pg * c.nkv + h) << (c.page_shift - a.block_shift)) + ((kb & pmask) >> a.block_shift)];
+        };
+        auto load_k = [&](int b, int pg) {
+            const int kb = key0 + b * 16;
+            const uint8_t* p = kbase + (int64_t)max(pg, 0) * c.page_stride + (int64_t)(kb & pmask) * c.token_stride;
+            if (pg >= 0) ks = scale_at(a.ks, kb, pg);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool ok = pg >= 0 && kb + g + 8 * i < key1;
+                kr[i][0] = ldg16(p, ok);
+                kr[i][1] = ldg16(p + 64, ok);
+                p += 8 * c.token_stride;
+            }
+        };
+        auto load_v = [&](int b, int pg) {
+            const int kb = key0 + b * 16;
+            const uint8_t* p = vbase + (int64_t)max(pg, 0) * c.page_stride + (int64_t)(kb & pmask) * c.token_stride;
+            vs = pg >= 0 ? scale_at(a.vs, kb, pg) : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                vr[i] = ldg16(p, pg >= 0 && kb + 2 * t + (i & 1) + 8 * (i >> 1) < key1);
+                p += (i == 1 ? 7 : 1) * c.token_stride;
+            }
+        };
+        int b = warp;
+        int pg = page_at(b), pgn = page_at(b + DW);
+        if (b < nb) { load_k(b, pg); load_v(b, pg); }
+
+        // ---- query rows into B fragments, and the factors of the rows whose softmax the lane follows (columns 2t, 2t+1)
+        uint32_t qb[NT][8][2];
+        float qs[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = F32 ? 4 * n + (g & 3) : 8 * n + g;
+            const bool there = r < rows;
+            const int rr = rg * RG + r, tok = rr / c.G;
+            const TA* src = (const TA*)a.q + (int64_t)(q.row0 + (there ? tok : 0)) * a.q_stride +
+                            (int64_t)(h * c.G + (there ? rr - tok * c.G : 0)) * HD + t * 16;
+            float x[32], top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; j += 16 / (int)sizeof(TA)) {
+                const uint4 w = there ? *(const uint4*)(src + (j >> 4) * 64 + (j & 15)) : make_uint4(0, 0, 0, 0);
+                if constexpr (F32) {
+                    x[j] = __uint_as_float(w.x); x[j + 1] = __uint_as_float(w.y);
+                    x[j + 2] = __uint_as_float(w.z); x[j + 3] = __uint_as_float(w.w);
+                } else {
+                    float v[8];
+                    unpack_bf16x8(w, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[j + i] = v[i];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(x[j]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = min((int)(__float_as_uint(top) >> 23), 254), fe = min(268 - ex, 253);   // largest value to 2^14..2^15
+            const float f = __uint_as_float((uint32_t)fe << 23);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x0 = x[4 * j + 2 * e] * f, x1 = x[4 * j + 2 * e + 1] * f;
+                    const uint32_t hi = half2_bits(x0, x1);
+                    qb[n][j][e] = F32 && g >= 4 ? rest2(x0, x1, hi) : hi;
+                }
+            const float inv = sl2 * __uint_as_float((uint32_t)(254 - fe) << 23);
+            qs[n][0] = __shfl_sync(0xffffffffu, inv, 8 * t);
+            qs[n][1] = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+        }
+        int lim[NT][2];   // keys that those rows see
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = F32 ? 4 * n + 2 * (t & 1) + e : 8 * n + 2 * t + e;
+                lim[n][e] = r < rows ? min(q.ctx - q.n_new + (rg * RG + r) / c.G + 1, key1) : 0;
+            }
+        const int lim_all = min(q.ctx - q.n_new + rg * RG / c.G + 1, key1);   // keys that every row sees
+
+        float o[NT][8][4], mx[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[n][i >> 2][i & 3] = 0.f;
+            mx[n][0] = mx[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
+        for (; b < nb; b += DW) {
+            const int pgnn = page_at(b + 2 * DW);
+            const int kb = key0 + b * 16;
+            float x[NT][4];   // scores: [key g: columns 2t, 2t+1; key g + 8: the same]
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t w0[4] = {kr[0][j].x, kr[0][j].y, kr[0][j].z, kr[0][j].w};
+                const uint32_t w1[4] = {kr[1][j].x, kr[1][j].y, kr[1][j].z, kr[1][j].w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t a0 = half2_of(w0[w]), a1 = half2_of(w1[w]), a2 = half2_of(w0[w] >> 16), a3 = half2_of(w1[w] >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16816(x[n], a0, a1, a2, a3, qb[n][4 * j + w][0], qb[n][4 * j + w][1]);
+                }
+            }
+            const float kf = e8m0(ks);
+            if (b + DW < nb) load_k(b + DW, pgn);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (F32) x[n][i] += __shfl_xor_sync(0xffffffffu, x[n][i], 2);
+                    x[n][i] = x[n][i] * qs[n][i & 1] * kf;
+                }
+            if (kb + 16 > lim_all || pg < 0) {
+                if (pg < 0 && lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (pg < 0 || kb + g + 8 * (i >> 1) >= lim[n][i & 1]) x[n][i] = -INFINITY;
+            }
+            bool grew = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grew |= fmaxf(x[n][e], x[n][e + 2]) > mx[n][e] + 8.f;
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(x[n][e], x[n][e + 2]);
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        m = fmaxf(m, mx[n][e]);
+                        f[e] = m == -INFINITY ? 1.f : ex2(mx[n][e] - m);   // first keys: 0
+                        mx[n][e] = m;
+                        l[n][e] *= f[e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) o[n][i][z] *= f[z & 1];
+                }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float m = mx[n][i & 1];
+                    p[i] = ex2(x[n][i] - (m == -INFINITY ? 0.f : m - P_SHIFT));
+                    l[n][i & 1] += p[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t v = half2_bits(p[2 * i], p[2 * i + 1]);
+                    if (F32 && t >= 2) v = rest2(p[2 * i], p[2 * i + 1], v);
+                    pb[n][i] = transpose8(v);
+                }
+            }
+            const float vf = e8m0(vs);
+            {
+                const uint32_t v0[4] = {vr[0].x, vr[0].y, vr[0].z, vr[0].w}, v1[4] = {vr[1].x, vr[1].y, vr[1].z, vr[1].w};
+                const uint32_t v2[4] = {vr[2].x, vr[2].y, vr[2].z, vr[2].w}, v3[4] = {vr[3].x, vr[3].y, vr[3].z, vr[3].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int w = i >> 1, sel = i & 1 ? 0x7362 : 0x5140;
+                    const uint32_t lo = __byte_perm(v0[w], v1[w], sel), hi = __byte_perm(v2[w], v3[w], sel);
+                    const uint32_t a0 = half2_of(lo), a1 = half2_of(lo >> 16), a2 = half2_of(hi), a3 = half2_of(hi >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float z[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma16816(z, a0, a1, a2, a3, pb[n][0], pb[n][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][i][e] = fmaf(z[e], vf, o[n][i][e]);
+                    }
+                }
+            }
+            if (b + DW < nb) load_v(b + DW, pgn);
+            pg = pgn;
+            pgn = pgnn;
+        }
+
+        // ---- the four warps' outputs, joined
+        __syncthreads();   // the previous segment's readers are done
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = l[n][e];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                const int r = F32 ? 4 * n + 2 * t + e : 8 * n + 2 * t + e;
+                if (g == 0 && (!F32 || t < 2)) { sm_m[warp][r] = mx[n][e]; sm_l[warp][r] = v; }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *(float2*)&so[warp][8 * n + 2 * t + e][16 * g + 2 * i] = make_float2(o[n][i][e], o[n][i][e + 2]);
+        }
+        __syncthreads();
+        const bool whole = u == item0 && seg_end == item0 + nu;
+        const int ca = paged_cut_first(R, item0), cb = paged_cut_last(R, item0 + nu);   // where it is cut
+        float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == ca ? 1 : 0)) * SLOT;
+        TA* out = (TA*)a.out;
+        auto store = [&](int r, float v) {
+            const int rr = rg * RG + r, tok = rr / c.G;
+            out[(int64_t)(q.row0 + tok) * a.out_stride + (int64_t)(h * c.G + rr - tok * c.G) * HD + tid] = from_f<TA>(v);
+        };
+        for (int r = 0; r < rows; ++r) {
+            float m = sm_m[0][r];
+#pragma unroll
+            for (int w = 1; w < DW; ++w) m = fmaxf(m, sm_m[w][r]);
+            const float ms = m == -INFINITY ? 0.f : m;
+            float acc = 0.f, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < DW; ++w) {
+                const float f = ex2(sm_m[w][r] - ms);
+                const int col = F32 ? 8 * (r >> 2) + (r & 3) : r;
+                acc += f * (F32 ? so[w][col][tid] + so[w][col + 4][tid] : so[w][col][tid]);
+                sum += f * sm_l[w][r];
+            }
+            if (whole) {
+                store(r, sum != 0.f ? acc / sum : 0.f);
+            } else {
+                slot[r * HD + tid] = acc;
+                if (tid == 0) { slot[RG * HD + r] = m; slot[RG * HD + RG + r] = sum; }
+            }
+        }
+        if (!whole) {
+            __syncthreads();
+            if (tid == 0) {
+                __threadfence();
+                s_last = atomicAdd(&counters[ca], 1) == cb - ca;
+                if (s_last) counters[ca] = 0;
+                __threadfence();
+            }
+            __syncthreads();
+            if (s_last) {
+                // weights of the parts (the outputs' place is free: every thread is past the barriers above), then each
+                // warp adds up every fourth part
+                const int n = cb - ca + 1;
+                float* wt = so_all;
+                auto part = [&](int i) { return parts + (size_t)((ca + i) * 2 + (i == 0 ? 1 : 0)) * SLOT; };
+                const int sub = lane & 15;
+                for (int r = warp * 2 + (lane >> 4); r < (rows + 1) / 2 * 2; r += 2 * DW) {   // sixteen lanes a row
+                    float m = -INFINITY, sum = 0.f;
+                    if (r < rows)
+#pragma unroll 3
+                        for (int i = sub; i < n; i += 16) {
+                            const float v = __ldcg(part(i) + RG * HD + r), l = __ldcg(part(i) + RG * HD + RG + r);
+                            const float nm = fmaxf(m, v), ms = nm == -INFINITY ? 0.f : nm;
+                            sum = sum * ex2(m - ms) + l * ex2(v - ms);
+                            m = nm;
+                            wt[i * RG + r] = v;
+                        }
+#pragma unroll
+                    for (int z = 1; z < 16; z <<= 1) {
+                        const float v = __shfl_xor_sync(0xffffffffu, m, z), l = __shfl_xor_sync(0xffffffffu, sum, z);
+                        const float nm = fmaxf(m, v), ms = nm == -INFINITY ? 0.f : nm;
+                        sum = sum * ex2(m - ms) + l * ex2(v - ms);
+                        m = nm;
+                    }
+                    if (r < rows) {
+                        const float ms = m == -INFINITY ? 0.f : m;
+                        for (int i = sub; i < n; i += 16) wt[i * RG + r] = ex2(wt[i * RG + r] - ms);
+                        if (sub == 0) sm_l[0][r] = sum;
+                    }
+                }
+                __syncthreads();
+                float4 acc[RG];
+#pragma unroll
+                for (int r = 0; r < RG; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int i = warp; i < n; i += DW) {
+                    const float* p = part(i) + lane * 4;
+#pragma unroll
+                    for (int r = 0; r < RG; ++r)
+                        if (r < rows) {
+                            const float4 v = __ldcg((const float4*)(p + r * HD));
+                            const float f = wt[i * RG + r];
+                            acc[r].x = fmaf(v.x, f, acc[r].x); acc[r].y = fmaf(v.y, f, acc[r].y);
+                            acc[r].z = fmaf(v.z, f, acc[r].z); acc[r].w = fmaf(v.w, f, acc[r].w);
+                        }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < RG; ++r)
+                    if (r < rows) *(float4*)&so[warp][r][lane * 4] = acc[r];
+                __syncthreads();
+                for (int r = 0; r < rows; ++r) {
+                    const float sum = sm_l[0][r];
+                    const float v = so[0][r][tid] + so[1][r][tid] + so[2][r][tid] + so[3][r][tid];
+                    store(r, sum != 0.f ? v / sum : 0.f);
+                }
+            }
+        }
+        if (seg_end < item0 + nu || !next_item()) return;
+        u = item0;
+    }
+}
+
+template <typename TA, int NT>
+cudaError_t launch_t(const Paged8Attn& a, cudaStream_t st) {
+    const int grid = min(device_sm_count(), 160) * d8_ctas(NT);
+    return launch_pdl(paged8_decode_kernel<TA, NT>, grid, DW * 32, 0, st, a, grid);
+}
+
+}  // namespace
+
+// rows of a kv head that one sequence may have: two tiles of columns
+bool paged8_decode_takes(const Paged8Attn& a) { return (int64_t)a.max_q * a.c.G <= (a.act == Q3_BF16 ? 16 : 8); }
+
+cudaError_t launch_paged8_decode(const Paged8Attn& a, cudaStream_t st) {
+    const int rows = a.max_q * a.c.G;
+    if (a.act == Q3_BF16) return rows <= 8 ? launch_t<bf16, 1>(a, st) : launch_t<bf16, 2>(a, st);
+    return rows <= 4 ? launch_t<float, 1>(a, st) : launch_t<float, 2>(a, st);
+}
+
+}  // namespace q3
