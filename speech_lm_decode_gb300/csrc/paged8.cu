@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(A8_WARPS * 32, 2) paged8_append_kernel(const P
                 const __half2 f = __float2half2_rn(__uint_as_float((uint32_t)(127 - d) << 23));
                 for (int t = 0; t < p0 - block0; ++t) {
                     uint32_t* at = (uint32_t*)(codes + t * c.token_stride) + lane;
-                    const uint32_t v = *at;
-                    const uint32_t lo = half2_of(v), hi = half2_of(v >> 16);
+                    uint32_t lo, hi;
+                    half4_of(*at, lo, hi);
                     const float2 x = __half22float2(__hmul2(*(const __half2*)&lo, f)), z = __half22float2(__hmul2(*(const __half2*)&hi, f));
                     *at = codes_of(x.x, x.y) | codes_of(z.x, z.y) << 16;
                 }
@@ -266,8 +266,10 @@ __global__ void __launch_bounds__(256) paged8_read_kernel(PagedView c, int block
         float v[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 a = float2_of(words[j]), b = float2_of(words[j] >> 16);
-            v[4 * j] = a.x * f; v[4 * j + 1] = a.y * f; v[4 * j + 2] = b.x * f; v[4 * j + 3] = b.y * f;
+            float x[4];
+            float4_of(words[j], x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * j + e] = x[e] * f;
         }
         TO* dst = out + row * HD + piece * 16;
         if constexpr (sizeof(TO) == 2) {

@@ -43,14 +43,16 @@ constexpr int E8_MIN = 127 - 100, E8_MAX = 127 + 119;   // scales that append wr
 __device__ __forceinline__ float e8m0(uint32_t b) {
     return __uint_as_float(b == 255 ? 0x7fffffffu : b == 0 ? 0x00400000u : b << 23);
 }
-// two codes as f16 values (exact), the lower byte first
-__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+// codes as f16 values (exact), the lower byte first
+__device__ __forceinline__ void half4_of(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(codes));
 }
-__device__ __forceinline__ float2 float2_of(uint32_t codes) {
-    const uint32_t h = half2_of(codes);
-    return __half22float2(*(const __half2*)&h);
+__device__ __forceinline__ void float4_of(uint32_t codes, float (&v)[4]) {
+    uint32_t lo, hi;
+    half4_of(codes, lo, hi);
+    const float2 a = __half22float2(*(const __half2*)&lo), b = __half22float2(*(const __half2*)&hi);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 // two values as codes, the first in the lower byte: nearest, ties to even, at most 448 (NaN stays, infinities do not)
 __device__ __forceinline__ uint32_t codes_of(float a, float b) {

@@ -30,13 +30,14 @@ __global__ void __launch_bounds__(128) paged8_row_kernel(const Paged8Attn a) {
             const int64_t at = page * c.page_stride + hk * c.head_stride + slot * c.token_stride + lane * 4;
             const int64_t sc = (((int64_t)page * c.nkv + hk) << (c.page_shift - a.block_shift)) + (slot >> a.block_shift);
             const uint32_t kw = *(const uint32_t*)((const uint8_t*)c.k + at), vw = *(const uint32_t*)((const uint8_t*)c.v + at);
-            const float2 k0 = float2_of(kw), k1 = float2_of(kw >> 16), v0 = float2_of(vw), v1 = float2_of(vw >> 16);
-            const float score = warp_sum(x[0] * k0.x + x[1] * k0.y + x[2] * k1.x + x[3] * k1.y) * e8m0(a.ks[sc]);
+            float k[4], v[4];
+            float4_of(kw, k);
+            float4_of(vw, v);
+            const float score = warp_sum(x[0] * k[0] + x[1] * k[1] + x[2] * k[2] + x[3] * k[3]) * e8m0(a.ks[sc]);
             const float nm = fmaxf(m, score), f = expf(m - nm), p = expf(score - nm), fv = e8m0(a.vs[sc]);
             m = nm;
             l = l * f + p;
-            o[0] = o[0] * f + p * (v0.x * fv); o[1] = o[1] * f + p * (v0.y * fv);
-            o[2] = o[2] * f + p * (v1.x * fv); o[3] = o[3] * f + p * (v1.y * fv);
+            for (int j = 0; j < 4; ++j) o[j] = o[j] * f + p * (v[j] * fv);
         }
         TA* dst = (TA*)a.out + (int64_t)(q.row0 + tok) * a.out_stride + h * HD + lane * 4;
         for (int j = 0; j < 4; ++j) dst[j] = from_f<TA>(l != 0.f ? o[j] / l : 0.f);

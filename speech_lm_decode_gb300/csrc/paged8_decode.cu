@@ -32,17 +32,9 @@ namespace {
 
 constexpr int DW = 4;             // warps of a CTA
 constexpr int DU = 64;            // keys of a unit
-constexpr int d8_ctas(int nt) { return nt == 1 ? 4 : 3; }   // resident CTAs of an SM (registers)
+constexpr int d8_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of an SM (registers)
 constexpr float P_SHIFT = 7.f;    // weights are 2^7 times exp2 of score - maximum
 
-__device__ __forceinline__ uint4 ldg16(const void* p, bool ok) {
-    uint4 r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
-        "mov.b32 %3, 0;\n\t@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"((int)ok));
-    return r;
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -125,44 +117,59 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
         const int32_t* table = c.table + (int64_t)s * c.max_pages;
         const int pmask = (1 << c.page_shift) - 1;
         const int64_t head_off = (int64_t)h * c.head_stride;
-        auto page_at = [&](int b) -> int {   // page of block b; < 0: none
+        // A warp takes blocks w, w + 4 of every eight; lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9 of
+        // each.  Past the last key the last one stands in: its score is masked, and a weight of zero times its value is zero.
+        auto page_at = [&](int b) -> int {   // page of block b; -1: past the cut, -2: out of range
             if (b >= nb) return -1;
             const int pg = __ldg(table + ((key0 + b * 16) >> c.page_shift));
-            return (unsigned)pg < (unsigned)c.n_pages ? pg : -1;
+            return (unsigned)pg < (unsigned)c.n_pages ? pg : -2;
         };
-        // blocks of 16 keys: lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9
-        const uint8_t* kbase = (const uint8_t*)c.k + head_off + g * c.token_stride + t * 16;
-        const uint8_t* vbase = (const uint8_t*)c.v + head_off + 2 * t * c.token_stride + g * 16;
-        uint4 kr[2][2], vr[4];
-        uint32_t ks = 0, vs = 0;
+        const uint8_t* kbase = (const uint8_t*)c.k + head_off + t * 16;
+        const uint8_t* vbase = (const uint8_t*)c.v + head_off + g * 16;
+        const int64_t ts = c.token_stride;
+        uint4 kr[2][2][2], vr[2][4];
+        uint32_t ks[2] = {0, 0}, vs[2] = {0, 0};
         auto scale_at = [&](const uint8_t* sc, int kb, int pg) -> uint32_t {
-            return sc[(((int64_t)pg * c.nkv + h) << (c.page_shift - a.block_shift)) + ((kb & pmask) >> a.block_shift)];
+            return __ldg(sc + ((((int64_t)pg * c.nkv + h) << (c.page_shift - a.block_shift)) + ((kb & pmask) >> a.block_shift)));
         };
-        auto load_k = [&](int b, int pg) {
+        auto load_k = [&](int i, int b, int pg) {
+            if (pg < 0) return;
             const int kb = key0 + b * 16;
-            const uint8_t* p = kbase + (int64_t)max(pg, 0) * c.page_stride + (int64_t)(kb & pmask) * c.token_stride;
-            if (pg >= 0) ks = scale_at(a.ks, kb, pg);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool ok = pg >= 0 && kb + g + 8 * i < key1;
-                kr[i][0] = ldg16(p, ok);
-                kr[i][1] = ldg16(p + 64, ok);
-                p += 8 * c.token_stride;
+            const uint8_t* p = kbase + (int64_t)pg * c.page_stride + (kb & pmask) * ts;
+            ks[i] = scale_at(a.ks, kb, pg);
+            int64_t r0 = g * ts, r1 = r0 + 8 * ts;
+            if (kb + 16 > key1) {
+                r0 = min(g, key1 - 1 - kb) * ts;
+                r1 = min(g + 8, key1 - 1 - kb) * ts;
             }
+            kr[i][0][0] = ld_stream_u4(p + r0);
+            kr[i][0][1] = ld_stream_u4(p + r0 + 64);
+            kr[i][1][0] = ld_stream_u4(p + r1);
+            kr[i][1][1] = ld_stream_u4(p + r1 + 64);
         };
-        auto load_v = [&](int b, int pg) {
+        auto load_v = [&](int i, int b, int pg) {
+            if (pg < 0) return;
             const int kb = key0 + b * 16;
-            const uint8_t* p = vbase + (int64_t)max(pg, 0) * c.page_stride + (int64_t)(kb & pmask) * c.token_stride;
-            vs = pg >= 0 ? scale_at(a.vs, kb, pg) : 0;
+            const uint8_t* p = vbase + (int64_t)pg * c.page_stride + (kb & pmask) * ts;
+            vs[i] = scale_at(a.vs, kb, pg);
+            if (kb + 16 > key1) {
+                const int last = key1 - 1 - kb;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                vr[i] = ldg16(p, pg >= 0 && kb + 2 * t + (i & 1) + 8 * (i >> 1) < key1);
-                p += (i == 1 ? 7 : 1) * c.token_stride;
+                for (int j = 0; j < 4; ++j) vr[i][j] = ld_stream_u4(p + min(2 * t + (j & 1) + 8 * (j >> 1), last) * ts);
+            } else {
+                p += 2 * t * ts;
+                vr[i][0] = ld_stream_u4(p);
+                vr[i][1] = ld_stream_u4(p + ts);
+                vr[i][2] = ld_stream_u4(p + 8 * ts);
+                vr[i][3] = ld_stream_u4(p + 9 * ts);
             }
         };
         int b = warp;
-        int pg = page_at(b), pgn = page_at(b + DW);
-        if (b < nb) { load_k(b, pg); load_v(b, pg); }
+        int pg[2], pgn[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) { pg[i] = page_at(b + DW * i); pgn[i] = page_at(b + DW * (2 + i)); }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) { load_k(i, b + DW * i, pg[i]); load_v(i, b + DW * i, pg[i]); }
 
         // ---- query rows into B fragments, and the factors of the rows whose softmax the lane follows (columns 2t, 2t+1)
         uint32_t qb[NT][8][2];
@@ -224,52 +231,67 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             mx[n][0] = mx[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
         }
-        for (; b < nb; b += DW) {
-            const int pgnn = page_at(b + 2 * DW);
-            const int kb = key0 + b * 16;
-            float x[NT][4];   // scores: [key g: columns 2t, 2t+1; key g + 8: the same]
+        for (; b < nb; b += 2 * DW) {
+            int pgnn[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
+            for (int i = 0; i < 2; ++i) pgnn[i] = page_at(b + DW * (4 + i));
+            float x[2][NT][4];   // scores: [key g: columns 2t, 2t+1; key g + 8: the same]
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t w0[4] = {kr[0][j].x, kr[0][j].y, kr[0][j].z, kr[0][j].w};
-                const uint32_t w1[4] = {kr[1][j].x, kr[1][j].y, kr[1][j].z, kr[1][j].w};
+            for (int i = 0; i < 2; ++i) {
+                const int kb = key0 + (b + DW * i) * 16;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t a0 = half2_of(w0[w]), a1 = half2_of(w1[w]), a2 = half2_of(w0[w] >> 16), a3 = half2_of(w1[w] >> 16);
+                for (int n = 0; n < NT; ++n) x[i][n][0] = x[i][n][1] = x[i][n][2] = x[i][n][3] = 0.f;
+                if (pg[i] >= 0) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16816(x[n], a0, a1, a2, a3, qb[n][4 * j + w][0], qb[n][4 * j + w][1]);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t w0[4] = {kr[i][0][j].x, kr[i][0][j].y, kr[i][0][j].z, kr[i][0][j].w};
+                        const uint32_t w1[4] = {kr[i][1][j].x, kr[i][1][j].y, kr[i][1][j].z, kr[i][1][j].w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t a0, a1, a2, a3;
+                            half4_of(w0[w], a0, a2);
+                            half4_of(w1[w], a1, a3);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma16816(x[i][n], a0, a1, a2, a3, qb[n][4 * j + w][0], qb[n][4 * j + w][1]);
+                        }
+                    }
+                } else if (pg[i] == -2 && lane == 0 && a.err) {
+                    atomicOr(a.err, ERRB_BOUNDS);
                 }
-            }
-            const float kf = e8m0(ks);
-            if (b + DW < nb) load_k(b + DW, pgn);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (F32) x[n][i] += __shfl_xor_sync(0xffffffffu, x[n][i], 2);
-                    x[n][i] = x[n][i] * qs[n][i & 1] * kf;
-                }
-            if (kb + 16 > lim_all || pg < 0) {
-                if (pg < 0 && lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
+                const float kf = e8m0(ks[i]);
+                load_k(i, b + DW * (2 + i), pgn[i]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (pg < 0 || kb + g + 8 * (i >> 1) >= lim[n][i & 1]) x[n][i] = -INFINITY;
+                    for (int z = 0; z < 4; ++z) {
+                        if constexpr (F32) x[i][n][z] += __shfl_xor_sync(0xffffffffu, x[i][n][z], 2);
+                        x[i][n][z] = x[i][n][z] * qs[n][z & 1] * kf;
+                    }
+                if (kb + 16 > lim_all || pg[i] < 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            if (pg[i] < 0 || kb + g + 8 * (z >> 1) >= lim[n][z & 1]) x[i][n][z] = -INFINITY;
+                }
             }
             bool grew = false;
+            float top[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) grew |= fmaxf(x[n][e], x[n][e + 2]) > mx[n][e] + 8.f;
+                for (int e = 0; e < 2; ++e) {
+                    top[n][e] = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2]));
+                    grew |= top[n][e] > mx[n][e] + 8.f;
+                }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(x[n][e], x[n][e + 2]);
+                        float m = top[n][e];
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -284,44 +306,48 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
                         for (int z = 0; z < 4; ++z) o[n][i][z] *= f[z & 1];
                 }
             }
-            uint32_t pb[NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float p[4];
+            for (int i = 0; i < 2; ++i) {
+                uint32_t pb[NT][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float m = mx[n][i & 1];
-                    p[i] = ex2(x[n][i] - (m == -INFINITY ? 0.f : m - P_SHIFT));
-                    l[n][i & 1] += p[i];
-                }
+                for (int n = 0; n < NT; ++n) {
+                    float p[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t v = half2_bits(p[2 * i], p[2 * i + 1]);
-                    if (F32 && t >= 2) v = rest2(p[2 * i], p[2 * i + 1], v);
-                    pb[n][i] = transpose8(v);
-                }
-            }
-            const float vf = e8m0(vs);
-            {
-                const uint32_t v0[4] = {vr[0].x, vr[0].y, vr[0].z, vr[0].w}, v1[4] = {vr[1].x, vr[1].y, vr[1].z, vr[1].w};
-                const uint32_t v2[4] = {vr[2].x, vr[2].y, vr[2].z, vr[2].w}, v3[4] = {vr[3].x, vr[3].y, vr[3].z, vr[3].w};
+                    for (int z = 0; z < 4; ++z) {
+                        const float m = mx[n][z & 1];
+                        p[z] = ex2(x[i][n][z] - (m == -INFINITY ? 0.f : m - P_SHIFT));
+                        l[n][z & 1] += p[z];
+                    }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int w = i >> 1, sel = i & 1 ? 0x7362 : 0x5140;
-                    const uint32_t lo = __byte_perm(v0[w], v1[w], sel), hi = __byte_perm(v2[w], v3[w], sel);
-                    const uint32_t a0 = half2_of(lo), a1 = half2_of(lo >> 16), a2 = half2_of(hi), a3 = half2_of(hi >> 16);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float z[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma16816(z, a0, a1, a2, a3, pb[n][0], pb[n][1]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[n][i][e] = fmaf(z[e], vf, o[n][i][e]);
+                    for (int z = 0; z < 2; ++z) {
+                        uint32_t v = half2_bits(p[2 * z], p[2 * z + 1]);
+                        if (F32 && t >= 2) v = rest2(p[2 * z], p[2 * z + 1], v);
+                        pb[n][z] = transpose8(v);
                     }
                 }
+                if (pg[i] >= 0) {
+                    const float vf = e8m0(vs[i]);
+                    const uint32_t v0[4] = {vr[i][0].x, vr[i][0].y, vr[i][0].z, vr[i][0].w}, v1[4] = {vr[i][1].x, vr[i][1].y, vr[i][1].z, vr[i][1].w};
+                    const uint32_t v2[4] = {vr[i][2].x, vr[i][2].y, vr[i][2].z, vr[i][2].w}, v3[4] = {vr[i][3].x, vr[i][3].y, vr[i][3].z, vr[i][3].w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int w = k >> 1, sel = k & 1 ? 0x7362 : 0x5140;
+                        uint32_t a0, a1, a2, a3;
+                        half4_of(__byte_perm(v0[w], v1[w], sel), a0, a1);
+                        half4_of(__byte_perm(v2[w], v3[w], sel), a2, a3);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float z[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma16816(z, a0, a1, a2, a3, pb[n][0], pb[n][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[n][k][e] = fmaf(z[e], vf, o[n][k][e]);
+                        }
+                    }
+                }
+                load_v(i, b + DW * (2 + i), pgn[i]);
+                pg[i] = pgn[i];
+                pgn[i] = pgnn[i];
             }
-            if (b + DW < nb) load_v(b + DW, pgn);
-            pg = pgn;
-            pgn = pgnn;
         }
 
         // ---- the four warps' outputs, joined
