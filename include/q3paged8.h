@@ -32,7 +32,7 @@ extern "C" {
 
 typedef struct {
     q3paged_cache cache;    /* kv_dtype Q3_E4M3, act_dtype Q3_F32 or Q3_BF16; pages are bytes
-                               (strides in multiples of 16)                                  */
+                               (strides in multiples of 16; page_size * token_stride below 2^31) */
     int scale_block;        /* positions of a block: a power of two, 16..page_size           */
     uint8_t* k_scale;       /* [n_pages][n_kv_heads][page_size / scale_block], packed        */
     uint8_t* v_scale;

@@ -306,6 +306,8 @@ int view8_of(const q3paged8_cache* c8, PagedView* v, int* block_shift, bool pool
     for (int64_t s : {v->token_stride, v->head_stride, v->page_stride})
         if (s < HD || s % 16 || s >= (int64_t)1 << 40)
             return paged_fail(Q3_ERR_ARG, "strides must be at least 128 bytes, below 2^40, in multiples of 16");
+    if (v->token_stride * c->page_size > 0x7fffffff)
+        return paged_fail(Q3_ERR_ARG, "the positions of a page must lie within 2^31 bytes");
     if (!aligned16(v->k) || !aligned16(v->v)) return paged_fail(Q3_ERR_ARG, "pages must start on 16-byte boundaries");
     return Q3_OK;
 }

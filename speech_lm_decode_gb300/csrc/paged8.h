@@ -40,9 +40,7 @@ cudaError_t launch_paged8_decode(const Paged8Attn& a, cudaStream_t st);
 constexpr int E8_MIN = 127 - 100, E8_MAX = 127 + 119;   // scales that append writes
 
 // 2^(b - 127); 255: NaN
-__device__ __forceinline__ float e8m0(uint32_t b) {
-    return __uint_as_float(b == 255 ? 0x7fffffffu : b == 0 ? 0x00400000u : b << 23);
-}
+__device__ __forceinline__ float e8m0(uint32_t b) { return __uint_as_float(max((b << 23) + ((b + 1) >> 8), 0x00400000u)); }
 // codes as f16 values (exact), the lower byte first
 __device__ __forceinline__ void half4_of(uint32_t codes, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"

@@ -32,19 +32,32 @@ namespace {
 
 constexpr int DW = 4;             // warps of a CTA
 constexpr int DU = 64;            // keys of a unit
-constexpr int d8_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of an SM (registers)
+constexpr int d8_ctas(int nt) { return nt == 1 ? 4 : 3; }   // resident CTAs of an SM (registers)
+constexpr int d8_stages(int nt) { return nt == 1 ? 3 : 4; } // blocks of a warp's ring
+constexpr int D8_STAGE = 2 * 16 * HD;                       // bytes of one: K and V of 16 keys
 constexpr float P_SHIFT = 7.f;    // weights are 2^7 times exp2 of score - maximum
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// without a sum to add to
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -72,9 +85,18 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
     constexpr int RG = F32 ? 4 * NT : 8 * NT;   // query rows of an item
     const PagedView& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    constexpr int SO = DW * 8 * NT * (HD + 4), WT = 160 * d8_ctas(NT) * RG;
-    __shared__ __align__(16) float so_all[SO > WT ? SO : WT];   // outputs; the weights of an item's parts
-    float (*so)[8 * NT][HD + 4] = (float (*)[8 * NT][HD + 4])so_all;
+    constexpr int S = d8_stages(NT);
+    // The warps' rings; between two segments the outputs and the weights of an item's parts.  A row of 16 keys' codes is 128
+    // bytes; its 16-byte pieces are moved about so that a warp's reads of fragments meet no bank twice.
+    extern __shared__ __align__(128) unsigned char raw[];
+    static_assert(8 * NT * (HD + 4) * 4 <= S * D8_STAGE && 160 * d8_ctas(NT) * RG * 4 <= DW * S * D8_STAGE, "what lies over the rings");
+    float* so_all = (float*)raw;
+    float (*so)[8 * NT][HD + 4] = (float (*)[8 * NT][HD + 4])raw;
+    unsigned char* ring = raw + warp * S * D8_STAGE;
+    const uint32_t ring32 = (uint32_t)__cvta_generic_to_shared(ring);
+    const uint32_t kdst = ring32 + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3 & 1) << 2) << 4);
+    const uint32_t vdst = ring32 + 2048 + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 4) << 1) << 4);
+    const int kread = g * 128 + (t << 4), kflip = (g & 1) << 6, vread = 2048 + 2 * t * 128 + ((g ^ t << 1) << 4);
     __shared__ float sm_m[DW][RG], sm_l[DW][RG];
     __shared__ int s_last;
 
@@ -117,59 +139,45 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
         const int32_t* table = c.table + (int64_t)s * c.max_pages;
         const int pmask = (1 << c.page_shift) - 1;
         const int64_t head_off = (int64_t)h * c.head_stride;
-        // A warp takes blocks w, w + 4 of every eight; lane (g, t) holds K rows g, g + 8 and V rows 2t, 2t+1, 2t+8, 2t+9 of
-        // each.  Past the last key the last one stands in: its score is masked, and a weight of zero times its value is zero.
+        // A warp takes every fourth block of 16 keys.  Their codes come through its own ring in shared memory, S - 1 blocks
+        // ahead; keys past the last one read as zeros (a weight of zero times a value of zero).
         auto page_at = [&](int b) -> int {   // page of block b; -1: past the cut, -2: out of range
             if (b >= nb) return -1;
             const int pg = __ldg(table + ((key0 + b * 16) >> c.page_shift));
             return (unsigned)pg < (unsigned)c.n_pages ? pg : -2;
         };
-        const uint8_t* kbase = (const uint8_t*)c.k + head_off + t * 16;
-        const uint8_t* vbase = (const uint8_t*)c.v + head_off + g * 16;
-        const int64_t ts = c.token_stride;
-        uint4 kr[2][2][2], vr[2][4];
-        uint32_t ks[2] = {0, 0}, vs[2] = {0, 0};
-        auto scale_at = [&](const uint8_t* sc, int kb, int pg) -> uint32_t {
-            return __ldg(sc + ((((int64_t)pg * c.nkv + h) << (c.page_shift - a.block_shift)) + ((kb & pmask) >> a.block_shift)));
-        };
-        auto load_k = [&](int i, int b, int pg) {
-            if (pg < 0) return;
-            const int kb = key0 + b * 16;
-            const uint8_t* p = kbase + (int64_t)pg * c.page_stride + (kb & pmask) * ts;
-            ks[i] = scale_at(a.ks, kb, pg);
-            int64_t r0 = g * ts, r1 = r0 + 8 * ts;
-            if (kb + 16 > key1) {
-                r0 = min(g, key1 - 1 - kb) * ts;
-                r1 = min(g + 8, key1 - 1 - kb) * ts;
+        // (a page's positions lie within 2^31 bytes, the caller checks, and its scales within 2^31 of the pool's first)
+        const int ts = (int)c.token_stride, lr = lane >> 3, per_shift = c.page_shift - a.block_shift;
+        const int64_t lane_off = head_off + lr * ts + (lane & 7) * 16;
+        const uint8_t *kbase = (const uint8_t*)c.k + lane_off, *vbase = (const uint8_t*)c.v + lane_off;
+        auto issue = [&](int b, int pg, int slot) {
+            if (b < nb) {
+                const int kb = key0 + b * 16, left = pg < 0 ? 0 : key1 - kb - lr;
+                const int64_t off = max(pg, 0) * c.page_stride + (kb & pmask) * ts;
+                const uint32_t kd = kdst + slot * D8_STAGE, vd = vdst + slot * D8_STAGE;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    copy16(kd + i * 512, kbase + off + 4 * i * ts, left > 4 * i);
+                    copy16((vd ^ (i & 1) << 6) + i * 512, vbase + off + 4 * i * ts, left > 4 * i);
+                }
             }
-            kr[i][0][0] = ld_stream_u4(p + r0);
-            kr[i][0][1] = ld_stream_u4(p + r0 + 64);
-            kr[i][1][0] = ld_stream_u4(p + r1);
-            kr[i][1][1] = ld_stream_u4(p + r1 + 64);
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto load_v = [&](int i, int b, int pg) {
+        auto scales = [&](int b, int pg, uint32_t& k, uint32_t& v) {
+            k = v = 127;
             if (pg < 0) return;
-            const int kb = key0 + b * 16;
-            const uint8_t* p = vbase + (int64_t)pg * c.page_stride + (kb & pmask) * ts;
-            vs[i] = scale_at(a.vs, kb, pg);
-            if (kb + 16 > key1) {
-                const int last = key1 - 1 - kb;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) vr[i][j] = ld_stream_u4(p + min(2 * t + (j & 1) + 8 * (j >> 1), last) * ts);
-            } else {
-                p += 2 * t * ts;
-                vr[i][0] = ld_stream_u4(p);
-                vr[i][1] = ld_stream_u4(p + ts);
-                vr[i][2] = ld_stream_u4(p + 8 * ts);
-                vr[i][3] = ld_stream_u4(p + 9 * ts);
-            }
+            const int i = ((pg * c.nkv + h) << per_shift) + (((key0 + b * 16) & pmask) >> a.block_shift);
+            k = __ldg(a.ks + i);
+            v = __ldg(a.vs + i);
         };
-        int b = warp;
-        int pg[2], pgn[2];
+        int b = warp, slot = 0;
+        int pg[S + 1];     // pages of this block and the next ones
+        uint32_t ks, vs;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) { pg[i] = page_at(b + DW * i); pgn[i] = page_at(b + DW * (2 + i)); }
+        for (int i = 0; i <= S; ++i) pg[i] = page_at(b + DW * i);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) { load_k(i, b + DW * i, pg[i]); load_v(i, b + DW * i, pg[i]); }
+        for (int i = 0; i < S - 1; ++i) issue(b + DW * i, pg[i], i);
+        scales(b, pg[0], ks, vs);
 
         // ---- query rows into B fragments, and the factors of the rows whose softmax the lane follows (columns 2t, 2t+1)
         uint32_t qb[NT][8][2];
@@ -231,67 +239,68 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             mx[n][0] = mx[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
         }
-        for (; b < nb; b += 2 * DW) {
-            int pgnn[2];
+        for (; b < nb; b += DW) {
+            const int next = page_at(b + DW * (S + 1));
+            const int kb = key0 + b * 16;
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            __syncwarp();
+            issue(b + DW * (S - 1), pg[S - 1], slot == 0 ? S - 1 : slot - 1);
+            uint32_t ksn, vsn;
+            scales(b + DW, pg[1], ksn, vsn);
+            const unsigned char* st = ring + slot * D8_STAGE;
+            float x[NT][4];   // scores: [key g: columns 2t, 2t+1; key g + 8: the same]
+            {
+                float y[NT][4];   // of every other step, so that a product does not wait for the one before it
 #pragma unroll
-            for (int i = 0; i < 2; ++i) pgnn[i] = page_at(b + DW * (4 + i));
-            float x[2][NT][4];   // scores: [key g: columns 2t, 2t+1; key g + 8: the same]
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 r0 = *(const uint4*)(st + kread + (j << 6 ^ kflip)), r1 = *(const uint4*)(st + kread + 1024 + (j << 6 ^ kflip));
+                    const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int kb = key0 + (b + DW * i) * 16;
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t a0, a1, a2, a3;
+                        half4_of(w0[w], a0, a2);
+                        half4_of(w1[w], a1, a3);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) x[i][n][0] = x[i][n][1] = x[i][n][2] = x[i][n][3] = 0.f;
-                if (pg[i] >= 0) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t w0[4] = {kr[i][0][j].x, kr[i][0][j].y, kr[i][0][j].z, kr[i][0][j].w};
-                        const uint32_t w1[4] = {kr[i][1][j].x, kr[i][1][j].y, kr[i][1][j].z, kr[i][1][j].w};
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            uint32_t a0, a1, a2, a3;
-                            half4_of(w0[w], a0, a2);
-                            half4_of(w1[w], a1, a3);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma16816(x[i][n], a0, a1, a2, a3, qb[n][4 * j + w][0], qb[n][4 * j + w][1]);
+                        for (int n = 0; n < NT; ++n) {
+                            float (&z)[4] = w & 1 ? y[n] : x[n];
+                            if (j == 0 && w < 2) mma16816_first(z, a0, a1, a2, a3, qb[n][4 * j + w][0], qb[n][4 * j + w][1]);
+                            else mma16816(z, a0, a1, a2, a3, qb[n][4 * j + w][0], qb[n][4 * j + w][1]);
                         }
                     }
-                } else if (pg[i] == -2 && lane == 0 && a.err) {
-                    atomicOr(a.err, ERRB_BOUNDS);
                 }
-                const float kf = e8m0(ks[i]);
-                load_k(i, b + DW * (2 + i), pgn[i]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        if constexpr (F32) x[i][n][z] += __shfl_xor_sync(0xffffffffu, x[i][n][z], 2);
-                        x[i][n][z] = x[i][n][z] * qs[n][z & 1] * kf;
-                    }
-                if (kb + 16 > lim_all || pg[i] < 0) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            if (pg[i] < 0 || kb + g + 8 * (z >> 1) >= lim[n][z & 1]) x[i][n][z] = -INFINITY;
-                }
+                    for (int z = 0; z < 4; ++z) x[n][z] += y[n][z];
             }
-            bool grew = false;
-            float top[NT][2];
+            const float kf = e8m0(ks);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    top[n][e] = fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2]));
-                    grew |= top[n][e] > mx[n][e] + 8.f;
+                for (int z = 0; z < 4; ++z) {
+                    if constexpr (F32) x[n][z] += __shfl_xor_sync(0xffffffffu, x[n][z], 2);
+                    x[n][z] = x[n][z] * qs[n][z & 1] * kf;
                 }
+            if (kb + 16 > lim_all || pg[0] < 0) {
+                if (pg[0] < 0 && lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        if (pg[0] < 0 || kb + g + 8 * (z >> 1) >= lim[n][z & 1]) x[n][z] = -INFINITY;
+            }
+            bool grew = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grew |= fmaxf(x[n][e], x[n][e + 2]) > mx[n][e] + 8.f;
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = top[n][e];
+                        float m = fmaxf(x[n][e], x[n][e + 2]);
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -306,52 +315,52 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
                         for (int z = 0; z < 4; ++z) o[n][i][z] *= f[z & 1];
                 }
             }
+            uint32_t pb[NT][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t pb[NT][2];
+            for (int n = 0; n < NT; ++n) {
+                float p[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float m = mx[n][z & 1];
+                    p[z] = ex2(x[n][z] - (m == -INFINITY ? 0.f : m - P_SHIFT));
+                    l[n][z & 1] += p[z];
+                }
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    uint32_t v = half2_bits(p[2 * z], p[2 * z + 1]);
+                    if (F32 && t >= 2) v = rest2(p[2 * z], p[2 * z + 1], v);
+                    pb[n][z] = transpose8(v);
+                }
+            }
+            const float vf = e8m0(vs);
+            const uint4 r0 = *(const uint4*)(st + vread), r1 = *(const uint4*)(st + vread + 128);
+            const uint4 r2 = *(const uint4*)(st + vread + 1024), r3 = *(const uint4*)(st + vread + 1152);
+            const uint32_t v0[4] = {r0.x, r0.y, r0.z, r0.w}, v1[4] = {r1.x, r1.y, r1.z, r1.w};
+            const uint32_t v2[4] = {r2.x, r2.y, r2.z, r2.w}, v3[4] = {r3.x, r3.y, r3.z, r3.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int w = k >> 1, sel = k & 1 ? 0x7362 : 0x5140;
+                uint32_t a0, a1, a2, a3;
+                half4_of(__byte_perm(v0[w], v1[w], sel), a0, a1);
+                half4_of(__byte_perm(v2[w], v3[w], sel), a2, a3);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float p[4];
+                    float z[4];
+                    mma16816_first(z, a0, a1, a2, a3, pb[n][0], pb[n][1]);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const float m = mx[n][z & 1];
-                        p[z] = ex2(x[i][n][z] - (m == -INFINITY ? 0.f : m - P_SHIFT));
-                        l[n][z & 1] += p[z];
-                    }
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        uint32_t v = half2_bits(p[2 * z], p[2 * z + 1]);
-                        if (F32 && t >= 2) v = rest2(p[2 * z], p[2 * z + 1], v);
-                        pb[n][z] = transpose8(v);
-                    }
+                    for (int e = 0; e < 4; ++e) o[n][k][e] = fmaf(z[e], vf, o[n][k][e]);
                 }
-                if (pg[i] >= 0) {
-                    const float vf = e8m0(vs[i]);
-                    const uint32_t v0[4] = {vr[i][0].x, vr[i][0].y, vr[i][0].z, vr[i][0].w}, v1[4] = {vr[i][1].x, vr[i][1].y, vr[i][1].z, vr[i][1].w};
-                    const uint32_t v2[4] = {vr[i][2].x, vr[i][2].y, vr[i][2].z, vr[i][2].w}, v3[4] = {vr[i][3].x, vr[i][3].y, vr[i][3].z, vr[i][3].w};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int w = k >> 1, sel = k & 1 ? 0x7362 : 0x5140;
-                        uint32_t a0, a1, a2, a3;
-                        half4_of(__byte_perm(v0[w], v1[w], sel), a0, a1);
-                        half4_of(__byte_perm(v2[w], v3[w], sel), a2, a3);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float z[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma16816(z, a0, a1, a2, a3, pb[n][0], pb[n][1]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[n][k][e] = fmaf(z[e], vf, o[n][k][e]);
-                        }
-                    }
-                }
-                load_v(i, b + DW * (2 + i), pgn[i]);
-                pg[i] = pgn[i];
-                pgn[i] = pgnn[i];
             }
+            ks = ksn;
+            vs = vsn;
+            slot = slot + 1 == S ? 0 : slot + 1;
+#pragma unroll
+            for (int i = 0; i < S; ++i) pg[i] = pg[i + 1];
+            pg[S] = next;
         }
 
         // ---- the four warps' outputs, joined
-        __syncthreads();   // the previous segment's readers are done
+        __syncthreads();   // every warp is done with its ring
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
         __syncthreads();
         const bool whole = u == item0 && seg_end == item0 + nu;
         const int ca = paged_cut_first(R, item0), cb = paged_cut_last(R, item0 + nu);   // where it is cut
-        float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == ca ? 1 : 0)) * SLOT;
+        float* mine = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == ca ? 1 : 0)) * SLOT;
         TA* out = (TA*)a.out;
         auto store = [&](int r, float v) {
             const int rr = rg * RG + r, tok = rr / c.G;
@@ -394,8 +403,8 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             if (whole) {
                 store(r, sum != 0.f ? acc / sum : 0.f);
             } else {
-                slot[r * HD + tid] = acc;
-                if (tid == 0) { slot[RG * HD + r] = m; slot[RG * HD + RG + r] = sum; }
+                mine[r * HD + tid] = acc;
+                if (tid == 0) { mine[RG * HD + r] = m; mine[RG * HD + RG + r] = sum; }
             }
         }
         if (!whole) {
@@ -468,13 +477,18 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
         }
         if (seg_end < item0 + nu || !next_item()) return;
         u = item0;
+        __syncthreads();   // the rings are free
     }
 }
 
 template <typename TA, int NT>
 cudaError_t launch_t(const Paged8Attn& a, cudaStream_t st) {
     const int grid = min(device_sm_count(), 160) * d8_ctas(NT);
-    return launch_pdl(paged8_decode_kernel<TA, NT>, grid, DW * 32, 0, st, a, grid);
+    constexpr int smem = DW * d8_stages(NT) * D8_STAGE;
+    // a per-device attribute: set on every call (a host-side table lookup)
+    const cudaError_t e = cudaFuncSetAttribute(paged8_decode_kernel<TA, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged8_decode_kernel<TA, NT>, grid, DW * 32, smem, st, a, grid);
 }
 
 }  // namespace

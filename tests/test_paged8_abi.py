@@ -78,7 +78,7 @@ def test_arguments_that_are_refused():
     for kw in (dict(n=-1), dict(pages=None), dict(dt=2), dict(k=4100), dict(v=4104)):
         assert read(**kw) == ERR_ARG, kw
     for kw in (dict(k_pages=None), dict(v_pages=4100), dict(page_table=None), dict(token_stride=64), dict(head_stride=129),
-               dict(page_stride=-16), dict(page_stride=1 << 60), dict(k_scale=None), dict(v_scale=None)):
+               dict(page_stride=-16), dict(page_stride=1 << 60), dict(token_stride=1 << 26), dict(k_scale=None), dict(v_scale=None)):
         c = cache(q3, **kw)
         assert append(c) == ERR_ARG and attend(c) == ERR_ARG and read(c) == ERR_ARG, kw
     assert append(n=0) == 0 and append(max_q=0) == 0 and attend(n=0) == 0 and attend(max_q=0) == 0
