@@ -31,8 +31,8 @@ namespace q3 {
 namespace {
 
 constexpr int DW = 4;             // warps of a CTA
-constexpr int DU = 64;            // keys of a unit
-constexpr int d8_ctas(int nt) { return nt == 1 ? 4 : 3; }   // resident CTAs of an SM (registers)
+constexpr int DU = 16 * DW;       // keys of a unit
+constexpr int d8_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of an SM (registers)
 constexpr int d8_stages(int nt) { return nt == 1 ? 3 : 4; } // blocks of a warp's ring
 constexpr int D8_STAGE = 2 * 16 * HD;                       // bytes of one: K and V of 16 keys
 constexpr float P_SHIFT = 7.f;    // weights are 2^7 times exp2 of score - maximum
@@ -68,6 +68,8 @@ __device__ __forceinline__ uint32_t rest2(float x0, float x1, uint32_t h) {
     const float2 f = __half22float2(*(const __half2*)&h);
     return half2_bits(x0 - f.x, x1 - f.y);
 }
+// 2^e, e <= 0; below 2^-126: zero
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)max(127 + e, 0) << 23); }
 // transposes an 8 x 8 matrix of 16-bit values (lane (g, t): row g, columns 2t and 2t+1)
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
@@ -139,45 +141,39 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
         const int32_t* table = c.table + (int64_t)s * c.max_pages;
         const int pmask = (1 << c.page_shift) - 1;
         const int64_t head_off = (int64_t)h * c.head_stride;
-        // A warp takes every fourth block of 16 keys.  Their codes come through its own ring in shared memory, S - 1 blocks
+        // A warp takes every DW-th block of 16 keys.  Their codes come through its own ring in shared memory, S - 1 blocks
         // ahead; keys past the last one read as zeros (a weight of zero times a value of zero).
-        auto page_at = [&](int b) -> int {   // page of block b; -1: past the cut, -2: out of range
-            if (b >= nb) return -1;
-            const int pg = __ldg(table + ((key0 + b * 16) >> c.page_shift));
-            return (unsigned)pg < (unsigned)c.n_pages ? pg : -2;
-        };
+        auto page_at = [&](int b) -> int { return b < nb ? __ldg(table + ((key0 + b * 16) >> c.page_shift)) : 0; };
         // (a page's positions lie within 2^31 bytes, the caller checks, and its scales within 2^31 of the pool's first)
         const int ts = (int)c.token_stride, lr = lane >> 3, per_shift = c.page_shift - a.block_shift;
         const int64_t lane_off = head_off + lr * ts + (lane & 7) * 16;
         const uint8_t *kbase = (const uint8_t*)c.k + lane_off, *vbase = (const uint8_t*)c.v + lane_off;
-        auto issue = [&](int b, int pg, int slot) {
+        // place i of the ring: the page of its block (-1: out of range), its scales, and the page of its next block
+        int pg[S], ahead[S] = {};
+        uint32_t ks[S], vs[S];
+        auto issue = [&](int i, int b) {
             if (b < nb) {
-                const int kb = key0 + b * 16, left = pg < 0 ? 0 : key1 - kb - lr;
-                const int64_t off = max(pg, 0) * c.page_stride + (kb & pmask) * ts;
-                const uint32_t kd = kdst + slot * D8_STAGE, vd = vdst + slot * D8_STAGE;
+                const bool there = (unsigned)ahead[i] < (unsigned)c.n_pages;
+                const int kb = key0 + b * 16, slot = kb & pmask, page = there ? ahead[i] : 0, left = there ? key1 - kb - lr : 0;
+                pg[i] = there ? page : -1;
+                ahead[i] = page_at(b + DW * S);
+                const int64_t off = page * c.page_stride + slot * ts;
+                const uint32_t kd = kdst + i * D8_STAGE, vd = vdst + i * D8_STAGE;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    copy16(kd + i * 512, kbase + off + 4 * i * ts, left > 4 * i);
-                    copy16((vd ^ (i & 1) << 6) + i * 512, vbase + off + 4 * i * ts, left > 4 * i);
+                for (int j = 0; j < 4; ++j) {
+                    copy16(kd + j * 512, kbase + off + 4 * j * ts, left > 4 * j);
+                    copy16((vd ^ (j & 1) << 6) + j * 512, vbase + off + 4 * j * ts, left > 4 * j);
                 }
+                const int sc = ((page * c.nkv + h) << per_shift) + (slot >> a.block_shift);
+                ks[i] = vs[i] = 0;
+                if (there) { ks[i] = __ldg(a.ks + sc); vs[i] = __ldg(a.vs + sc); }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto scales = [&](int b, int pg, uint32_t& k, uint32_t& v) {
-            k = v = 127;
-            if (pg < 0) return;
-            const int i = ((pg * c.nkv + h) << per_shift) + (((key0 + b * 16) & pmask) >> a.block_shift);
-            k = __ldg(a.ks + i);
-            v = __ldg(a.vs + i);
-        };
-        int b = warp, slot = 0;
-        int pg[S + 1];     // pages of this block and the next ones
-        uint32_t ks, vs;
 #pragma unroll
-        for (int i = 0; i <= S; ++i) pg[i] = page_at(b + DW * i);
+        for (int i = 0; i < S; ++i) ahead[i] = page_at(warp + DW * i);
 #pragma unroll
-        for (int i = 0; i < S - 1; ++i) issue(b + DW * i, pg[i], i);
-        scales(b, pg[0], ks, vs);
+        for (int i = 0; i < S - 1; ++i) issue(i, warp + DW * i);
 
         // ---- query rows into B fragments, and the factors of the rows whose softmax the lane follows (columns 2t, 2t+1)
         uint32_t qb[NT][8][2];
@@ -231,7 +227,8 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             }
         const int lim_all = min(q.ctx - q.n_new + rg * RG / c.G + 1, key1);   // keys that every row sees
 
-        float o[NT][8][4], mx[NT][2], l[NT][2];
+        float o[NT][8][4], mx[NT][2], l[NT][2];   // o: in units of the largest scale of values so far, 2^(vcur - 127)
+        int vcur = 0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -239,15 +236,15 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             mx[n][0] = mx[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
         }
-        for (; b < nb; b += DW) {
-            const int next = page_at(b + DW * (S + 1));
-            const int kb = key0 + b * 16;
+        for (int b0 = warp; b0 < nb; b0 += DW * S) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            const int b = b0 + DW * i, kb = key0 + b * 16;
+            if (b >= nb) break;
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-            __syncwarp();
-            issue(b + DW * (S - 1), pg[S - 1], slot == 0 ? S - 1 : slot - 1);
-            uint32_t ksn, vsn;
-            scales(b + DW, pg[1], ksn, vsn);
-            const unsigned char* st = ring + slot * D8_STAGE;
+            __syncwarp();      // the block is there, and every lane is done with the one before it
+            issue((i + S - 1) % S, b + DW * (S - 1));
+            const unsigned char* st = ring + i * D8_STAGE;
             float x[NT][4];   // scores: [key g: columns 2t, 2t+1; key g + 8: the same]
             {
                 float y[NT][4];   // of every other step, so that a product does not wait for the one before it
@@ -273,7 +270,7 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
 #pragma unroll
                     for (int z = 0; z < 4; ++z) x[n][z] += y[n][z];
             }
-            const float kf = e8m0(ks);
+            const float kf = e8m0(ks[i]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -281,13 +278,13 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
                     if constexpr (F32) x[n][z] += __shfl_xor_sync(0xffffffffu, x[n][z], 2);
                     x[n][z] = x[n][z] * qs[n][z & 1] * kf;
                 }
-            if (kb + 16 > lim_all || pg[0] < 0) {
-                if (pg[0] < 0 && lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
+            if (kb + 16 > lim_all || pg[i] < 0) {
+                if (pg[i] < 0 && lane == 0 && a.err) atomicOr(a.err, ERRB_BOUNDS);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
-                        if (pg[0] < 0 || kb + g + 8 * (z >> 1) >= lim[n][z & 1]) x[n][z] = -INFINITY;
+                        if (pg[i] < 0 || kb + g + 8 * (z >> 1) >= lim[n][z & 1]) x[n][z] = -INFINITY;
             }
             bool grew = false;
 #pragma unroll
@@ -310,9 +307,9 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
                         l[n][e] *= f[e];
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int k = 0; k < 8; ++k)
 #pragma unroll
-                        for (int z = 0; z < 4; ++z) o[n][i][z] *= f[z & 1];
+                        for (int z = 0; z < 4; ++z) o[n][k][z] *= f[z & 1];
                 }
             }
             uint32_t pb[NT][2];
@@ -332,32 +329,44 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
                     pb[n][z] = transpose8(v);
                 }
             }
-            const float vf = e8m0(vs);
             const uint4 r0 = *(const uint4*)(st + vread), r1 = *(const uint4*)(st + vread + 128);
             const uint4 r2 = *(const uint4*)(st + vread + 1024), r3 = *(const uint4*)(st + vread + 1152);
             const uint32_t v0[4] = {r0.x, r0.y, r0.z, r0.w}, v1[4] = {r1.x, r1.y, r1.z, r1.w};
             const uint32_t v2[4] = {r2.x, r2.y, r2.z, r2.w}, v3[4] = {r3.x, r3.y, r3.z, r3.w};
+            auto outputs = [&](auto f) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int w = k >> 1, sel = k & 1 ? 0x7362 : 0x5140;
-                uint32_t a0, a1, a2, a3;
-                half4_of(__byte_perm(v0[w], v1[w], sel), a0, a1);
-                half4_of(__byte_perm(v2[w], v3[w], sel), a2, a3);
+                for (int k = 0; k < 8; ++k) {
+                    const int w = k >> 1, sel = k & 1 ? 0x7362 : 0x5140;
+                    uint32_t a0, a1, a2, a3;
+                    half4_of(__byte_perm(v0[w], v1[w], sel), a0, a1);
+                    half4_of(__byte_perm(v2[w], v3[w], sel), a2, a3);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float z[4];
-                    mma16816_first(z, a0, a1, a2, a3, pb[n][0], pb[n][1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][k][e] = fmaf(z[e], vf, o[n][k][e]);
+                    for (int n = 0; n < NT; ++n) f(o[n][k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
                 }
-            }
-            ks = ksn;
-            vs = vsn;
-            slot = slot + 1 == S ? 0 : slot + 1;
+            };
+            const int vb = (int)vs[i];
+            if (vb > vcur) {
+                const float f = two_to(vcur - vb);
 #pragma unroll
-            for (int i = 0; i < S; ++i) pg[i] = pg[i + 1];
-            pg[S] = next;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[n][k >> 2][k & 3] *= f;
+                vcur = vb;
+            }
+            if (!F32 && vb == vcur) {
+                outputs(mma16816);
+            } else {
+                const float f = two_to(vb - vcur);
+                outputs([&](float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+                    float z[4];
+                    mma16816_first(z, a0, a1, a2, a3, b0, b1);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e] = fmaf(z[e], f, d[e]);
+                });
+            }
         }
+        }
+        const float of = e8m0(vcur);
 
         // ---- the four warps' outputs, joined
         __syncthreads();   // every warp is done with its ring
@@ -376,18 +385,19 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    *(float2*)&so[warp][8 * n + 2 * t + e][16 * g + 2 * i] = make_float2(o[n][i][e], o[n][i][e + 2]);
+                    *(float2*)&so[warp][8 * n + 2 * t + e][16 * g + 2 * i] = make_float2(o[n][i][e] * of, o[n][i][e + 2] * of);
         }
         __syncthreads();
         const bool whole = u == item0 && seg_end == item0 + nu;
         const int ca = paged_cut_first(R, item0), cb = paged_cut_last(R, item0 + nu);   // where it is cut
         float* mine = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == ca ? 1 : 0)) * SLOT;
         TA* out = (TA*)a.out;
+        const int dim = tid & (HD - 1), r0 = tid / HD;     // value and first row that the thread puts out
         auto store = [&](int r, float v) {
             const int rr = rg * RG + r, tok = rr / c.G;
-            out[(int64_t)(q.row0 + tok) * a.out_stride + (int64_t)(h * c.G + rr - tok * c.G) * HD + tid] = from_f<TA>(v);
+            out[(int64_t)(q.row0 + tok) * a.out_stride + (int64_t)(h * c.G + rr - tok * c.G) * HD + dim] = from_f<TA>(v);
         };
-        for (int r = 0; r < rows; ++r) {
+        for (int r = r0; r < rows; r += DW / 4) {
             float m = sm_m[0][r];
 #pragma unroll
             for (int w = 1; w < DW; ++w) m = fmaxf(m, sm_m[w][r]);
@@ -397,14 +407,14 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             for (int w = 0; w < DW; ++w) {
                 const float f = ex2(sm_m[w][r] - ms);
                 const int col = F32 ? 8 * (r >> 2) + (r & 3) : r;
-                acc += f * (F32 ? so[w][col][tid] + so[w][col + 4][tid] : so[w][col][tid]);
+                acc += f * (F32 ? so[w][col][dim] + so[w][col + 4][dim] : so[w][col][dim]);
                 sum += f * sm_l[w][r];
             }
             if (whole) {
                 store(r, sum != 0.f ? acc / sum : 0.f);
             } else {
-                mine[r * HD + tid] = acc;
-                if (tid == 0) { mine[RG * HD + r] = m; mine[RG * HD + RG + r] = sum; }
+                mine[r * HD + dim] = acc;
+                if (dim == 0) { mine[RG * HD + r] = m; mine[RG * HD + RG + r] = sum; }
             }
         }
         if (!whole) {
@@ -418,7 +428,7 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
             __syncthreads();
             if (s_last) {
                 // weights of the parts (the outputs' place is free: every thread is past the barriers above), then each
-                // warp adds up every fourth part
+                // warp adds up every DW-th part
                 const int n = cb - ca + 1;
                 float* wt = so_all;
                 auto part = [&](int i) { return parts + (size_t)((ca + i) * 2 + (i == 0 ? 1 : 0)) * SLOT; };
@@ -468,9 +478,11 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
                 for (int r = 0; r < RG; ++r)
                     if (r < rows) *(float4*)&so[warp][r][lane * 4] = acc[r];
                 __syncthreads();
-                for (int r = 0; r < rows; ++r) {
+                for (int r = r0; r < rows; r += DW / 4) {
                     const float sum = sm_l[0][r];
-                    const float v = so[0][r][tid] + so[1][r][tid] + so[2][r][tid] + so[3][r][tid];
+                    float v = 0.f;
+#pragma unroll
+                    for (int w = 0; w < DW; ++w) v += so[w][r][dim];
                     store(r, sum != 0.f ? v / sum : 0.f);
                 }
             }
