@@ -33,7 +33,7 @@ namespace {
 constexpr int DW = 4;             // warps of a CTA
 constexpr int DU = 16 * DW;       // keys of a unit
 constexpr int d8_ctas(int nt) { return nt == 1 ? 3 : 2; }   // resident CTAs of an SM (registers)
-constexpr int d8_stages(int nt) { return nt == 1 ? 3 : 4; } // blocks of a warp's ring
+constexpr int D8_RING = 3;                                  // blocks of a warp's ring
 constexpr int D8_STAGE = 2 * 16 * HD;                       // bytes of one: K and V of 16 keys
 constexpr float P_SHIFT = 7.f;    // weights are 2^7 times exp2 of score - maximum
 
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
     constexpr int RG = F32 ? 4 * NT : 8 * NT;   // query rows of an item
     const PagedView& c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    constexpr int S = d8_stages(NT);
+    constexpr int S = D8_RING;
     // The warps' rings; between two segments the outputs and the weights of an item's parts.  A row of 16 keys' codes is 128
     // bytes; its 16-byte pieces are moved about so that a warp's reads of fragments meet no bank twice.
     extern __shared__ __align__(128) unsigned char raw[];
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
 template <typename TA, int NT>
 cudaError_t launch_t(const Paged8Attn& a, cudaStream_t st) {
     const int grid = min(device_sm_count(), 160) * d8_ctas(NT);
-    constexpr int smem = DW * d8_stages(NT) * D8_STAGE;
+    constexpr int smem = DW * D8_RING * D8_STAGE;
     // a per-device attribute: set on every call (a host-side table lookup)
     const cudaError_t e = cudaFuncSetAttribute(paged8_decode_kernel<TA, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
