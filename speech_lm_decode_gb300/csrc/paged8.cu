@@ -382,7 +382,8 @@ int q3paged8_attention(const q3paged8_cache* cache, int n_tokens, int max_q, con
         return r;
     a.ks = cache->k_scale;
     a.vs = cache->v_scale;
-    const cudaError_t e = launch_paged8_attention(a, (cudaStream_t)stream);
+    const cudaError_t e = paged8_decode_takes(a) ? launch_paged8_decode(a, (cudaStream_t)stream)
+                                                 : launch_paged8_chunk(a, (cudaStream_t)stream);
     if (e != cudaSuccess) return paged_fail(Q3_ERR_CUDA, "attention: %s", cudaGetErrorString(e));
     return Q3_OK;
 }

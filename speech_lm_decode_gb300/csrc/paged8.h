@@ -32,10 +32,11 @@ struct Paged8Append {
     int* err;
 };
 
-cudaError_t launch_paged8_attention(const Paged8Attn& a, cudaStream_t st);
 // few query rows (paged8_decode.cu)
 bool paged8_decode_takes(const Paged8Attn& a);
 cudaError_t launch_paged8_decode(const Paged8Attn& a, cudaStream_t st);
+// many query rows (paged8_chunk.cu)
+cudaError_t launch_paged8_chunk(const Paged8Attn& a, cudaStream_t st);
 
 constexpr int E8_MIN = 127 - 100, E8_MAX = 127 + 119;   // scales that append writes
 

@@ -48,26 +48,9 @@ namespace q3 {
 
 namespace {
 
-constexpr int CT = 128;                    // rows of a tile, keys of a unit
-constexpr int STAGE = CT * HD * 2;         // bytes of a K or V tile
 constexpr int C_THREADS = 384;
-constexpr int C_MAX_CTAS = 192;
-constexpr int C_OVER = 4;                  // units that an item costs besides its keys
-constexpr int C_MIN_UNITS = C_OVER + 2;
 constexpr int c_stages(bool f32) { return f32 ? 4 : 5; }
 constexpr int c_qbytes(bool f32) { return f32 ? 3 * STAGE : 2 * STAGE; }
-constexpr size_t C_SLOT = (size_t)2 * CT * (HD + 2);   // floats of a partial
-
-// One cut of an item that a CTA works on.
-struct Seg {
-    int s, h;             // sequence, kv head
-    int tok0, ntok;       // first token (of the sequence's new ones) and tokens of the item
-    int n;                // key tiles of this cut (0: the item sees no key)
-    int kt0;              // first of them
-    bool two;             // two tiles of rows
-    bool whole;           // the cut is the item
-    int ca, cb;           // CTAs of the item
-};
 
 struct ChunkSmem {
     uint64_t full[5], empty[5], s_full[2], p_full[2], r_full[2], pv_full, q_full, o_full, drain;
@@ -88,26 +71,6 @@ __device__ __forceinline__ void seg_sync(int id) { asm volatile("bar.sync %0, 28
 // fp32 D, bf16 A and B, M = N = 128; bit 16: B is MN-major
 constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(CT >> 3) << 17) | ((uint32_t)(CT >> 4) << 24);
 constexpr uint32_t IDESC_V = IDESC | (1u << 16);
-
-// ------------------------------------------------------------------ items
-// the part of the walk's item that this CTA takes
-__device__ __forceinline__ bool walk_seg(Walk& w, const PagedRange& R, int tpt, int tpi, Seg& g) {
-    int end;
-    if (!w.more || !paged_cut(R, w.item0, w.item0 + w.nu, &end)) return false;
-    g.s = w.s;
-    g.h = w.h;
-    g.tok0 = w.item * tpi;
-    g.ntok = min(tpi, w.q.n_new - g.tok0);
-    g.two = g.ntok > tpt;
-    g.kt0 = w.u == w.item0 ? 0 : w.u - w.item0 - C_OVER;
-    g.n = end - w.item0 - C_OVER - g.kt0;
-    if (w.q.ctx - w.q.n_new + g.tok0 + g.ntok <= 0 || w.q.ctx <= 0) g.n = 0;
-    g.whole = w.u == w.item0 && end == w.item0 + w.nu;
-    g.ca = paged_cut_first(R, w.item0);
-    g.cb = paged_cut_last(R, w.item0 + w.nu);
-    w.more = end == w.item0 + w.nu;   // a cut end is this CTA's last
-    return true;
-}
 
 template <typename TA>
 __global__ void __launch_bounds__(C_THREADS, 1)
@@ -557,37 +520,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             const int blk0 = g.two ? 0 : 2 * t, blk1 = g.two ? 4 : blk0 + 2;
             TA* dst = (TA*)a.out + (int64_t)(wq.row0 + tok) * a.out_stride + (int64_t)head * HD;
             const float inv = l != 0.f ? 1.f / l : 0.f;   // (NaN stays NaN)
-            // The output leaves through the tile's place for Q, whose products are done: a thread puts 32 values of its
-            // row, then the warp stores its rows side by side (16-byte pieces at places that depend on the row).
-            constexpr int PR = HD * (int)sizeof(TA) / 16, PB = PR / 4;   // pieces of a row, of 32 values
-            unsigned char* stage = qs + (size_t)(F32 ? 0 : tile) * STAGE;
-            auto put = [&](int blk, const float (&v)[32]) {
-#pragma unroll
-                for (int i = 0; i < PB; ++i) {
-                    uint4 d;
-                    if constexpr (F32)
-                        d = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                       __float_as_uint(v[4 * i + 3]));
-                    else
-                        d = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                                       pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-                    *(uint4*)(stage + (size_t)(r * PR + ((blk * PB + i) ^ (r & (PR - 1)))) * 16) = d;
-                }
-            };
-            auto flush = [&](int blk0, int blk1) {     // blocks [blk0, blk1) of the warp's 32 rows
-                __syncwarp();
-                const int n = (blk1 - blk0) * PB, per = 32 / n, piece = blk0 * PB + lane % n;
-#pragma unroll 4
-                for (int i0 = 0; i0 < 32; i0 += per) {
-                    const int i = i0 + lane / n;
-                    TA* to = (TA*)__shfl_sync(0xffffffffu, (unsigned long long)dst, i);
-                    const bool there = __shfl_sync(0xffffffffu, (int)live, i);
-                    const int row = (r & ~31) + i;
-                    const uint4 d = *(const uint4*)(stage + (size_t)(row * PR + (piece ^ (row & (PR - 1)))) * 16);
-                    if (there) *((uint4*)to + piece) = d;
-                }
-                __syncwarp();
-            };
+            // the output leaves through the tile's place for Q, whose products are done
+            const RowOut<TA> row_out = {qs + (size_t)(F32 ? 0 : tile) * STAGE, r, dst, live};
             // partials: [32 groups of 4 values][256 rows], then maxima and sums
             const int prow = tile * CT + r;
             float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == g.ca ? 1 : 0)) * C_SLOT;
@@ -620,7 +554,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = l != 0.f ? __uint_as_float(x[e][i]) * w0 : 0.f;
                         if (g.whole) {
-                            put(cc, v);
+                            row_out.put(cc, v);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
@@ -630,7 +564,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                 }
                 if (g.whole) {
-                    flush(blk0, blk1);
+                    row_out.flush(blk0, blk1);
                 } else if (blk0 == 0) {
                     slot[2 * CT * HD + prow] = mx;
                     slot[2 * CT * HD + 2 * CT + prow] = l;
@@ -647,62 +581,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 }
                 wg_sync(3);
                 if (sm.last) {
-                    const int mrow = tile * CT + r;
-                    auto part = [&](int cc) { return parts + (size_t)(cc * 2 + (cc == g.ca)) * C_SLOT; };
-                    float m = -INFINITY, sum = 0.f;
-#pragma unroll 1
-                    for (int c0 = g.ca; c0 <= g.cb; c0 += 8) {
-                        float pm[8], pl[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float* p = part(min(c0 + j, g.cb)) + 2 * CT * HD + mrow;
-                            pm[j] = __ldcg(p);
-                            pl[j] = __ldcg(p + 2 * CT);
-                        }
-                        const float was = m;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) m = fmaxf(m, pm[j]);
-                        const float ms = m == -INFINITY ? 0.f : m;
-                        sum *= ex2f((was - ms) * sl2);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (c0 + j <= g.cb) sum = fmaf(ex2f((pm[j] - ms) * sl2), pl[j], sum);
-                    }
-                    const float ms = m == -INFINITY ? 0.f : m, rs = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll 1
-                    for (int b = blk0; b < blk1; ++b) {
-                        float v[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-#pragma unroll 1
-                        for (int c0 = g.ca; c0 <= g.cb; c0 += 2) {
-                            float4 z[2][8];
-                            float f[2];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float* p = part(min(c0 + j, g.cb));
-                                f[j] = __ldcg(p + 2 * CT * HD + mrow);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    z[j][i] = __ldcg((const float4*)(p + ((size_t)(8 * b + i) * 2 * CT + mrow) * 4));
-                            }
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const float wj = c0 + j <= g.cb ? ex2f((f[j] - ms) * sl2) : 0.f;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    v[4 * i] = fmaf(z[j][i].x, wj, v[4 * i]);
-                                    v[4 * i + 1] = fmaf(z[j][i].y, wj, v[4 * i + 1]);
-                                    v[4 * i + 2] = fmaf(z[j][i].z, wj, v[4 * i + 2]);
-                                    v[4 * i + 3] = fmaf(z[j][i].w, wj, v[4 * i + 3]);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] *= rs;
-                        put(b, v);
-                    }
-                    flush(blk0, blk1);
+                    chunk_join(parts, g.ca, g.cb, tile * CT + r, sl2, blk0, blk1, row_out);
+                    row_out.flush(blk0, blk1);
                 }
             }
             seg_sync(1);

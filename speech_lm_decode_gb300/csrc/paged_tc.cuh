@@ -1,13 +1,21 @@
 // What the chunk kernels of paged attention share: mbarriers, TMA, tcgen05 and
-// packed fp32 arithmetic (sm_103a).
+// packed fp32 arithmetic (sm_103a); their items, their outputs and the join of
+// the parts of a cut item.
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "paged_sched.cuh"
 
 namespace q3 {
 
+constexpr int CT = 128;                    // rows of a tile, keys of a unit
+constexpr int STAGE = CT * HD * 2;         // bytes of a K or V tile of 16-bit values
+constexpr int C_MAX_CTAS = 192;
+constexpr int C_OVER = 4;                  // units that an item costs besides its keys
+constexpr int C_MIN_UNITS = C_OVER + 2;
+constexpr size_t C_SLOT = (size_t)2 * CT * (HD + 2);   // floats of a partial
 constexpr long long C_WAIT_LIMIT = 2000000000LL;   // cycles
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -150,6 +158,137 @@ __device__ __forceinline__ f2c add_pair(f2c a, f2c b) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *(const uint32_t*)&v;
+}
+
+// One cut of an item that a CTA works on.
+struct Seg {
+    int s, h;             // sequence, kv head
+    int tok0, ntok;       // first token (of the sequence's new ones) and tokens of the item
+    int n;                // key tiles of this cut (0: the item sees no key)
+    int kt0;              // first of them
+    bool two;             // two tiles of rows
+    bool whole;           // the cut is the item
+    int ca, cb;           // CTAs of the item
+};
+
+// ------------------------------------------------------------------ items
+// the part of the walk's item that this CTA takes
+__device__ __forceinline__ bool walk_seg(Walk& w, const PagedRange& R, int tpt, int tpi, Seg& g) {
+    int end;
+    if (!w.more || !paged_cut(R, w.item0, w.item0 + w.nu, &end)) return false;
+    g.s = w.s;
+    g.h = w.h;
+    g.tok0 = w.item * tpi;
+    g.ntok = min(tpi, w.q.n_new - g.tok0);
+    g.two = g.ntok > tpt;
+    g.kt0 = w.u == w.item0 ? 0 : w.u - w.item0 - C_OVER;
+    g.n = end - w.item0 - C_OVER - g.kt0;
+    if (w.q.ctx - w.q.n_new + g.tok0 + g.ntok <= 0 || w.q.ctx <= 0) g.n = 0;
+    g.whole = w.u == w.item0 && end == w.item0 + w.nu;
+    g.ca = paged_cut_first(R, w.item0);
+    g.cb = paged_cut_last(R, w.item0 + w.nu);
+    w.more = end == w.item0 + w.nu;   // a cut end is this CTA's last
+    return true;
+}
+
+// ------------------------------------------------------------------ outputs
+// 32 values at a time of a thread's row (row r of a tile of 128) through shared
+// memory: 16-byte pieces at places that depend on the row, so that the warp then
+// stores its rows side by side.
+template <typename TA> struct RowOut {
+    static constexpr int PR = HD * (int)sizeof(TA) / 16, PB = PR / 4;   // pieces of a row, of 32 values
+    unsigned char* stage;
+    int r;
+    TA* dst;
+    bool live;
+    __device__ __forceinline__ void put(int blk, const float (&v)[32]) const {
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            uint4 d;
+            if constexpr (sizeof(TA) == 4)
+                d = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                               __float_as_uint(v[4 * i + 3]));
+            else
+                d = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                               pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+            *(uint4*)(stage + (size_t)(r * PR + ((blk * PB + i) ^ (r & (PR - 1)))) * 16) = d;
+        }
+    }
+    __device__ __forceinline__ void flush(int blk0, int blk1) const {     // blocks [blk0, blk1) of the warp's 32 rows
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+        const int n = (blk1 - blk0) * PB, per = 32 / n, piece = blk0 * PB + lane % n;
+#pragma unroll 4
+        for (int i0 = 0; i0 < 32; i0 += per) {
+            const int i = i0 + lane / n;
+            TA* to = (TA*)__shfl_sync(0xffffffffu, (unsigned long long)dst, i);
+            const bool there = __shfl_sync(0xffffffffu, (int)live, i);
+            const int row = (r & ~31) + i;
+            const uint4 d = *(const uint4*)(stage + (size_t)(row * PR + (piece ^ (row & (PR - 1)))) * 16);
+            if (there) *((uint4*)to + piece) = d;
+        }
+        __syncwarp();
+    }
+};
+
+// Row mrow of an item cut over CTAs ca .. cb: the blocks [blk0, blk1) of their
+// parts, which hold maxima in units of 1 / sl2, put out.
+template <typename TA>
+__device__ __forceinline__ void chunk_join(const float* parts, int ca, int cb, int mrow, float sl2, int blk0, int blk1,
+                                           const RowOut<TA>& out) {
+    auto part = [&](int cc) { return parts + (size_t)(cc * 2 + (cc == ca)) * C_SLOT; };
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll 1
+    for (int c0 = ca; c0 <= cb; c0 += 8) {
+        float pm[8], pl[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float* p = part(min(c0 + j, cb)) + 2 * CT * HD + mrow;
+            pm[j] = __ldcg(p);
+            pl[j] = __ldcg(p + 2 * CT);
+        }
+        const float was = m;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, pm[j]);
+        const float ms = m == -INFINITY ? 0.f : m;
+        sum *= ex2f((was - ms) * sl2);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c0 + j <= cb) sum = fmaf(ex2f((pm[j] - ms) * sl2), pl[j], sum);
+    }
+    const float ms = m == -INFINITY ? 0.f : m, rs = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll 1
+    for (int b = blk0; b < blk1; ++b) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+        for (int c0 = ca; c0 <= cb; c0 += 2) {
+            float4 z[2][8];
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float* p = part(min(c0 + j, cb));
+                f[j] = __ldcg(p + 2 * CT * HD + mrow);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[j][i] = __ldcg((const float4*)(p + ((size_t)(8 * b + i) * 2 * CT + mrow) * 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float wj = c0 + j <= cb ? ex2f((f[j] - ms) * sl2) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[4 * i] = fmaf(z[j][i].x, wj, v[4 * i]);
+                    v[4 * i + 1] = fmaf(z[j][i].y, wj, v[4 * i + 1]);
+                    v[4 * i + 2] = fmaf(z[j][i].z, wj, v[4 * i + 2]);
+                    v[4 * i + 3] = fmaf(z[j][i].w, wj, v[4 * i + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= rs;
+        out.put(b, v);
+    }
 }
 
 // the driver's encoder of tensor maps (null: none)
