@@ -339,24 +339,28 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
             const int kmax = sm.mail[k & 1].kmax, vmax = sm.mail[k & 1].vmax;
             __syncwarp();
             if (lane == 0) bar_arrive(&sm.mail_empty[k & 1]);
-            auto convert = [&](int most, int live) {      // the next tile; rows from `live` on become zeros
+            for (int i = 0; i < 2 * g.n; ++i) {
+                // the order of the products: K0 V0 K1 V1 .. or, with one tile of rows, K0 K1 V0 K2 V1 .. V(n-1)
+                const bool is_v = g.two ? i & 1 : i == 2 * g.n - 1 || (i > 0 && !(i & 1));
+                const int most = is_v ? vmax : kmax, live = w.q.ctx - (g.kt0 + (i == 2 * g.n - 1 ? g.n - 1 : g.two ? i / 2 : i / 2 - 1)) * CT;
                 const int rs = cnt % RS, st = cnt % ST;
                 ok = ok && bar_wait(&sm.raw_full[rs], (cnt / RS) & 1, sm, a.err);
                 if (cnt >= ST) ok = ok && bar_wait(&sm.empty[st], (cnt / ST - 1) & 1, sm, a.err);
                 ok = __all_sync(0xffffffffu, ok);
                 ++cnt;
-                if (!ok) return;
+                if (!ok) continue;
                 const unsigned char* from = codes + (size_t)rs * RAW;
                 unsigned char* to = ring + (size_t)st * STAGE;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = sm.scale[rs][cw * 2 + (i >> 1)], row = row0 + 8 * i;
+                // (a short loop: long straight code of one warp per scheduler starves on instruction fetches)
+#pragma unroll 1
+                for (int j8 = 0; j8 < 4; ++j8) {
+                    const int e = sm.scale[rs][cw * 2 + (j8 >> 1)], row = row0 + 8 * j8;
                     const uint32_t f = e == 255 ? 0x7fffu : half_two(most - e), f2 = f | f << 16;
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const int piece = (lane & 3) + 4 * (half ^ z);
                         uint4 v = *(const uint4*)(from + row * HD + piece * 16);
-                        if (row >= live) v = make_uint4(0, 0, 0, 0);
+                        if (is_v && row >= live) v = make_uint4(0, 0, 0, 0);    // keys that do not exist
                         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
                         uint32_t d[8];
 #pragma unroll
@@ -379,12 +383,6 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                     bar_arrive(&sm.full[st]);
                     bar_arrive(&sm.raw_empty[rs]);
                 }
-            };
-            const int lead = g.two ? 1 : 2;
-            for (int i = 0; i < min(lead, g.n); ++i) convert(kmax, CT);
-            for (int i = 0; i < g.n; ++i) {
-                convert(vmax, w.q.ctx - (g.kt0 + i) * CT);
-                if (i + lead < g.n) convert(kmax, CT);
             }
             if (w.more) walk_step<CT, C_OVER>(w, a, R, tpi);
         }
