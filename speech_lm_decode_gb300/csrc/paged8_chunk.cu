@@ -35,7 +35,12 @@ namespace q3 {
 
 namespace {
 
-constexpr int C8_THREADS = 512;
+constexpr int CONV = 4;                    // warps that convert
+constexpr int C8_THREADS = 384 + 32 * CONV;
+// registers a thread: at launch (the launcher checks it), and of warps 0-3, the softmax and the conversion after they
+// have divided them; more than there are would be waited for for ever
+constexpr int REGS = 128, REGS_0 = 48, REGS_SOFT = 176, REGS_CONV = 112;
+static_assert(128 * REGS_0 + 256 * REGS_SOFT + 32 * CONV * REGS_CONV <= REGS * C8_THREADS, "registers of the CTA");
 constexpr int ST = 3;                      // f16 tiles (32 KB)
 constexpr int RS = 3;                      // tiles of codes (16 KB)
 constexpr int RAW = CT * HD;
@@ -105,9 +110,9 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
     if (R.u0 >= R.u1) return;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < ST; ++i) { bar_init(&sm.full[i], 4); bar_init(&sm.empty[i], 1); }   // (4: a warp each)
-        for (int i = 0; i < RS; ++i) { bar_init(&sm.raw_full[i], 1); bar_init(&sm.raw_empty[i], 4); }
-        for (int i = 0; i < 2; ++i) { bar_init(&sm.mail_full[i], 1); bar_init(&sm.mail_empty[i], 12); }
+        for (int i = 0; i < ST; ++i) { bar_init(&sm.full[i], CONV); bar_init(&sm.empty[i], 1); }   // (a warp each)
+        for (int i = 0; i < RS; ++i) { bar_init(&sm.raw_full[i], 1); bar_init(&sm.raw_empty[i], CONV); }
+        for (int i = 0; i < 2; ++i) { bar_init(&sm.mail_full[i], 1); bar_init(&sm.mail_empty[i], 8 + CONV); }
         for (int i = 0; i < 2; ++i) {
             bar_init(&sm.s_full[i], 1);
             bar_init(&sm.p_full[i], CT / 32);   // a warp each
@@ -134,9 +139,8 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
     walk_begin<CT, C_OVER>(w, a, R, tpi);
     if (threadIdx.x == 128) { sm.range = R; sm.walk = w; }
 
-    // registers: 512 threads x 128 at launch = 128 x 56 + 256 x 200 + 128 x 56 (the launcher checks the 128)
     if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_0));
     Seg g;
     if (warp == 0) {
         // ---------------------------------------------------------- tiles of codes
@@ -245,7 +249,7 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                 for (int p = 0; p < PP; ++p)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_ts(d + p * CT, pa + 64 * p + 8 * ks, vd + ks * (2048 >> 4), IDESC_V, ks != 0 ? 1u : first);
+                        umma_ts(d + p * CT, pa + 32 * (ks >> 1) + 16 * p + 8 * (ks & 1), vd + ks * (2048 >> 4), IDESC_V, ks != 0 ? 1u : first);
             }
             __syncwarp();
         };
@@ -326,13 +330,20 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
         }
     }
     } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONV));
         // ---------------------------------------------------------- codes to f16 tiles
         Seg g;
         bool ok = true;
         int cnt = 0;
         // Eight lanes take half a row each of two rows, so that neither their loads nor their stores meet a bank twice.
-        const int cw = warp - 12, half = lane >> 2 & 1, row0 = cw * 32 + (lane >> 3) * 2 + half;
+        const int half = lane >> 2 & 1, row0 = (warp - 12) * (CT / CONV) + (lane >> 3) * 2 + half;
+        int src[2], dst[2];      // places of the lane's two pieces of row0 (eight rows on: 1024 bytes, in either tile)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int piece = (lane & 3) + 4 * (half ^ z);
+            src[z] = row0 * HD + piece * 16;
+            dst[z] = (piece >> 2) * (STAGE / 2) + row0 * 128 + (((piece & 3) * 2 ^ (row0 & 7)) << 4);    // (the second half: ^ 16)
+        }
         for (int k = 0; walk_seg(w, R, tpt, tpi, g); ++k) {
             ok = ok && bar_wait(&sm.mail_full[k & 1], (k >> 1) & 1, sm, a.err);
             ok = __all_sync(0xffffffffu, ok);
@@ -351,30 +362,40 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                 if (!ok) continue;
                 const unsigned char* from = codes + (size_t)rs * RAW;
                 unsigned char* to = ring + (size_t)st * STAGE;
+                const bool tail = is_v && live < CT;      // values of keys that do not exist become zeros
                 // (a short loop: long straight code of one warp per scheduler starves on instruction fetches)
 #pragma unroll 1
-                for (int j8 = 0; j8 < 4; ++j8) {
-                    const int e = sm.scale[rs][cw * 2 + (j8 >> 1)], row = row0 + 8 * j8;
+                for (int j = 0; j < CT / CONV; j += 16) {
+                    const int e = sm.scale[rs][((warp - 12) * (CT / CONV) + j) >> 4];
                     const uint32_t f = e == 255 ? 0x7fffu : half_two(most - e), f2 = f | f << 16;
+                    uint4 v[4];
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const int piece = (lane & 3) + 4 * (half ^ z);
-                        uint4 v = *(const uint4*)(from + row * HD + piece * 16);
-                        if (is_v && row >= live) v = make_uint4(0, 0, 0, 0);    // keys that do not exist
-                        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t d[8];
+                    for (int z = 0; z < 4; ++z) v[z] = *(const uint4*)(from + src[z & 1] + (j + 8 * (z >> 1)) * 128);
+                    if (tail) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            half4_of(w4[j], d[2 * j], d[2 * j + 1]);
+                        for (int z = 0; z < 4; ++z)
+                            if (row0 + j + 8 * (z >> 1) >= live) v[z] = make_uint4(0, 0, 0, 0);
+                    }
+                    uint32_t d[4][8];
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const __half2 p = __hmul2(*(const __half2*)&d[2 * j + y], *(const __half2*)&f2);
-                                d[2 * j + y] = *(const uint32_t*)&p;
-                            }
+                    for (int z = 0; z < 4; ++z) {
+                        half4_of(v[z].x, d[z][0], d[z][1]);
+                        half4_of(v[z].y, d[z][2], d[z][3]);
+                        half4_of(v[z].z, d[z][4], d[z][5]);
+                        half4_of(v[z].w, d[z][6], d[z][7]);
+                    }
+                    if (f != 0x3c00u) {
+#pragma unroll
+                        for (int z = 0; z < 32; ++z) {
+                            const __half2 p = __hmul2(*(const __half2*)&d[z >> 3][z & 7], *(const __half2*)&f2);
+                            d[z >> 3][z & 7] = *(const uint32_t*)&p;
                         }
-                        unsigned char* line = to + (piece >> 2) * (STAGE / 2) + row * 128;
-                        *(uint4*)(line + (((piece & 3) * 2 ^ (row & 7)) << 4)) = make_uint4(d[0], d[1], d[2], d[3]);
-                        *(uint4*)(line + (((piece & 3) * 2 + 1 ^ (row & 7)) << 4)) = make_uint4(d[4], d[5], d[6], d[7]);
+                    }
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        unsigned char* at = to + (j + 8 * (z >> 1)) * 128;
+                        *(uint4*)(at + dst[z & 1]) = make_uint4(d[z][0], d[z][1], d[z][2], d[z][3]);
+                        *(uint4*)(at + (dst[z & 1] ^ 16)) = make_uint4(d[z][4], d[z][5], d[z][6], d[z][7]);
                     }
                 }
                 fence_async_smem();
@@ -387,7 +408,7 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
             if (w.more) walk_step<CT, C_OVER>(w, a, R, tpi);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFT));
         // ---------------------------------------------------------- softmax
         const int t = warp >= 8 ? 1 : 0;
         const int r = (threadIdx.x & 127);                 // this thread's row of a tile
@@ -486,45 +507,47 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                 ++sc;
                 ok = __all_sync(0xffffffffu, ok);
                 fence_after();
-                uint32_t x[4][32];
+                const bool masked = __any_sync(0xffffffffu, plain - k0 < CT);
+                const int seen = masked ? lim() - k0 : CT;          // columns that the row sees
+                if (masked && lost) {   // keys of pages out of range do not count: their scores become -inf
+                    const int key = k0 + 16 * (lane & 7);
+                    const unsigned gone = __ballot_sync(0xffffffffu, key < wq.ctx &&    // bit i: keys 16 i .. 16 i + 15
+                        (unsigned)c.table[(int64_t)g.s * c.max_pages + (key >> c.page_shift)] >= (unsigned)c.n_pages);
+                    uint32_t none[16];
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, x[cc]);
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(x[cc]);
-                if (__any_sync(0xffffffffu, plain - k0 < CT)) {
-                    if (lost) {   // keys of pages out of range do not count: their scores become -inf, all are read again
-                        const int key = k0 + 16 * (lane & 7);
-                        const unsigned gone = __ballot_sync(0xffffffffu, key < wq.ctx &&    // bit i: keys 16 i .. 16 i + 15
-                            (unsigned)c.table[(int64_t)g.s * c.max_pages + (key >> c.page_shift)] >= (unsigned)c.n_pages);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[0][i] = 0xff800000u;
-                        uint32_t (&none)[16] = *reinterpret_cast<uint32_t (*)[16]>(&x[0][0]);
+                    for (int i = 0; i < 16; ++i) none[i] = 0xff800000u;
 #pragma unroll 1
-                        for (int i = 0; i < 8; ++i)
-                            if (gone >> i & 1) tmem_st16(tS + 16 * i, none);
-                        tmem_wait_st();
+                    for (int i = 0; i < 8; ++i)
+                        if (gone >> i & 1) tmem_st16(tS + 16 * i, none);
+                    tmem_wait_st();
+                }
+                // The scores are read twice, for their maximum and for the weights, whose place is over the scores that
+                // they come from: short loops and few registers, as instruction fetches of the softmax and of the
+                // conversion go to one cache.
+                uint32_t x[2][32];
+                auto scores = [&](int col) {         // of columns col .. col + 63
+                    tmem_ld32(tS + col, x[0]);
+                    tmem_ld32(tS + col + 32, x[1]);
+                    tmem_wait_ld(x[0]);
+                    tmem_wait_ld(x[1]);
+                    if (masked) {
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, x[cc]);
-#pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(x[cc]);
+                        for (int i = 0; i < 64; ++i)
+                            if (i >= seen - col) x[i >> 5][i & 31] = 0xff800000u;
                     }
-                    const int seen = lim() - k0;                   // columns that the row sees
+                };
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int col = 0; col < CT; col += 64) {
+                    scores(col);
+                    float m[2] = {__uint_as_float(x[0][0]), __uint_as_float(x[1][0])};
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * cc + i >= seen) x[cc][i] = 0xff800000u;
+                    for (int i = 1; i < 31; i += 2) {
+                        m[0] = fmaxf(fmaxf(m[0], __uint_as_float(x[0][i])), __uint_as_float(x[0][i + 1]));
+                        m[1] = fmaxf(fmaxf(m[1], __uint_as_float(x[1][i])), __uint_as_float(x[1][i + 1]));
+                    }
+                    top = fmaxf(fmaxf(top, fmaxf(m[0], __uint_as_float(x[0][31]))), fmaxf(m[1], __uint_as_float(x[1][31])));
                 }
-                float tops[4];
-#pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    tops[cc] = __uint_as_float(x[cc][0]);
-#pragma unroll
-                    for (int i = 1; i < 31; i += 2)
-                        tops[cc] = fmaxf(fmaxf(tops[cc], __uint_as_float(x[cc][i])), __uint_as_float(x[cc][i + 1]));
-                    tops[cc] = fmaxf(tops[cc], __uint_as_float(x[cc][31]));
-                }
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // The maximum that the weights refer to moves only when a score passes it by 2^8.  Two slots with one
                 // tile share it: a step takes it over from the step before, which is the other slot's.
                 const int step = g.two ? j : 2 * j + t;
@@ -567,21 +590,25 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                 const float ref = mx == -INFINITY ? 0.f : P_SHIFT - mx * sl;
                 const f2c sf = pair(sl, sl), rf = pair(ref, ref);
                 f2c sums = pair(0.f, 0.f);
+#pragma unroll 1
+                for (int col = 0; col < CT; col += 64) {
+                    scores(col);
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
-                    uint32_t hi[16], lo[16];
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float p0, p1;
-                        unpair(fma_pair(pair(__uint_as_float(x[cc][2 * i]), __uint_as_float(x[cc][2 * i + 1])), sf, rf), p0, p1);
-                        p0 = ex2f(p0);
-                        p1 = ex2f(p1);
-                        sums = add_pair(sums, pair(p0, p1));
-                        hi[i] = half2_bits(p0, p1);
-                        if constexpr (F32) lo[i] = rest2(p0, p1, hi[i]);
+                        for (int i = 0; i < 16; ++i) {
+                            float p0, p1;
+                            unpair(fma_pair(pair(__uint_as_float(x[e][2 * i]), __uint_as_float(x[e][2 * i + 1])), sf, rf), p0, p1);
+                            p0 = ex2f(p0);
+                            p1 = ex2f(p1);
+                            sums = add_pair(sums, pair(p0, p1));
+                            hi[i] = half2_bits(p0, p1);
+                            if constexpr (F32) lo[i] = rest2(p0, p1, hi[i]);
+                        }
+                        tmem_st16(tS + col + 32 * e, hi);
+                        if constexpr (F32) tmem_st16(tS + col + 32 * e + 16, lo);
                     }
-                    tmem_st16(tS + 16 * cc, hi);
-                    if constexpr (F32) tmem_st16(tS + 64 + 16 * cc, lo);
                 }
                 tmem_wait_st();
                 fence_before();
@@ -717,7 +744,7 @@ cudaError_t launch_t(const Paged8Attn& a, cudaStream_t st) {
     // the kernel's warps redistribute exactly this many registers; with fewer they would wait for ever
     static const bool regs_ok = [] {
         cudaFuncAttributes at;
-        return cudaFuncGetAttributes(&at, paged8_chunk_kernel<TA>) == cudaSuccess && at.numRegs == 128;
+        return cudaFuncGetAttributes(&at, paged8_chunk_kernel<TA>) == cudaSuccess && at.numRegs == REGS;
     }();
     if (!regs_ok) return cudaErrorInvalidConfiguration;
     const int grid = min(device_sm_count(), C_MAX_CTAS);
