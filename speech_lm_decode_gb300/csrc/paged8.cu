@@ -2,6 +2,7 @@
 // the append and the read kernel.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged8.h"
@@ -19,24 +20,30 @@ namespace {
 // Blocks of more than sixteen new tokens are gone through twice.
 constexpr int A8_WARPS = 8, A8_TOKENS = 16;
 
-__device__ __forceinline__ void expand(const uint4& r, float (&v)[8]) { unpack_bf16x8(r, v); }
-__device__ __forceinline__ void expand(const uint4& r, float (&v)[4]) {
-    v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+// A lane has eight values of a head: four from 4 i on and their partners of the rotation, 64 further on.
+struct Raw16 { uint2 lo, hi; };
+struct Raw32 { float4 lo, hi; };
+__device__ __forceinline__ void fetch(const bf16* p, Raw16& r) { r = {*(const uint2*)p, *(const uint2*)(p + HD / 2)}; }
+__device__ __forceinline__ void fetch(const float* p, Raw32& r) { r = {*(const float4*)p, *(const float4*)(p + HD / 2)}; }
+__device__ __forceinline__ void expand(const Raw16& r, float (&v)[8]) { unpack_bf16x8(make_uint4(r.lo.x, r.lo.y, r.hi.x, r.hi.y), v); }
+__device__ __forceinline__ void expand(const Raw32& r, float (&v)[8]) {
+    v[0] = r.lo.x; v[1] = r.lo.y; v[2] = r.lo.z; v[3] = r.lo.w; v[4] = r.hi.x; v[5] = r.hi.y; v[6] = r.hi.z; v[7] = r.hi.w;
 }
 __device__ __forceinline__ uint32_t two(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *(const uint32_t*)&v;
 }
 __device__ __forceinline__ void put(bf16* p, const float (&v)[8]) {
-    *(uint4*)p = make_uint4(two(v[0], v[1]), two(v[2], v[3]), two(v[4], v[5]), two(v[6], v[7]));
+    *(uint2*)p = make_uint2(two(v[0], v[1]), two(v[2], v[3]));
+    *(uint2*)(p + HD / 2) = make_uint2(two(v[4], v[5]), two(v[6], v[7]));
 }
-__device__ __forceinline__ void put(float* p, const float (&v)[4]) { *(float4*)p = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void put(float* p, const float (&v)[8]) {
+    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)(p + HD / 2) = make_float4(v[4], v[5], v[6], v[7]);
+}
 __device__ __forceinline__ void put_codes(uint8_t* p, const float (&v)[8], float f) {
-    *(uint2*)p = make_uint2(codes_of(v[0] * f, v[1] * f) | codes_of(v[2] * f, v[3] * f) << 16,
-                            codes_of(v[4] * f, v[5] * f) | codes_of(v[6] * f, v[7] * f) << 16);
-}
-__device__ __forceinline__ void put_codes(uint8_t* p, const float (&v)[4], float f) {
     *(uint32_t*)p = codes_of(v[0] * f, v[1] * f) | codes_of(v[2] * f, v[3] * f) << 16;
+    *(uint32_t*)(p + HD / 2) = codes_of(v[4] * f, v[5] * f) | codes_of(v[6] * f, v[7] * f) << 16;
 }
 
 // the byte of the least 2^e with amax <= 448 2^e = 1.75 2^(8 + e), held to what append writes
@@ -67,10 +74,11 @@ template <typename TA>
 __global__ void __launch_bounds__(A8_WARPS * 32, 2) paged8_append_kernel(const Paged8Append a) {
     pdl_wait();
     pdl_trigger();
-    constexpr int VL = 16 / (int)sizeof(TA), LPH = HD / VL, TPL = 32 / LPH, NL = A8_TOKENS / TPL;
+    constexpr int NB = 4;      // pairs of tokens whose loads are in flight together
+    using Raw = std::conditional_t<sizeof(TA) == 2, Raw16, Raw32>;
     const PagedView& c = a.c;
     const int heads = c.nq + 2 * c.nkv, groups = (heads + A8_WARPS - 1) / A8_WARPS;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (LPH - 1);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, odd = lane >> 4, sub = lane & 15;
     const int B = 1 << a.block_shift, per_shift = c.page_shift - a.block_shift;
     auto blocks_of = [&](const A8Seq& q) {
         return q.to > q.from ? ((q.to - 1) >> a.block_shift) - (q.from >> a.block_shift) + 1 : 0;
@@ -132,78 +140,74 @@ __global__ void __launch_bounds__(A8_WARPS * 32, 2) paged8_append_kernel(const P
             continue;
         }
         const int slot0 = block0 & ((1 << c.page_shift) - 1);
-        const TA* src = (const TA*)a.qkv + ((int64_t)q.row0 - q.first) * a.ldq + (int64_t)h * HD + sub * VL;   // of position 0
+        const TA* src = (const TA*)a.qkv + ((int64_t)q.row0 - q.first) * a.ldq + (int64_t)h * HD + sub * 4;   // of position 0
         const bool is_q = h < c.nq, is_v = h >= c.nq + c.nkv;
         const float* w = is_q ? a.qn : a.kn;
-        float y[NL][VL], amax = 0.f;
-        auto form = [&](int t0) {      // entries of the tokens at positions t0 .. t0 + 15 into y
-            uint4 raw[NL];
+        float wn[8];
+        if (!is_v && w) {
+            const float4 lo = *(const float4*)(w + sub * 4), hi = *(const float4*)(w + HD / 2 + sub * 4);
+            wn[0] = lo.x; wn[1] = lo.y; wn[2] = lo.z; wn[3] = lo.w; wn[4] = hi.x; wn[5] = hi.y; wn[6] = hi.z; wn[7] = hi.w;
+        }
+        // use(i, p, x) of the tokens at positions t0 .. t0 + 7, two at a time: the lane's is p, its values x
+        auto batch = [&](int t0, auto use) {
+            Raw raw[NB];
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int p = t0 + i * TPL + lane / LPH;
-                raw[i] = p < p1 ? *(const uint4*)(src + p * a.ldq) : make_uint4(0, 0, 0, 0);
-            }
+            for (int i = 0; i < NB; ++i) fetch(src + min(t0 + 2 * i + odd, p1 - 1) * a.ldq, raw[i]);
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                if (t0 + i * TPL >= p1) {
-#pragma unroll
-                    for (int j = 0; j < VL; ++j) y[i][j] = 0.f;
-                    continue;
-                }
-                float x[VL];
+            for (int i = 0; i < NB; ++i) {
+                const int p = min(t0 + 2 * i + odd, p1 - 1);       // (past the last one: that one again)
+                float x[8];
                 expand(raw[i], x);
                 if (!is_v) {
+                    const float4* cs = (const float4*)(a.rope + (int64_t)p * (HD / 2) + sub * 4);
+                    const float4 c01 = cs[0], c23 = cs[1];
                     if (w) {
                         float ss = 0.f;
 #pragma unroll
-                        for (int j = 0; j < VL; ++j) ss = fmaf(x[j], x[j], ss);
+                        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
-                        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                        for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                         const float r = rsqrtf(fmaf(ss, 1.0f / HD, a.eps));   // within 2^-22
 #pragma unroll
-                        for (int j = 0; j < VL; j += 4) {
-                            const float4 f = *(const float4*)(w + sub * VL + j);
-                            x[j] *= r * f.x; x[j + 1] *= r * f.y; x[j + 2] *= r * f.z; x[j + 3] *= r * f.w;
-                        }
+                        for (int j = 0; j < 8; ++j) x[j] *= r * wn[j];
                     }
-                    const int p = min(t0 + i * TPL + lane / LPH, p1 - 1);
-                    const float4* cs = (const float4*)(a.rope + (int64_t)p * (HD / 2) + (sub & (LPH / 2 - 1)) * VL);
-                    const float sign = sub < LPH / 2 ? -1.f : 1.f;
+                    const float co[4] = {c01.x, c01.z, c23.x, c23.z}, si[4] = {c01.y, c01.w, c23.y, c23.w};
 #pragma unroll
-                    for (int j = 0; j < VL; j += 2) {
-                        const float4 f = cs[j / 2];
-                        y[i][j] = fmaf(x[j], f.x, __shfl_xor_sync(0xffffffffu, x[j], LPH / 2) * (sign * f.y));
-                        y[i][j + 1] = fmaf(x[j + 1], f.z, __shfl_xor_sync(0xffffffffu, x[j + 1], LPH / 2) * (sign * f.w));
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VL; ++j) y[i][j] = x[j];
-                }
-                if (!is_q) {
-#pragma unroll
-                    for (int j = 0; j < VL; ++j) {
-                        y[i][j] = fmaf(y[i][j], 0.f, y[i][j]);      // infinities become NaN, which the maximum passes over
-                        amax = fmaxf(amax, fabsf(y[i][j]));
+                    for (int j = 0; j < 4; ++j) {
+                        const float lo = x[j], hi = x[j + 4];
+                        x[j] = fmaf(lo, co[j], -hi * si[j]);
+                        x[j + 4] = fmaf(hi, co[j], lo * si[j]);
                     }
                 }
+                use(i, p, x);
             }
         };
         if (is_q) {
-            TA* dst = (TA*)a.q_out + ((int64_t)q.row0 - q.first) * a.ldo + (int64_t)h * HD + sub * VL;
-            for (int t0 = p0; t0 < p1; t0 += A8_TOKENS) {
-                form(t0);
-#pragma unroll
-                for (int i = 0; i < NL; ++i) {
-                    const int p = t0 + i * TPL + lane / LPH;
-                    if (p < p1) put(dst + p * a.ldo, y[i]);
-                }
-            }
+            TA* dst = (TA*)a.q_out + ((int64_t)q.row0 - q.first) * a.ldo + (int64_t)h * HD + sub * 4;
+            for (int t0 = p0; t0 < p1; t0 += 2 * NB)
+                batch(t0, [&](int i, int p, const float (&x)[8]) {
+                    if (t0 + 2 * i + odd < p1) put(dst + p * a.ldo, x);
+                });
             continue;
         }
         const int hk = h - c.nq - (is_v ? c.nkv : 0);
         uint8_t* sc = (is_v ? a.vs : a.ks) + (((int64_t)page * c.nkv + hk) << per_shift) + (slot0 >> a.block_shift);
         uint8_t* codes = (uint8_t*)(is_v ? c.v : c.k) + page * c.page_stride + hk * c.head_stride + slot0 * c.token_stride;
         const bool once = p1 - p0 <= A8_TOKENS;
+        float y[A8_TOKENS / 2][8], amax = 0.f;
+        auto form = [&](int t0) {      // entries of the tokens at positions t0 .. t0 + 15
+#pragma unroll
+            for (int z = 0; z < A8_TOKENS / 2 / NB; ++z)
+                if (t0 + 2 * NB * z < p1)
+                    batch(t0 + 2 * NB * z, [&](int i, int, const float (&x)[8]) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float v = fmaf(x[j], 0.f, x[j]);      // infinities become NaN, which the maximum passes over
+                            amax = fmaxf(amax, fabsf(v));
+                            y[z * NB + i][j] = v;
+                        }
+                    });
+        };
         for (int t0 = p0; t0 < p1; t0 += A8_TOKENS) form(t0);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -229,9 +233,9 @@ __global__ void __launch_bounds__(A8_WARPS * 32, 2) paged8_append_kernel(const P
         for (int t0 = p0; t0 < p1; t0 += A8_TOKENS) {
             if (!once) form(t0);
 #pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int p = t0 + i * TPL + lane / LPH;
-                if (p < p1) put_codes(codes + (p - block0) * c.token_stride + sub * VL, y[i], f);
+            for (int i = 0; i < A8_TOKENS / 2; ++i) {
+                const int p = t0 + 2 * i + odd;
+                if (p < p1) put_codes(codes + (p - block0) * c.token_stride + sub * 4, y[i], f);
             }
         }
         if (lane == 0) *sc = (uint8_t)e;
@@ -239,39 +243,51 @@ __global__ void __launch_bounds__(A8_WARPS * 32, 2) paged8_append_kernel(const P
 }
 
 // ------------------------------------------------------------------ read
-// Bound by the bytes: one in and two (four) out a code.  A thread takes sixteen codes.
+// Bound by the bytes: one in and two (four) out a code.  A CTA takes 1024 pieces of sixteen codes of one page's keys or
+// values, a thread four of them, all in flight.
+constexpr int R8_PIECES = 1024;
+
 template <typename TO>
 __global__ void __launch_bounds__(256) paged8_read_kernel(PagedView c, int block_shift, const uint8_t* ks, const uint8_t* vs,
-                                                          int n, const int32_t* __restrict__ pages, TO* k_out, TO* v_out,
-                                                          int* err) {
+                                                          const int32_t* __restrict__ pages, TO* k_out, TO* v_out, int* err) {
     pdl_wait();
     pdl_trigger();
-    const int64_t rows = (int64_t)n * c.nkv << c.page_shift;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * 16; i += (int64_t)gridDim.x * 256) {
-        const bool is_v = i >= rows * 8;
-        TO* out = is_v ? v_out : k_out;
-        if (!out) continue;
-        const int64_t r = is_v ? i - rows * 8 : i;
-        const int piece = (int)(r & 7);
-        const int64_t row = r >> 3, ph = row >> c.page_shift;
-        const int slot = (int)(row & ((1 << c.page_shift) - 1)), h = (int)(ph % c.nkv), page = pages[ph / c.nkv];
-        if ((unsigned)page >= (unsigned)c.n_pages) {
-            if (err) atomicOr(err, ERRB_BOUNDS);
-            continue;
-        }
-        const uint8_t* src = (const uint8_t*)(is_v ? c.v : c.k) + page * c.page_stride + h * c.head_stride + slot * c.token_stride;
-        const uint4 w = *(const uint4*)(src + piece * 16);
-        const float f = e8m0((is_v ? vs : ks)[(((int64_t)page * c.nkv + h) << (c.page_shift - block_shift)) + (slot >> block_shift)]);
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    const int slices = gridDim.y / 2;
+    const bool is_v = (int)blockIdx.y >= slices;
+    TO* out = is_v ? v_out : k_out;
+    if (!out) return;
+    const int page = pages[blockIdx.x], count = c.nkv << (c.page_shift + 3);
+    if ((unsigned)page >= (unsigned)c.n_pages) {
+        if (threadIdx.x == 0 && err) atomicOr(err, ERRB_BOUNDS);
+        return;
+    }
+    const uint8_t* src = (const uint8_t*)(is_v ? c.v : c.k) + page * c.page_stride;
+    const uint8_t* sc = (is_v ? vs : ks) + (((int64_t)page * c.nkv) << (c.page_shift - block_shift));
+    out += (int64_t)blockIdx.x * count * 16;
+    const int p0 = (is_v ? blockIdx.y - slices : blockIdx.y) * R8_PIECES + threadIdx.x;
+    uint4 w[4];
+    uint32_t e[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        const int p = min(p0 + 256 * z, count - 1), row = p >> 3, h = row >> c.page_shift, slot = row & ((1 << c.page_shift) - 1);
+        w[z] = ld_stream_u4(src + h * c.head_stride + slot * c.token_stride + (p & 7) * 16);
+        e[z] = __ldg(sc + (row >> block_shift));      // (blocks of a page's heads follow each other)
+    }
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        const int p = p0 + 256 * z;
+        if (p >= count) break;
+        const float f = e8m0(e[z]);
+        const uint32_t words[4] = {w[z].x, w[z].y, w[z].z, w[z].w};
         float v[16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float x[4];
             float4_of(words[j], x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * j + e] = x[e] * f;
+            for (int i = 0; i < 4; ++i) v[4 * j + i] = x[i] * f;
         }
-        TO* dst = out + row * HD + piece * 16;
+        TO* dst = out + (int64_t)p * 16;
         if constexpr (sizeof(TO) == 2) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -399,12 +415,11 @@ int q3paged8_read(const q3paged8_cache* cache, int n, const int32_t* pages, int 
     if (!aligned16(k_out) || !aligned16(v_out)) return paged_fail(Q3_ERR_ARG, "k_out and v_out must start on 16-byte boundaries");
     if (n == 0 || (!k_out && !v_out)) return Q3_OK;
     if (!pages) return paged_fail(Q3_ERR_ARG, "pages is NULL");
-    const int64_t threads = ((int64_t)n * v.nkv << v.page_shift) * 16;
-    const unsigned grid = (unsigned)std::min<int64_t>((threads + 255) / 256, (int64_t)device_sm_count() * 8);
+    const dim3 grid((unsigned)n, 2 * (((v.nkv << (v.page_shift + 3)) + R8_PIECES - 1) / R8_PIECES));
     const uint8_t *ks = cache->k_scale, *vs = cache->v_scale;
     const cudaError_t e = out_dtype == Q3_BF16
-        ? launch_pdl(paged8_read_kernel<bf16>, grid, 256, 0, (cudaStream_t)stream, v, shift, ks, vs, n, pages, (bf16*)k_out, (bf16*)v_out, err)
-        : launch_pdl(paged8_read_kernel<float>, grid, 256, 0, (cudaStream_t)stream, v, shift, ks, vs, n, pages, (float*)k_out, (float*)v_out, err);
+        ? launch_pdl(paged8_read_kernel<bf16>, grid, 256, 0, (cudaStream_t)stream, v, shift, ks, vs, pages, (bf16*)k_out, (bf16*)v_out, err)
+        : launch_pdl(paged8_read_kernel<float>, grid, 256, 0, (cudaStream_t)stream, v, shift, ks, vs, pages, (float*)k_out, (float*)v_out, err);
     if (e != cudaSuccess) return paged_fail(Q3_ERR_CUDA, "read: %s", cudaGetErrorString(e));
     return Q3_OK;
 }
