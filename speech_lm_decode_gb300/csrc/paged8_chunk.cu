@@ -41,6 +41,7 @@ constexpr int C8_THREADS = 384 + 32 * CONV;
 // have divided them; more than there are would be waited for for ever
 constexpr int REGS = 128, REGS_0 = 48, REGS_SOFT = 176, REGS_CONV = 112;
 static_assert(128 * REGS_0 + 256 * REGS_SOFT + 32 * CONV * REGS_CONV <= REGS * C8_THREADS, "registers of the CTA");
+static_assert(REGS_0 <= REGS && REGS_CONV <= REGS && REGS_SOFT >= REGS, "the former give registers up, the latter take them");
 constexpr int ST = 3;                      // f16 tiles (32 KB)
 constexpr int RS = 3;                      // tiles of codes (16 KB)
 constexpr int RAW = CT * HD;

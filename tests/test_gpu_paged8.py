@@ -506,6 +506,56 @@ def test_pages_past_32_bits():
         del t, big, cache, k
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("lens", [[(1, 3000), (1, 700)], [(4, 3000), (3, 700)], [(150, 700), (200, 1500)]])
+def test_bits_that_attention_keeps(lens, act):
+    """Errors relative to the result's norm.  fp32: parts of 22 bits and sums of fp32, 5e-7 and less here; a part that is
+    lost leaves 11 bits, 1e-4.  bf16: the output's rounding is 1.7e-3 of the norm (uniform within half a step of 2^-8,
+    values uniform between two powers of two), weights of 11 bits add 1e-4 to it at most; of 8 bits they would make it 2.3e-3."""
+    s = make(lens, 8, 4, 32, 16, ACTS[act], seed=71)
+    got = cache_of(s).attend(s["q"], s["off"], s["ctx"], max(n for n, _ in lens))
+    want, _ = attend64(s)
+    off = float((got.double() - want).norm() / want.norm())
+    assert off < (2e-6 if act == "f32" else 1.8e-3), off
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("lens", [[(150, 3000), (40, 333)], [(40, 900), (17, 64), (1, 500)]])
+def test_a_wait_that_runs_out(lens, act):
+    """Every CTA's wait for room for its n-th tile of codes counts as run out, at the start of an item or inside: the call
+    returns, says so, and leaves counters with which the next call on the workspace gives the bits that it should."""
+    import speech_lm_decode_gb300 as q3
+    s = make(lens, 8, 4, 16, 16, ACTS[act], seed=44)
+    most = max(q for q, _ in lens)
+    cache = cache_of(s)
+    want = cache.attend(s["q"], s["off"], s["ctx"], most)
+    cache.check()
+    (ws,) = cache._ws.values()
+    for n in list(range(1, 14)) + [20, 33]:
+        broken = cache_of(s, inject_timeout=n)
+        broken.attend(s["q"], s["off"], s["ctx"], most)
+        torch.cuda.synchronize()
+        e = int(broken.err.item())
+        assert e in (0, q3.Q3PAGED_ERR_TIMEOUT) and (e or n > 2)     # (a CTA may have fewer tiles than that)
+        assert list(broken._ws.values())[0] is ws
+        assert not ws[:q3.Q3PAGED_COUNTER_BYTES].any()
+        assert torch.equal(cache.attend(s["q"], s["off"], s["ctx"], most), want)
+        cache.check()
+
+
+def test_scales_past_what_many_rows_keep():
+    """Blocks whose scales are 2^30 apart: finite results, and those of the blocks that count."""
+    for act in ACTS.values():
+        s = make([(70, 200), (9, 90)], 4, 2, 16, 16, act, seed=72)
+        s["ks"][int(s["table"][0, 3])] -= 30
+        s["vs"][int(s["table"][0, 5])] -= 30
+        got = cache_of(s).attend(s["q"], s["off"], s["ctx"], 70)
+        want, bound = attend64(s)
+        # what such a block loses is below 2^-24 of its neighbours' values
+        k, v = gather(s, 0, 200)
+        close(got, want, bound + float(v.abs().max()) * 2.0 ** -20)
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("act", ACTS)
 def test_prompt_then_tokens(act):

@@ -202,6 +202,57 @@ def test_in_front_of_the_draw_in_a_graph(dtype):
             assert m < 0 or int(kw["mask"][m, ids[r] // 32]) >> int(ids[r] % 32) & 1
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [40, 700])
+def test_many_rows(rows, dtype):
+    """Batches whose parts do not all run at once: copying and the named ids in kernels of their own; histories that
+    their table does not take, empty ones, and rows without a mask beside those with one."""
+    import speech_lm_decode_gb300 as q3
+    x, kw = case(rows, 60000 if rows == 40 else 9001, TYPES[dtype], rows, history=300, biases=20, masks=5, rows=True)
+    got = q3.process_logits(x, **kw)
+    check(x, kw, got)
+    y = x.clone()
+    assert torch.equal(q3.process_logits(y, **kw, out=y), got)
+    part = {k: v for k, v in kw.items() if not k.startswith("mask")}
+    check(x, part, q3.process_logits(x, **part))
+    y = x.clone()
+    check(x, part, q3.process_logits(y, **part, out=y))
+    part = {k: v for k, v in kw.items() if k.startswith("bias") or k.startswith("mask")}
+    check(x, part, q3.process_logits(x, **part))
+
+
+def test_more_biases_than_the_table_takes():
+    import speech_lm_decode_gb300 as q3
+    x, kw = case(40, 60000, torch.float32, 12, history=300, biases=9000)
+    kw["bias_off"] = torch.tensor([0, 9000] + [9000] * 38 + [int(kw["bias_off"][-1])], dtype=torch.int32, device="cuda")
+    kw["bias_ids"], kw["bias"] = kw["bias_ids"][:int(kw["bias_off"][-1])], kw["bias"][:int(kw["bias_off"][-1])]
+    kw["bias_off"][-1] = 9300
+    check(x, kw, q3.process_logits(x, **kw))
+
+
+def test_two_streams_at_once_and_what_follows():
+    """Calls on two streams with the draw behind each: it sees the whole of its logits."""
+    import speech_lm_decode_gb300 as q3
+    sets = [case(60, 50000, torch.bfloat16, seed, history=200, biases=9, masks=60) for seed in (13, 14)]
+    n = 60
+    f = (torch.zeros(n, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda"), torch.ones(n, device="cuda"), torch.zeros(n, device="cuda"))
+    u = torch.rand(n, device="cuda")
+    want = [q3.process_logits(x, **kw) for x, kw in sets]
+    ids = [q3.sample_given(w, u, *f)[0] for w in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(15):
+        for i, (x, kw) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                y = q3.process_logits(x, **kw)
+                got[i].append((q3.sample_given(y, u, *f)[0], y.float().nan_to_num(0, 0, -1e4).sum(1), y))
+    torch.cuda.synchronize()
+    for i in range(2):
+        s = want[i].float().nan_to_num(0, 0, -1e4).sum(1)
+        assert all(torch.equal(a, ids[i]) and torch.equal(b, s) and torch.equal(c, want[i]) for a, b, c in got[i])
+
+
 def test_refusals():
     import speech_lm_decode_gb300 as q3
     x, kw = case(4, 500, torch.float32, 10, history=50, biases=10, masks=4)
