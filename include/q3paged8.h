@@ -72,14 +72,14 @@ int q3paged8_append(const q3paged8_cache* c, int n_tokens, int max_q, const void
 size_t q3paged8_workspace_bytes(const q3paged8_cache* c);
 
 /* Causal attention of new tokens over the cache, which holds them already: the
- * arguments and rules of q3paged_attention.  Sums are fp32.  Few rows (new tokens
- * times the q heads of a kv head up to 16): q enters the products with 22 bits
- * and more relative to the row's largest value (bf16: exact), the weights with 11
- * bits (bf16 activations) or 22 (fp32), whatever the scales.  More rows: the
- * same, and codes are taken relative to the largest scale among 128 keys: those
- * of a block whose scale is less than 2^-15 of it lose bits from the smallest
- * on.  Values of keys below ctx_len must not be NaN codes or scales; what pages
- * hold beyond it does not matter. */
+ * arguments and rules of q3paged_attention.  Sums are fp32.  q enters the
+ * products with 22 bits relative to the row's largest value (bf16: exact), the
+ * weights with 11 bits (bf16 activations) or 22 (fp32).  Few rows (new tokens times
+ * the q heads of a kv head up to 16): the scales may be any.  More rows: codes are
+ * taken relative to the largest scale among the keys that a row sees, those of a
+ * block whose scale is less than 2^-15 of it lose bits from the smallest on.
+ * Values of keys below ctx_len must not be NaN codes or scales; what pages hold
+ * beyond it does not matter. */
 int q3paged8_attention(const q3paged8_cache* c, int n_tokens, int max_q, const void* q, int64_t q_stride,
                        const int32_t* q_off, const int32_t* ctx_len, float scale, void* out, int64_t out_stride,
                        void* workspace, size_t workspace_bytes, int32_t* err, void* stream);

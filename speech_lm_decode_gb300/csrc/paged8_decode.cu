@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(DW * 32, d8_ctas(NT)) paged8_decode_kernel(con
                 float4 acc[RG];
 #pragma unroll
                 for (int r = 0; r < RG; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
                 for (int i = warp; i < n; i += DW) {
                     const float* p = part(i) + lane * 4;
 #pragma unroll
@@ -505,8 +505,10 @@ cudaError_t launch_t(const Paged8Attn& a, cudaStream_t st) {
 
 }  // namespace
 
-// rows of a kv head that one sequence may have: two tiles of columns
-bool paged8_decode_takes(const Paged8Attn& a) { return (int64_t)a.max_q * a.c.G <= (a.act == Q3_BF16 ? 16 : 8); }
+// Rows of a kv head that one sequence may have: 16, of two tiles of columns (bf16) or two groups of two (fp32: the keys
+// are read twice, by neighbours of the same L2).  Sequences of eight tokens and two heads over 2000 keys, 64 of them: 70
+// us here and 148 by the chunk kernel (bf16), 120 and 169 (fp32).
+bool paged8_decode_takes(const Paged8Attn& a) { return (int64_t)a.max_q * a.c.G <= 16; }
 
 cudaError_t launch_paged8_decode(const Paged8Attn& a, cudaStream_t st) {
     const int rows = a.max_q * a.c.G;

@@ -370,6 +370,20 @@ def test_nan_stays_where_it_belongs(lens, act):
     assert torch.equal(got.nan_to_num(7e7), want.nan_to_num(7e7))
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("new", [2, 40])
+def test_a_block_whose_scale_is_nan(new, act):
+    """Its keys give NaN to the rows that see one of them, and to no other."""
+    s = make([(new, 333), (new, 90)], 4, 2, 16, 16, ACTS[act], seed=19)
+    base = cache_of(s).attend(s["q"], s["off"], s["ctx"], new)
+    s["ks"][int(s["table"][0, 20]), 1] = 255         # positions 320..332 of sequence 0, head 1
+    got = cache_of(s).attend(s["q"], s["off"], s["ctx"], new)
+    last = 333 - new + torch.arange(new, device="cuda")
+    want = base.clone()
+    want[:new, 2:][last >= 320] = float("nan")
+    assert torch.equal(got.nan_to_num(7e7), want.nan_to_num(7e7))
+
+
 GONE = {"few": [(2, 700), (1, 90)], "chunk": [(90, 700), (40, 130)], "one-tile": [(40, 3000)]}
 
 

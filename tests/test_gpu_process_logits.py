@@ -248,6 +248,16 @@ def test_two_streams_at_once_and_what_follows():
                 y = q3.process_logits(x, **kw)
                 got[i].append((q3.sample_given(y, u, *f)[0], y.float().nan_to_num(0, 0, -1e4).sum(1), y))
     torch.cuda.synchronize()
+    # the same in a graph
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = q3.process_logits(sets[0][0], **sets[0][1])
+        drawn = q3.sample_given(y, u, *f)[0]
+    for _ in range(3):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(drawn, ids[0])
     for i in range(2):
         s = want[i].float().nan_to_num(0, 0, -1e4).sum(1)
         assert all(torch.equal(a, ids[i]) and torch.equal(b, s) and torch.equal(c, want[i]) for a, b, c in got[i])
