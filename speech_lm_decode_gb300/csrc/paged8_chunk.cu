@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(C8_THREADS, 1)
 paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                    const __grid_constant__ Paged8Attn a) {
     constexpr bool F32 = sizeof(TA) == 4;
-    constexpr int QP = F32 ? 2 : 1, PP = F32 ? 2 : 1;
+    constexpr int QP = F32 ? 2 : 1, PP = F32 ? 2 : 1, NX = F32 ? 1 : 2;   // NX: 32 scores of a thread at a time
     // tensor memory: the slots' scores (the weights over them), then outputs: of the two tiles, or (fp32) of the
     // weights' two parts
     constexpr int SLOT = CT, OUT = 2 * SLOT;
@@ -524,30 +524,35 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                 }
                 // The scores are read twice, for their maximum and for the weights, whose place is over the scores that
                 // they come from: short loops and few registers, as instruction fetches of the softmax and of the
-                // conversion go to one cache.
-                uint32_t x[2][32];
-                auto scores = [&](int col) {         // of columns col .. col + 63
-                    tmem_ld32(tS + col, x[0]);
-                    tmem_ld32(tS + col + 32, x[1]);
-                    tmem_wait_ld(x[0]);
-                    tmem_wait_ld(x[1]);
+                // conversion go to one cache (once, from registers: 499 us instead of 422 at 4096 tokens over 12288).  64
+                // columns at a time, or 32 of fp32's longer code (prompts: 89 and 82 us; bf16 as above: 422 and 441).
+                uint32_t x[NX][32];
+                auto scores = [&](int col) {         // of the columns from col on
+#pragma unroll
+                    for (int e = 0; e < NX; ++e) tmem_ld32(tS + col + 32 * e, x[e]);
+#pragma unroll
+                    for (int e = 0; e < NX; ++e) tmem_wait_ld(x[e]);
                     if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < 32 * NX; ++i)
                             if (i >= seen - col) x[i >> 5][i & 31] = 0xff800000u;
                     }
                 };
                 float top = -INFINITY;
 #pragma unroll 1
-                for (int col = 0; col < CT; col += 64) {
+                for (int col = 0; col < CT; col += 32 * NX) {
                     scores(col);
-                    float m[2] = {__uint_as_float(x[0][0]), __uint_as_float(x[1][0])};
+                    float m[2 * NX];         // of 16 columns each
 #pragma unroll
-                    for (int i = 1; i < 31; i += 2) {
-                        m[0] = fmaxf(fmaxf(m[0], __uint_as_float(x[0][i])), __uint_as_float(x[0][i + 1]));
-                        m[1] = fmaxf(fmaxf(m[1], __uint_as_float(x[1][i])), __uint_as_float(x[1][i + 1]));
+                    for (int e = 0; e < 2 * NX; ++e) {
+                        const uint32_t* y = &x[e >> 1][e & 1 ? 16 : 0];
+                        m[e] = __uint_as_float(y[0]);
+#pragma unroll
+                        for (int i = 1; i < 15; i += 2) m[e] = fmaxf(fmaxf(m[e], __uint_as_float(y[i])), __uint_as_float(y[i + 1]));
+                        m[e] = fmaxf(m[e], __uint_as_float(y[15]));
                     }
-                    top = fmaxf(fmaxf(top, fmaxf(m[0], __uint_as_float(x[0][31]))), fmaxf(m[1], __uint_as_float(x[1][31])));
+#pragma unroll
+                    for (int e = 0; e < 2 * NX; ++e) top = fmaxf(top, m[e]);
                 }
                 // The maximum that the weights refer to moves only when a score passes it by 2^8.  Two slots with one
                 // tile share it: a step takes it over from the step before, which is the other slot's.
@@ -592,10 +597,10 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                 const f2c sf = pair(sl, sl), rf = pair(ref, ref);
                 f2c sums = pair(0.f, 0.f);
 #pragma unroll 1
-                for (int col = 0; col < CT; col += 64) {
+                for (int col = 0; col < CT; col += 32 * NX) {
                     scores(col);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < NX; ++e) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
