@@ -851,14 +851,14 @@ def sample_given(logits, u, temperature, top_k, top_p, min_p, ids=None, logprob=
     return ids, logprob
 
 
-def _rows2d(t, name, n, width, dtypes, dev):
-    """A 2-D CUDA tensor [n, width] with contiguous rows that do not share memory: its row stride."""
-    if t.dim() != 2 or t.dtype not in dtypes or t.get_device() != dev or t.shape[0] != n or \
-            (width is not None and t.shape[1] != width) or (t.shape[1] > 1 and t.stride(1) != 1) or \
-            (n > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name}: [{n}, {'any' if width is None else width}] with contiguous rows, "
-                         f"{' or '.join(str(d) for d in dtypes)}, on cuda:{dev} is expected")
-    return t.stride(0) if n > 1 else t.shape[1]
+def _rows2d(t, name, n, width, dtype, dev):
+    """A 2-D CUDA tensor [n, width] (None: any width) with contiguous rows that do not share memory: its row stride."""
+    shape = t.shape
+    if len(shape) == 2 and t.dtype is dtype and t.get_device() == dev and shape[0] == n and width in (None, shape[1]):
+        step, one = t.stride()
+        if (one == 1 or shape[1] <= 1) and (n <= 1 or step >= shape[1]):
+            return step if n > 1 else shape[1]
+    raise ValueError(f"{name}: [{n}, {'any' if width is None else width}] with contiguous rows, {dtype}, on cuda:{dev} is expected")
 
 
 def process_logits(logits, history=None, n_history=None, n_prompt=None, repetition=None, presence=None, frequency=None,
@@ -875,16 +875,16 @@ def process_logits(logits, history=None, n_history=None, n_prompt=None, repetiti
         raise ValueError("logits: a CUDA tensor [n, vocab] with contiguous rows is expected")
     (n, vocab), dev, f, i32 = logits.shape, logits.get_device(), torch.float32, torch.int32
     code = _dtype_code(logits)
-    ld = _rows2d(logits, "logits", n, vocab, (logits.dtype,), dev)
+    ld = _rows2d(logits, "logits", n, vocab, logits.dtype, dev)
     if out is None:
         out = torch.empty((n, vocab), dtype=logits.dtype, device=logits.device)
-    ldo = _rows2d(out, "out", n, vocab, (logits.dtype,), dev)
+    ldo = _rows2d(out, "out", n, vocab, logits.dtype, dev)
 
     def row(t, name, dtype, size=n):
         return None if t is None else _need(t, name, dtype, (size,), dev)
     cap, ldh, n_bias, n_masks, ldm = 0, 0, 0, 0, 0
     if history is not None:
-        ldh, cap = _rows2d(history, "history", n, None, (i32,), dev), history.shape[1]
+        ldh, cap = _rows2d(history, "history", n, None, i32, dev), history.shape[1]
         if cap == 0:
             history = n_history = n_prompt = None
     if bias_ids is not None:
@@ -893,7 +893,7 @@ def process_logits(logits, history=None, n_history=None, n_prompt=None, repetiti
             bias_off = bias_ids = bias = None
     if mask is not None:
         n_masks = mask.shape[0]
-        ldm = _rows2d(mask, "mask", n_masks, (vocab + 31) // 32, (i32,), dev)
+        ldm = _rows2d(mask, "mask", n_masks, (vocab + 31) // 32, i32, dev)
     args = (row(n_history, "n_history", i32), row(n_prompt, "n_prompt", i32), row(repetition, "repetition", f),
             row(presence, "presence", f), row(frequency, "frequency", f), n_bias, row(bias_off, "bias_off", i32, n + 1),
             row(bias_ids, "bias_ids", i32, n_bias), row(bias, "bias", f, n_bias), n_masks,
