@@ -15,12 +15,19 @@
 // Codes are taken into f16 times their block's scale over the cut's largest one,
 // which is exact to a ratio of 2^15 (f16 has steps of 2^-24, codes of 2^-9); the
 // largest scale itself multiplies the scores' factor and the outputs, in fp32.
-// With the whole conversion beside the softmax nothing of it lies on the chain
-// score -> softmax -> output, and a tile is converted once for 256 query rows.
+// The conversion runs beside the softmax, and a tile is converted once for 256
+// query rows.
 // q enters in f16 relative to the power of two above its row's largest value, one
 // part (bf16 activations: exact) or two (fp32: 22 bits); weights relative to 2^-7
 // of the running maximum, one part (11 bits) or two, each with an output of its own
 // as over bf16 pages.
+//
+// Measured (16 q and 8 kv heads): 4096 tokens over 12288, bf16, 422 us = 1.14
+// PFLOP/s (58 % of the measured rate; without the conversion 391, without the
+// exponentials no less: what is left is a slot's chain score -> softmax -> output),
+// fp32 747; 24 prompts of 1..512 over 0..255, fp32, 81 us; 64 tokens over 32k, bf16,
+// 58 us.  Errors against 64 bits: bf16 1.67e-3 of the result (the output's rounding
+// is 1.66e-3 of it), fp32 3.6e-7 to 5.6e-7.
 //
 // Every wait is bounded: one that runs out sets the timeout bit, after which the
 // CTA goes through its remaining steps without waiting or issuing, drains its
@@ -38,7 +45,8 @@ namespace {
 constexpr int CONV = 4;                    // warps that convert
 constexpr int C8_THREADS = 384 + 32 * CONV;
 // registers a thread: at launch (the launcher checks it), and of warps 0-3, the softmax and the conversion after they
-// have divided them; more than there are would be waited for for ever
+// have divided them; more than there are would be waited for for ever (128 each: 849 us at 4096 tokens over 12288, as the
+// softmax has too few; eight converting warps and 136 registers of the softmax: 482)
 constexpr int REGS = 128, REGS_0 = 48, REGS_SOFT = 176, REGS_CONV = 112;
 static_assert(128 * REGS_0 + 256 * REGS_SOFT + 32 * CONV * REGS_CONV <= REGS * C8_THREADS, "registers of the CTA");
 static_assert(REGS_0 <= REGS && REGS_CONV <= REGS && REGS_SOFT >= REGS, "the former give registers up, the latter take them");
