@@ -625,6 +625,75 @@ def test_prompt_then_tokens(act):
             assert (far <= 2.2 * first).all()
 
 
+def test_a_serving_step():
+    """Append, attention, logits, penalties and mask, draw, the history grown on the device: steps of a captured graph
+    against 64 bits and against the same steps eager."""
+    import speech_lm_decode_gb300 as q3
+    from paged8_ref import process64
+    nq, nkv, n, vocab, T = 4, 2, 3, 1000, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(81)
+    emb = torch.randn(vocab, (nq + 2 * nkv) * HD, generator=g, device="cuda").to(T)
+    head = (torch.randn(nq * HD, vocab, generator=g, device="cuda") * 0.3).to(T)
+    words = torch.randint(-2 ** 31, 2 ** 31, (2, 32), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+    rope = rope_table(40)
+    full = dict(temperature=torch.ones(n, device="cuda"), top_k=torch.full((n,), 20, dtype=torch.int32, device="cuda"),
+                top_p=torch.full((n,), 0.9, device="cuda"), min_p=torch.zeros(n, device="cuda"))
+    us = torch.rand(20, n, generator=g, device="cuda")
+
+    def program():
+        s = make([(1, 1)] * n, nq, nkv, 16, 16, T, seed=82, spare=9, at_new=True)
+        s["table"] = torch.arange(9, dtype=torch.int32).view(3, 3).cuda()
+        st = {"s": s, "cache": cache_of(s), "ctx": torch.ones(n, dtype=torch.int32, device="cuda"),
+              "hist": torch.full((n, 40), -1, dtype=torch.int32, device="cuda"), "said": torch.zeros(n, dtype=torch.int32, device="cuda"),
+              "ids": torch.arange(n, dtype=torch.int32, device="cuda"), "u": torch.zeros(n, device="cuda"),
+              "off": torch.arange(n + 1, dtype=torch.int32, device="cuda")}
+        kw = dict(history=st["hist"], n_history=st["said"], repetition=torch.full((n,), 1.3, device="cuda"),
+                  presence=torch.full((n,), 0.4, device="cuda"), frequency=torch.full((n,), 0.2, device="cuda"),
+                  mask=words, mask_row=torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda"))
+
+        def step():
+            qkv = emb[st["ids"].long()]
+            q = st["cache"].append(qkv, st["off"], st["ctx"], 1, rope)
+            o = st["cache"].attend(q, st["off"], st["ctx"], 1)
+            raw = (o.view(n, -1) @ head).float()
+            logits = q3.process_logits(raw, **kw)
+            ids, logprob = q3.sample_given(logits, st["u"], **full)
+            out = [t.clone() for t in (q, o, raw, logits, ids, logprob)]
+            st["hist"].scatter_(1, st["said"].long()[:, None], ids[:, None])
+            st["ids"].copy_(ids)
+            st["said"] += 1
+            st["ctx"] += 1
+            return out
+        return st, kw, step
+    st, kw, step = program()
+    st2, _, step2 = program()
+    keep = {k: v.clone() for k, v in st2.items() if isinstance(v, torch.Tensor)}
+    step2()
+    for k, v in keep.items():
+        st2[k].copy_(v)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = step2()
+    for i in range(20):
+        for t in (st, st2):
+            t["u"].copy_(us[i])
+        said = {k: v.cpu().numpy().copy() for k, v in kw.items()}
+        lens = [(1, i + 1)] * n
+        q, o, raw, logits, ids, logprob = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        st["cache"].check()
+        st2["cache"].check()
+        assert all(torch.equal(a, b) for a, b in zip((q, o, raw, logits, ids, logprob), replayed)), i
+        close(o, *attend64({**st["s"], "q": q, "lens": lens, "off": st["off"]}), str(i))
+        want, bound = process64(raw.cpu().numpy(), **said)
+        err = (logits.double().cpu() - torch.from_numpy(want)).abs()
+        assert (err.nan_to_num(0) <= torch.from_numpy(bound) + torch.from_numpy(want).abs().nan_to_num(0, 0, 0) * 2.0 ** -24).all()
+        for r, m in ((0, 0), (1, 1)):
+            assert int(words[m, int(ids[r]) // 32]) >> (int(ids[r]) % 32) & 1
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_two_streams_at_once(act):
     states = [make([(1, 900), (1, 70)], 16, 8, 16, 16, ACTS[act], seed=61), make([(60, 900), (9, 70)], 8, 2, 16, 16, ACTS[act], seed=62)]
