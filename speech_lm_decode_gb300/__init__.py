@@ -768,7 +768,7 @@ class PagedKV8(PagedKV):
                 raise ValueError(f"{name}: a contiguous float8_e8m0fnu tensor [n_pages, n_kv_heads, page_size // block] "
                                  f"on {self.device} is expected")
         self.k_scale, self.v_scale = k_scale, v_scale
-        c.scale_block = page // k_scale.shape[2]
+        c.scale_block, self._page_shape = page // k_scale.shape[2], (heads, page, 128)
         c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
         self._ready(c, lambda c, act: setattr(c.cache, "act_dtype", act), lib().q3paged8_workspace_bytes)
 
@@ -809,19 +809,21 @@ class PagedKV8(PagedKV):
         import torch
         n, dev = pages.shape[0], self._dev
         if dtype is None:
-            dtype = next((t.dtype for t in (k_out, v_out) if t is not None), torch.bfloat16)
-        shape = (n,) + tuple(self.k_pages.shape[1:])
-        outs = []
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=self.device)
-            _need(t, name, dtype, shape, dev)
-            outs.append(t)
-        code = _dtype_code(outs[0])
+            dtype = torch.bfloat16 if k_out is v_out is None else (v_out if k_out is None else k_out).dtype
+        shape = (n,) + self._page_shape
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            _need(k_out, "k_out", dtype, shape, dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=self.device)
+        else:
+            _need(v_out, "v_out", dtype, shape, dev)
+        code = _dtype_code(k_out)
         _on_stream(dev, lambda stream: self._lib.q3paged8_read(
-            self._c[torch.float32][1], n, _need(pages, "pages", torch.int32, (n,), dev), code, outs[0].data_ptr(),
-            outs[1].data_ptr(), self._err, stream))
-        return tuple(outs)
+            self._c[torch.float32][1], n, _need(pages, "pages", torch.int32, (n,), dev), code, k_out.data_ptr(),
+            v_out.data_ptr(), self._err, stream))
+        return k_out, v_out
 
 
 def sample_given(logits, u, temperature, top_k, top_p, min_p, ids=None, logprob=None, err=None):
