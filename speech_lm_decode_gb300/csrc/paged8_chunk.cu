@@ -54,6 +54,9 @@ constexpr int ST = 3;                      // f16 tiles (32 KB)
 constexpr int RS = 3;                      // tiles of codes (16 KB)
 constexpr int RAW = CT * HD;
 constexpr int C8_QBYTES = 2 * STAGE;       // Q: of two tiles of rows, or the two parts of one
+// fp32 activations: key tiles after which the output leaves the tensor memory for a total in fp32.  Products add to it
+// cut off, not rounded, so that it falls behind by as much again with every tile: 1.1e-5 of the result after 120 tiles.
+constexpr int FLUSH = 16;
 constexpr float P_SHIFT = 7.f;             // weights are 2^7 times exp2 of score - reference (f16 holds 2^-21 of it in full)
 
 struct Chunk8Smem {
@@ -289,7 +292,7 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                         if (more) { scores(1, k); release(k); }
                     } else {
                         const int t = i & 1;
-                        outputs(t, v, i > 0);
+                        outputs(t, v, F32 ? i % FLUSH != 0 : i > 0);
                         if (ok && elect_one()) commit(&sm.pv_full);
                         __syncwarp();
                         release(v);
@@ -442,6 +445,11 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
             const bool live = r < tpt * c.G && tok < g.tok0 + g.ntok;
             auto lim = [&] { return live ? min(wq.ctx - wq.n_new + tok + 1, wq.ctx) : 0; };   // keys that the row sees
             float mx = -INFINITY, l = 0.f;
+            // the place of the cut's part, whose upper 128 rows have the output that left the tensor memory (one tile of
+            // rows alone), at the maximum mt
+            float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == g.ca ? 1 : 0)) * C_SLOT;
+            auto total = [&](int group) { return (float4*)(slot + ((size_t)group * 2 * CT + CT + r) * 4); };
+            float mt = -INFINITY;
             if (g.n > 0) {
                 // ---- query rows: 16 threads a row, 8 values each, loads of a batch in flight together
                 constexpr int NB = 8, V4 = F32 ? 2 : 1;
@@ -572,13 +580,34 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                     if (now != mx) l *= ex2f((mx - now) * sl);    // (never back to -inf)
                     mx = now;
                 }
-                const bool grew = top > mx + slack;
-                if (__any_sync(0xffffffffu, grew)) {
+                const bool grew = top > mx + slack, flush = F32 && step > 0 && step % FLUSH == 0;
+                if (flush || __any_sync(0xffffffffu, grew)) {
                     const float nm = fmaxf(mx, top);
                     const float f = nm == -INFINITY ? 1.f : ex2f((mx - nm) * sl);
                     mx = nm;
                     l *= f;
-                    if (step > 0) {
+                    if (flush) {       // (the first slot's, as FLUSH is even; the next product does not add)
+                        ok = ok && bar_wait(&sm.pv_full, (pvc + step - 1) & 1, sm, a.err);
+                        ok = __all_sync(0xffffffffu, ok);
+                        fence_after();
+                        const float h = step == FLUSH ? 0.f : mx == -INFINITY ? 1.f : ex2f((mt - mx) * sl);
+                        mt = mx;
+#pragma unroll 1
+                        for (int cc = 0; cc < 8; ++cc) {
+                            uint32_t y[16], z[16];
+                            tmem_ld16(tO + 16 * cc, y);
+                            tmem_ld16(tO + CT + 16 * cc, z);
+                            float4 was[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) was[i] = step == FLUSH ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(total(4 * cc + i));
+                            auto sum = [&](int i, float w) { return fmaf(__uint_as_float(y[i]) + __uint_as_float(z[i]), f, w * h); };
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                __stcg(total(4 * cc + i), make_float4(sum(4 * i, was[i].x), sum(4 * i + 1, was[i].y),
+                                                                      sum(4 * i + 2, was[i].z), sum(4 * i + 3, was[i].w)));
+                        }
+                        fence_before();
+                    } else if (step > 0) {
                         if (!g.two) {      // the products of the step before are in
                             ok = ok && bar_wait(&sm.pv_full, (pvc + step - 1) & 1, sm, a.err);
                             ok = __all_sync(0xffffffffu, ok);
@@ -647,7 +676,9 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
                 // both slots' sums, at the last maximum
                 sm.stats[t][r] = mx;
                 sm.stats[2 + t][r] = l;
+                if (t == 0) sm.row[CT + r] = mt;      // (free with one tile of rows)
                 wg_sync(2);
+                mt = sm.row[CT + r];
                 l = 0.f;
                 if (g.n > 0) {
                     mx = sm.ref[r];
@@ -663,8 +694,10 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
             const RowOut<TA> row_out = {qs + (size_t)(F32 ? 0 : tile) * STAGE, r, dst, live};
             // partials: [32 groups of 4 values][256 rows], then maxima and sums
             const int prow = tile * CT + r;
-            float* slot = parts + (size_t)(blockIdx.x * 2 + (blockIdx.x == g.ca ? 1 : 0)) * C_SLOT;
             {
+                // what left the tensor memory before, at the last maximum
+                const bool more = F32 && g.n > FLUSH;
+                const float h = more && mt != -INFINITY ? ex2f((mt - mx) * sl) : 0.f;
                 const float w0 = g.whole ? inv * vf : vf;
 #pragma unroll 1
                 for (int c2 = blk0; c2 < blk1; c2 += 2) {
@@ -683,6 +716,16 @@ paged8_chunk_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_const
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
                                     x[e][i] = __float_as_uint(__uint_as_float(x[e][i]) + __uint_as_float(y[i]));
+                                if (more) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const float4 z = __ldcg(total(8 * (c2 + e) + i));
+                                        x[e][4 * i] = __float_as_uint(fmaf(z.x, h, __uint_as_float(x[e][4 * i])));
+                                        x[e][4 * i + 1] = __float_as_uint(fmaf(z.y, h, __uint_as_float(x[e][4 * i + 1])));
+                                        x[e][4 * i + 2] = __float_as_uint(fmaf(z.z, h, __uint_as_float(x[e][4 * i + 2])));
+                                        x[e][4 * i + 3] = __float_as_uint(fmaf(z.w, h, __uint_as_float(x[e][4 * i + 3])));
+                                    }
+                                }
                             }
                         }
                     }
