@@ -25,9 +25,10 @@
 // Measured (16 q and 8 kv heads): 4096 tokens over 12288, bf16, 422 us = 1.14
 // PFLOP/s (58 % of the measured rate; without the conversion 391, without the
 // exponentials no less: what is left is a slot's chain score -> softmax -> output),
-// fp32 747; 24 prompts of 1..512 over 0..255, fp32, 81 us; 64 tokens over 32k, bf16,
+// fp32 830; 24 prompts of 1..512 over 0..255, fp32, 83 us; 64 tokens over 32k, bf16,
 // 58 us.  Errors against 64 bits: bf16 1.67e-3 of the result (the output's rounding
-// is 1.66e-3 of it), fp32 3.6e-7 to 5.6e-7.
+// is 1.66e-3 of it), fp32 4.5e-7 at those prompts, 1.3e-6 to 1.6e-6 over 1000 to
+// 32000 keys (the plain form in fp32: 6.1e-7, 1.0e-6 to 3.5e-6).
 //
 // Every wait is bounded: one that runs out sets the timeout bit, after which the
 // CTA goes through its remaining steps without waiting or issuing, drains its
@@ -55,8 +56,10 @@ constexpr int RS = 3;                      // tiles of codes (16 KB)
 constexpr int RAW = CT * HD;
 constexpr int C8_QBYTES = 2 * STAGE;       // Q: of two tiles of rows, or the two parts of one
 // fp32 activations: key tiles after which the output leaves the tensor memory for a total in fp32.  Products add to it
-// cut off, not rounded, so that it falls behind by as much again with every tile: 1.1e-5 of the result after 120 tiles.
-constexpr int FLUSH = 16;
+// cut off, not rounded, so that it falls behind by as much again with every tile: 1.1e-5 of the result after 120 tiles,
+// 2.7e-6 so after every sixteen, 1.6e-6 after every eight (the plain form in fp32: 2.6e-6); 4096 tokens over 12288 take
+// 750, 785 and 830 us.
+constexpr int FLUSH = 8;
 constexpr float P_SHIFT = 7.f;             // weights are 2^7 times exp2 of score - reference (f16 holds 2^-21 of it in full)
 
 struct Chunk8Smem {

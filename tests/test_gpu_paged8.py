@@ -535,8 +535,8 @@ def test_bits_that_attention_keeps(lens, act):
 
 def test_many_rows_of_fp32_over_a_long_context():
     """The tensor cores cut what they add, so that an output kept there falls behind by as much with every tile: 1.1e-5
-    of the result after 120 tiles.  Sixteen tiles are 128 sums of half a step of 2^-23 each at most, 7.6e-6, and a fourth of
-    that where the sum grows from nothing and a cut loses half a step on average."""
+    of the result after 120 tiles.  The eight tiles that it is kept for are 64 sums that lose a step of 2^-24 of it each
+    at most, 3.8e-6."""
     s = make([(700, 15000)], 16, 8, 64, 64, torch.float32, seed=73)
     got = cache_of(s).attend(s["q"], s["off"], s["ctx"], 700)
     want, _ = attend64(s)
